@@ -239,6 +239,59 @@ lr_status lr_attn_bwd(lr_dtype dt, int b, int s, int H, int dh, float scale, con
                       const void* v, const void* o, const void* saved, const void* dout, void* dq, void* dk,
                       void* dv, void* ws, size_t ws_bytes, void* stream);
 
+/* --------------------------------- query / key norm and position rotation
+ * What LLaMA-style attention does to q and k between their projections and the scores
+ * (the technical summary trains LLaMA-style models and leaves it unchanged), in one pass:
+ * per token t and head, x its dh channels, g the tensor's gain [dh] (shared by its heads):
+ *     n = x r g, r = (mean(x^2) + eps)^(-1/2) if g != NULL, else n = x
+ *     pair p of the first rot channels turns by  theta = pos[a(p)][t] * freq[p]:
+ *     y_i = n_i cos(theta) - n_j sin(theta),  y_j = n_i sin(theta) + n_j cos(theta)
+ * and the channels from rot on pass unturned.  layout: LR_PAIR_HALF pairs channels
+ * (p, p + rot/2), LR_PAIR_ADJACENT (2p, 2p + 1).  Positions may have several axes (time,
+ * height, width of a patch): axis 0 turns the first sec[0] pairs, axis 1 the next sec[1],
+ * and so on; sum of sec[0 .. axes-1] = rot/2.  pos: device int32 [axes, T], any value; NULL:
+ * position t mod seq on every axis (T tokens = sequences of seq tokens).
+ * turns: device uint64 [rot/2], the frequencies as lr_rot_turns makes them (units of
+ * 2^-64 turn per position): pos * turns wraps at whole turns, so the angle of a far
+ * position is as exact as that of a near one.
+ * q [T, Hq*dh], k [T, Hk*dh] (Hq != Hk allowed; a tensor with 0 heads is absent, its
+ * pointers unused), rows ldq, ldk, ... elements apart: a multiple of 8, at least the row's
+ * own width, so q and k may be columns of one packed matrix.  An output may be its input
+ * (the same pointer and row distance: qo = q, dq = dqo, ...); outputs must not overlap
+ * anything else.  Elements between rows' ends are not touched.
+ * dh and rot multiples of 8, 8 <= dh <= 256 (or dh <= 512 with dh and rot multiples of 16),
+ * 0 <= rot <= dh, axes 1..4.  Sums over channels and the dg sums are fp32; y, dx are rounded
+ * once.  |x| must stay below 1e18 (the square sums are fp32).
+ */
+typedef enum { LR_PAIR_HALF = 0, LR_PAIR_ADJACENT = 1 } lr_pair_layout;
+
+typedef struct {
+  int Hq, Hk;   /* heads of q and of k */
+  int dh, rot;  /* channels per head, of which the first rot are turned */
+  int layout;   /* lr_pair_layout */
+  int axes;     /* position axes, 1..4 */
+  int sec[4];   /* pairs turned by each axis */
+  int seq;      /* pos == NULL: tokens per sequence (else ignored) */
+} lr_qk_shape;
+
+/* Host arithmetic, no device needed: turns[i] = freq[i] / (2 pi) mod 1 in units of 2^-64
+ * (freq in radians per position, finite, at most 65536 in magnitude); both arrays host. */
+lr_status lr_rot_turns(int n, const double* freq, unsigned long long* turns);
+
+lr_status lr_qk_fwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const unsigned long long* turns,
+                    const int* pos, const void* gq, const void* gk, const void* q, long long ldq, const void* k,
+                    long long ldk, void* qo, long long ldqo, void* ko, long long ldko, void* stream);
+
+/* dqo, dko (gradients of qo, ko) -> dq, dk (dtype) and the gains' dgq, dgk [dh] fp32 (each
+ * ignored and may be NULL without its gain).  q, k: the forward's inputs (each ignored and
+ * may be NULL without its gain).  Nothing is saved by the forward. */
+size_t lr_qk_bwd_workspace_bytes(lr_dtype dt, int T, const lr_qk_shape* sh);
+lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const unsigned long long* turns,
+                    const int* pos, const void* gq, const void* gk, const void* q, long long ldq, const void* k,
+                    long long ldk, const void* dqo, long long lddqo, const void* dko, long long lddko, void* dq,
+                    long long lddq, void* dk, long long lddk, float* dgq, float* dgk, void* ws, size_t ws_bytes,
+                    void* stream);
+
 /* ------------------------------------------------- low-rank transformer block
  * One pre-norm LLaMA-style block whose linear maps are all low-rank pairs (d = H*dh,
  * T = b*s tokens, attention rank ra, MLP rank rm, MLP width f):
@@ -294,6 +347,28 @@ lr_status lr_stack_step(lr_dtype dt, lr_mode mode, int nblocks, int T, int d, in
                         const void* x, const void* target, const void* const* gs, const lr_pair* pairs,
                         float* loss, void* dx, float* const* dgs, const lr_pair_grad* grads, void* ws,
                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------ gradient norm and clipping
+ * The list of gradients that the backward entry points return, taken as one vector:
+ *     norm = sqrt(sum_i sum_j grads[i][j]^2),  scale = min(1, max_norm / (norm + 1e-6)),
+ *     outs[i] = scale * grads[i].
+ * grads, outs, numel: host arrays of n device pointers / element counts (read before the
+ * call returns; the kernels take them by value, so a call can be captured).  dt is the type
+ * of every tensor (LR_F32 for what the *_bwd entry points write).  outs[i] may be grads[i]
+ * (clipping in place) and must not overlap any other tensor of either list; a tensor may
+ * have 0 elements (its pointers are then unused).  A list that names a tensor twice counts
+ * it twice.  0 <= n <= 65536, each count below 2^40.
+ * stat: device fp32; lr_grad_norm writes stat[0] = norm, lr_grad_clip stat[0] = norm and
+ * stat[1] = scale.  The squares are summed to about fp32 accuracy at any size and any
+ * magnitude: neither squares beyond the fp32 range nor below it are lost.  A norm that is
+ * infinite or NaN is reported as such and scales as the formula says (scale 0 or NaN).
+ * max_norm: finite, >= 0.
+ */
+size_t lr_grad_workspace_bytes(int n);
+lr_status lr_grad_norm(lr_dtype dt, int n, const void* const* grads, const long long* numel, float* stat, void* ws,
+                       size_t ws_bytes, void* stream);
+lr_status lr_grad_clip(lr_dtype dt, int n, const void* const* grads, const long long* numel, float max_norm,
+                       void* const* outs, float* stat, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------- allocation-free variant
  * The pages have no counterpart to this entry point; it exists for callers

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -16,6 +17,8 @@
 #include "common.cuh"
 #include "gemm.h"
 #include "attn_kernels.cuh"
+#include "grad_kernels.cuh"
+#include "qk_kernels.cuh"
 #include "small_kernels.cuh"
 
 namespace lr {
@@ -1481,6 +1484,120 @@ static lr_status block_bwd_impl(const Ctx& c, int b, int s, int H, int dh, int f
   return proj_bwd_impl(c, T, d, d, ra, 3, qkv, w.g_attn, x, S.qkv, dqkv, dx, gr.dg_attn, gq, W.sub, W.dx1);
 }
 
+// ============================================================ query / key norm and rotation
+struct QkWs {
+  float* part[2];  // partial sums of dgq, dgk
+};
+
+static size_t qk_ws_layout(int dh, void* base, QkWs* W) {
+  Arena ar(base);
+  QkWs tmp;
+  if (!W) W = &tmp;
+  for (float*& p : W->part) p = static_cast<float*>(ar.take(sizeof(float) * kQkMaxParts * static_cast<size_t>(dh)));
+  return ar.size();
+}
+
+static QkArgs qk_args(int T, const lr_qk_shape& sh, float eps, const unsigned long long* turns, const int* pos) {
+  QkArgs a;
+  memset(&a, 0, sizeof(a));
+  a.turns = turns;
+  a.pos = pos;
+  a.T = T;
+  a.dh = sh.dh;
+  a.rot = sh.rot;
+  a.seq = sh.seq;
+  a.eps = eps;
+  int end = 0;
+  for (int i = 0; i < kQkMaxAxes - 1; ++i) {
+    if (i < sh.axes) end += sh.sec[i];
+    a.sec_end[i] = i < sh.axes - 1 ? end : sh.rot / 2;
+  }
+  return a;
+}
+
+static lr_status qk_fwd_impl(const Ctx& c, const lr_qk_shape& sh, const QkArgs& a) {
+  LaunchScope scope("qk_fwd", c.st, 0, 2.0 * c.es * a.T * (sh.Hq + sh.Hk) * a.dh);
+  const bool adj = sh.layout == LR_PAIR_ADJACENT;
+  cudaError_t e = c.dt == LR_BF16 ? launch_qk_fwd<bf16>(a, adj, c.st) : launch_qk_fwd<float>(a, adj, c.st);
+  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation: %s", cudaGetErrorString(e));
+  return LR_OK;
+}
+
+static lr_status qk_bwd_impl(const Ctx& c, const lr_qk_shape& sh, QkArgs& a, void* ws) {
+  QkWs W;
+  qk_ws_layout(a.dh, ws, &W);
+  for (int i = 0; i < 2; ++i) a.t[i].part = W.part[i];
+  const double rows = static_cast<double>(a.T) * a.dh;
+  LaunchScope scope("qk_bwd", c.st, 0,
+                    c.es * rows * (sh.Hq * (a.t[0].g ? 3.0 : 2.0) + sh.Hk * (a.t[1].g ? 3.0 : 2.0)));
+  const bool adj = sh.layout == LR_PAIR_ADJACENT;
+  cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.st) : launch_qk_bwd<float>(a, adj, c.st);
+  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
+  return LR_OK;
+}
+
+// ============================================================ gradient norm and clipping
+static size_t grad_ws_bytes(int n) {
+  const size_t launches = n > 0 ? (static_cast<size_t>(n) + kGradTable - 1) / kGradTable : 1;
+  return launches * kGradParts * sizeof(double);
+}
+
+// Tensors i0 .. i0 + k - 1 as one launch's table; false if its chunks exceed an int.
+template <int N>
+static bool grad_table(int i0, int k, const void* const* grads, const long long* numel, void* const* outs,
+                       GradTable<N>* t) {
+  long long first = 0;
+  for (int i = 0; i < k; ++i) {
+    t->src[i] = grads[i0 + i];
+    t->dst[i] = outs ? outs[i0 + i] : nullptr;
+    t->numel[i] = numel[i0 + i];
+    t->first[i] = static_cast<int>(first);
+    first += (numel[i0 + i] + kGradChunk - 1) / kGradChunk;
+    if (first > 0x7fffffffLL) return false;
+  }
+  t->first[k] = static_cast<int>(first);
+  t->n = k;
+  return true;
+}
+
+template <typename ST>
+static lr_status grad_impl(const Ctx& c, int n, const void* const* grads, const long long* numel, float max_norm,
+                           void* const* outs, float* stat, double* part) {
+  GradTable<kGradTable> tab;
+  int nparts = 0;
+  double elems = 0.0;
+  for (int i = 0; i < n; ++i) elems += static_cast<double>(numel[i]);
+  for (int i0 = 0; i0 < n; i0 += kGradTable) {  // every list checked before the first launch
+    if (!grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab))
+      return fail(LR_ERR_SHAPE, "gradient tensors %d..: too many elements", i0);
+  }
+  for (int i0 = 0; i0 < n; i0 += kGradTable) {
+    grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab);
+    const int chunks = tab.first[tab.n];
+    if (chunks == 0) continue;
+    LaunchScope scope("grad_sumsq", c.st, 0, c.es * elems);
+    cudaError_t e = launch_grad_sumsq<ST>(tab, part + nparts, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
+    nparts += grad_blocks(chunks);
+  }
+  bool stat_due = true;
+  for (int i0 = 0; i0 < n || stat_due; i0 += kGradTable) {
+    if (outs && i0 < n) {
+      grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab);
+    } else {
+      tab.n = 0;
+      tab.first[0] = 0;
+    }
+    if (tab.first[tab.n] == 0 && !stat_due) continue;
+    LaunchScope scope("grad_scale", c.st, 0, outs ? 2.0 * c.es * elems : 0.0);
+    cudaError_t e = launch_grad_scale<ST>(tab, part, nparts, max_norm, stat, !stat_due ? 0 : outs ? 2 : 1, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient clipping: %s", cudaGetErrorString(e));
+    stat_due = false;
+    if (!outs) break;
+  }
+  return LR_OK;
+}
+
 // ============================================================ block stack
 struct StackWs {
   void* acts;   // x_1 .. x_L, [L][T, d]
@@ -2090,6 +2207,187 @@ lr_status lr_btp_finish(lr_dtype dt, lr_act act, int T, int d, int r, int group,
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c, act));
   return btp_finish_impl(c, T, d, group * r, payload, eps, u, z, s);
+}
+
+static lr_status check_qk(lr_dtype dt, int T, const lr_qk_shape* sh) {
+  LR_TRY(check_dtype(dt));
+  if (!sh) return fail(LR_ERR_NULL, "shape is NULL");
+  LR_TRY(check_dim(T, "T", false));
+  LR_TRY(check_dim(sh->dh, "dh", true));
+  if (sh->rot < 0 || sh->rot > sh->dh || sh->rot % 8)
+    return fail(LR_ERR_SHAPE, "rot = %d must be a multiple of 8 in 0..dh = %d", sh->rot, sh->dh);
+  if (sh->dh > 256 && (sh->dh > 512 || sh->dh % 16 || sh->rot % 16))
+    return fail(LR_ERR_SHAPE, "dh = %d (rot = %d): at most 256, or at most 512 with both multiples of 16", sh->dh,
+                sh->rot);
+  if (sh->Hq < 0 || sh->Hk < 0 || sh->Hq + 0LL + sh->Hk < 1)
+    return fail(LR_ERR_SHAPE, "Hq = %d, Hk = %d: at least one head needed", sh->Hq, sh->Hk);
+  for (long long H : {sh->Hq, sh->Hk})
+    if (H * sh->dh > (1 << 24))
+      return fail(LR_ERR_SHAPE, "H*dh = %lld channels must not exceed 16777216", H * sh->dh);
+  if (sh->layout != LR_PAIR_HALF && sh->layout != LR_PAIR_ADJACENT)
+    return fail(LR_ERR_DTYPE, "unknown pair layout %d", sh->layout);
+  if (sh->axes < 1 || sh->axes > kQkMaxAxes) return fail(LR_ERR_SHAPE, "axes = %d must be 1..4", sh->axes);
+  long long pairs = 0;
+  for (int i = 0; i < sh->axes; ++i) {
+    if (sh->sec[i] < 0) return fail(LR_ERR_SHAPE, "sec[%d] = %d is negative", i, sh->sec[i]);
+    pairs += sh->sec[i];
+  }
+  if (pairs != sh->rot / 2)
+    return fail(LR_ERR_SHAPE, "the axes' sections hold %lld pairs, rot / 2 = %d", pairs, sh->rot / 2);
+  return LR_OK;
+}
+
+static lr_status check_rows(const void* p, long long ld, int H, int dh, const char* name) {
+  LR_TRY(check_ptr(p, name));
+  if (ld < 1LL * H * dh || ld % 8 || ld > (1LL << 31))
+    return fail(LR_ERR_SHAPE, "%s: row distance %lld must be a multiple of 8, at least H*dh = %lld and at most 2^31",
+                name, ld, 1LL * H * dh);
+  return LR_OK;
+}
+
+static lr_status check_qk_common(const lr_qk_shape* sh, float eps, const unsigned long long* turns, const int* pos,
+                                 const void* gq, const void* gk) {
+  if (!(eps >= 0.f) || eps > 1e30f) return fail(LR_ERR_SHAPE, "eps must be finite and not negative");
+  if (sh->rot > 0) {
+    LR_TRY(check_ptr(turns, "turns"));
+    if (pos) {
+      LR_TRY(check_ptr(pos, "pos"));
+    } else if (sh->seq < 1) {
+      return fail(LR_ERR_SHAPE, "seq = %d must be positive when pos is NULL", sh->seq);
+    }
+  }
+  if (sh->Hq && gq) LR_TRY(check_ptr(gq, "gq"));
+  if (sh->Hk && gk) LR_TRY(check_ptr(gk, "gk"));
+  return LR_OK;
+}
+
+lr_status lr_rot_turns(int n, const double* freq, unsigned long long* turns) {
+  t_last_error.clear();
+  if (n < 0) return fail(LR_ERR_SHAPE, "n = %d is negative", n);
+  if (n > 0 && (!freq || !turns)) return fail(LR_ERR_NULL, "freq / turns is NULL");
+  for (int i = 0; i < n; ++i)
+    if (!(fabs(freq[i]) <= 65536.0))
+      return fail(LR_ERR_SHAPE, "freq[%d] = %g must be finite and at most 65536 in magnitude", i, freq[i]);
+  // 1 / (2 pi) as a sum of two doubles: the product then holds some 2^-100 of its magnitude, below the 2^-64
+  // turns of the result for every frequency admitted.
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int i = 0; i < n; ++i) {
+    const double f = fabs(freq[i]), p = f * hi;
+    const double rest = fma(f, hi, -p) + f * lo;  // |rest| < 2^-37 turns
+    // p - floor(p) is exact and below 1, and so is its multiple of 2^-64
+    const unsigned long long v = static_cast<unsigned long long>((p - floor(p)) * 0x1p64) +
+                                 static_cast<unsigned long long>(llrint(rest * 0x1p64));
+    turns[i] = freq[i] < 0 ? 0ull - v : v;
+  }
+  return LR_OK;
+}
+
+lr_status lr_qk_fwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const unsigned long long* turns,
+                    const int* pos, const void* gq, const void* gk, const void* q, long long ldq, const void* k,
+                    long long ldk, void* qo, long long ldqo, void* ko, long long ldko, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_qk(dt, T, sh));
+  LR_TRY(check_qk_common(sh, eps, turns, pos, gq, gk));
+  if (sh->Hq) {
+    LR_TRY(check_rows(q, ldq, sh->Hq, sh->dh, "q"));
+    LR_TRY(check_rows(qo, ldqo, sh->Hq, sh->dh, "qo"));
+  }
+  if (sh->Hk) {
+    LR_TRY(check_rows(k, ldk, sh->Hk, sh->dh, "k"));
+    LR_TRY(check_rows(ko, ldko, sh->Hk, sh->dh, "ko"));
+  }
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  QkArgs a = qk_args(T, *sh, eps, turns, pos);
+  a.t[0] = QkTensor{q, nullptr, qo, gq, nullptr, nullptr, ldq, 0, ldqo, sh->Hq};
+  a.t[1] = QkTensor{k, nullptr, ko, gk, nullptr, nullptr, ldk, 0, ldko, sh->Hk};
+  return qk_fwd_impl(c, *sh, a);
+}
+
+size_t lr_qk_bwd_workspace_bytes(lr_dtype dt, int T, const lr_qk_shape* sh) {
+  if (check_qk(dt, T, sh)) return 0;
+  return qk_ws_layout(sh->dh, nullptr, nullptr);
+}
+
+lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const unsigned long long* turns,
+                    const int* pos, const void* gq, const void* gk, const void* q, long long ldq, const void* k,
+                    long long ldk, const void* dqo, long long lddqo, const void* dko, long long lddko, void* dq,
+                    long long lddq, void* dk, long long lddk, float* dgq, float* dgk, void* ws, size_t ws_bytes,
+                    void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_qk(dt, T, sh));
+  LR_TRY(check_qk_common(sh, eps, turns, pos, gq, gk));
+  if (sh->Hq) {
+    LR_TRY(check_rows(dqo, lddqo, sh->Hq, sh->dh, "dqo"));
+    LR_TRY(check_rows(dq, lddq, sh->Hq, sh->dh, "dq"));
+    if (gq) {
+      LR_TRY(check_rows(q, ldq, sh->Hq, sh->dh, "q"));
+      LR_TRY(check_ptr(dgq, "dgq"));
+    }
+  }
+  if (sh->Hk) {
+    LR_TRY(check_rows(dko, lddko, sh->Hk, sh->dh, "dko"));
+    LR_TRY(check_rows(dk, lddk, sh->Hk, sh->dh, "dk"));
+    if (gk) {
+      LR_TRY(check_rows(k, ldk, sh->Hk, sh->dh, "k"));
+      LR_TRY(check_ptr(dgk, "dgk"));
+    }
+  }
+  LR_TRY(check_ptr(ws, "ws"));
+  LR_TRY(check_size(ws_bytes, qk_ws_layout(sh->dh, nullptr, nullptr), "ws"));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  QkArgs a = qk_args(T, *sh, eps, turns, pos);
+  a.t[0] = QkTensor{q, dqo, dq, gq, dgq, nullptr, ldq, lddqo, lddq, sh->Hq};
+  a.t[1] = QkTensor{k, dko, dk, gk, dgk, nullptr, ldk, lddko, lddk, sh->Hk};
+  return qk_bwd_impl(c, *sh, a, ws);
+}
+
+static constexpr int kGradMaxTensors = 65536;
+
+static lr_status check_grads(lr_dtype dt, int n, const void* const* grads, const long long* numel,
+                             void* const* outs, bool clip, const float* stat, const void* ws, size_t ws_bytes) {
+  LR_TRY(check_dtype(dt));
+  if (n < 0 || n > kGradMaxTensors) return fail(LR_ERR_SHAPE, "n = %d tensors must be 0..%d", n, kGradMaxTensors);
+  if (n > 0 && (!grads || !numel || (clip && !outs))) return fail(LR_ERR_NULL, "grads / numel / outs is NULL");
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] < 0 || numel[i] >= (1LL << 40))
+      return fail(LR_ERR_SHAPE, "numel[%d] = %lld must be 0..2^40 - 1", i, numel[i]);
+    if (numel[i] == 0) continue;
+    LR_TRY(check_ptr(grads[i], "grads[i]"));
+    if (clip) LR_TRY(check_ptr(outs[i], "outs[i]"));
+  }
+  LR_TRY(check_ptr(stat, "stat"));
+  LR_TRY(check_ptr(ws, "ws"));
+  return check_size(ws_bytes, grad_ws_bytes(n), "ws");
+}
+
+size_t lr_grad_workspace_bytes(int n) {
+  if (n < 0 || n > kGradMaxTensors) return 0;
+  return grad_ws_bytes(n);
+}
+
+lr_status lr_grad_norm(lr_dtype dt, int n, const void* const* grads, const long long* numel, float* stat, void* ws,
+                       size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_grads(dt, n, grads, numel, nullptr, false, stat, ws, ws_bytes));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  double* part = static_cast<double*>(ws);
+  return dt == LR_BF16 ? grad_impl<bf16>(c, n, grads, numel, 0.f, nullptr, stat, part)
+                       : grad_impl<float>(c, n, grads, numel, 0.f, nullptr, stat, part);
+}
+
+lr_status lr_grad_clip(lr_dtype dt, int n, const void* const* grads, const long long* numel, float max_norm,
+                       void* const* outs, float* stat, void* ws, size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_grads(dt, n, grads, numel, outs, true, stat, ws, ws_bytes));
+  if (!(max_norm >= 0.f) || max_norm > 3.4e38f) return fail(LR_ERR_SHAPE, "max_norm must be finite and not negative");
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  double* part = static_cast<double*>(ws);
+  return dt == LR_BF16 ? grad_impl<bf16>(c, n, grads, numel, max_norm, outs, stat, part)
+                       : grad_impl<float>(c, n, grads, numel, max_norm, outs, stat, part);
 }
 
 size_t lr_stack_workspace_bytes(lr_dtype dt, lr_mode mode, int nblocks, int T, int d, int f, int r) {

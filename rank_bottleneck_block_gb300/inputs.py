@@ -22,7 +22,7 @@ shapes stand in for them):
 from __future__ import annotations
 
 import dataclasses
-from typing import Dict, List, Optional
+from typing import Dict, List, Optional, Tuple
 
 import torch
 
@@ -32,6 +32,9 @@ __all__ = [
     "make_mlp_case",
     "make_proj_case",
     "make_stack_case",
+    "QkShape",
+    "rotary_freq",
+    "make_qk_case",
     "MLP_TINY_F32",
     "MLP_BLOCK_BF16",
     "ATTN_PROJ_BF16",
@@ -170,6 +173,54 @@ def make_block_case(shape: BlockShape, seed: int = 0, device: str = "cpu") -> Di
     c["A_up"], c["B_up"] = _pair(gen, shape.rm, d, shape.f, dt)
     c["A_down"], c["B_down"] = _pair(gen, shape.rm, shape.f, d, dt)
     c["G"] = _normal(gen, (shape.T, d), 1.0).to(dt)
+    return c
+
+
+@dataclasses.dataclass(frozen=True)
+class QkShape:
+    """Norm and position rotation of T tokens' queries (Hq heads) and keys (Hk heads) of dh channels, the
+    first rot of them turned; sec: channel pairs turned by each position axis (sum rot / 2)."""
+
+    T: int
+    Hq: int
+    Hk: int
+    dh: int
+    rot: int
+    sec: Tuple[int, ...]
+    layout: str = "half"  # pairs (p, p + rot/2): "half", or (2p, 2p + 1): "pairs"
+    dtype: str = "bf16"
+    eps: float = 1e-6
+    seq: int = 0  # without positions: tokens per sequence
+
+
+def rotary_freq(rot: int, theta: float = 10000.0) -> List[float]:
+    """The usual geometric frequencies, theta^(-2p/rot) radians per position for pair p."""
+    return [theta ** (-2.0 * p / rot) for p in range(rot // 2)]
+
+
+def make_qk_case(shape: QkShape, seed: int = 0, norm: bool = True, with_grad: bool = True, packed: bool = False,
+                 far: int = 0, device: str = "cpu") -> Dict[str, object]:
+    """q [T, Hq*dh], k [T, Hk*dh] (packed: columns of one [T, (Hq + 2 Hk)*dh] matrix), gains gq, gk [dh] (None
+    without norm), pos int32 [axes, T] in 0..999 plus `far`, freq, and upstream grads dqo, dko."""
+    dt = _torch_dtype(shape.dtype)
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    nq, nk = shape.Hq * shape.dh, shape.Hk * shape.dh
+
+    def rows():
+        if not packed:
+            return _normal(gen, (shape.T, nq), 1.0).to(dt), _normal(gen, (shape.T, nk), 1.0).to(dt)
+        m = _normal(gen, (shape.T, nq + 2 * nk), 1.0).to(dt)
+        return m[:, :nq], m[:, nq:nq + nk]
+
+    c: Dict[str, object] = {}
+    c["q"], c["k"] = rows()
+    c["gq"] = _normal(gen, (shape.dh,), 0.1, mean=1.0).to(dt) if norm else None
+    c["gk"] = _normal(gen, (shape.dh,), 0.1, mean=1.0).to(dt) if norm else None
+    c["pos"] = torch.randint(0, 1000, (len(shape.sec), shape.T), generator=gen, device=device).add_(far).int()
+    c["freq"] = rotary_freq(shape.rot)
+    if with_grad:
+        c["dqo"], c["dko"] = rows()
     return c
 
 

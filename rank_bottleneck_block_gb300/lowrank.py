@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(PKG, "liblowrank.so")
 LR_F32, LR_BF16 = 0, 1
 LR_SAVE_FULL, LR_SAVE_CKPT = 0, 1
 LR_ACT_SILU, LR_ACT_IDENTITY = 0, 1
+LR_PAIR_HALF, LR_PAIR_ADJACENT = 0, 1
 STATUS = {
     0: "LR_OK", 1: "LR_ERR_NULL", 2: "LR_ERR_SHAPE", 3: "LR_ERR_ALIGN", 4: "LR_ERR_DTYPE",
     5: "LR_ERR_WORKSPACE", 6: "LR_ERR_CUDA", 7: "LR_ERR_TIMEOUT", 8: "LR_ERR_UNSUPPORTED",
@@ -32,7 +33,8 @@ EXPORTED = [
     "lr_proj_fwd_noalloc", "lr_dense_saved_bytes", "lr_dense_fwd_workspace_bytes", "lr_dense_bwd_workspace_bytes",
     "lr_dense_fwd", "lr_dense_bwd", "lr_btp_payload_floats", "lr_btp_workspace_bytes", "lr_btp_partial",
     "lr_btp_finish", "lr_attn_saved_bytes", "lr_attn_workspace_bytes", "lr_attn_fwd", "lr_attn_bwd",
-    "lr_block_saved_bytes", "lr_block_workspace_bytes", "lr_block_fwd", "lr_block_bwd",
+    "lr_block_saved_bytes", "lr_block_workspace_bytes", "lr_block_fwd", "lr_block_bwd", "lr_rot_turns", "lr_qk_fwd",
+    "lr_qk_bwd_workspace_bytes", "lr_qk_bwd", "lr_grad_workspace_bytes", "lr_grad_norm", "lr_grad_clip",
 ]
 
 
@@ -61,9 +63,15 @@ class lr_block_grads(ctypes.Structure):
                 ("down", lr_pair_grad)]
 
 
+class lr_qk_shape(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("dh", ctypes.c_int), ("rot", ctypes.c_int),
+                ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("sec", ctypes.c_int * 4), ("seq", ctypes.c_int)]
+
+
 _lib = None
 
 _I, _F, _P, _SZ = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_LL, _QKS = ctypes.c_longlong, ctypes.POINTER(lr_qk_shape)
 _SIGS = {
     "lr_mlp_saved_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "lr_mlp_fwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
@@ -104,6 +112,14 @@ _SIGS = {
     "lr_dense_bwd": (_I, [_I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "lr_stack_step": (_I, [_I, _I, _I, _I, _I, _I, _I, _F, _P, _P, ctypes.POINTER(_P), ctypes.POINTER(lr_pair), _P,
                            _P, ctypes.POINTER(_P), ctypes.POINTER(lr_pair_grad), _P, _SZ, _P]),
+    "lr_rot_turns": (_I, [_I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_ulonglong)]),
+    "lr_qk_fwd": (_I, [_I, _I, _QKS, _F, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P]),
+    "lr_qk_bwd_workspace_bytes": (_SZ, [_I, _I, _QKS]),
+    "lr_qk_bwd": (_I, [_I, _I, _QKS, _F, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P,
+                       _P, _P, _SZ, _P]),
+    "lr_grad_workspace_bytes": (_SZ, [_I]),
+    "lr_grad_norm": (_I, [_I, _I, ctypes.POINTER(_P), ctypes.POINTER(_LL), _P, _P, _SZ, _P]),
+    "lr_grad_clip": (_I, [_I, _I, ctypes.POINTER(_P), ctypes.POINTER(_LL), _F, ctypes.POINTER(_P), _P, _P, _SZ, _P]),
     "lr_last_error": (ctypes.c_char_p, []),
     "lr_check_device_error": (_I, [_P]),
     "lr_selftest_wait_timeout": (_I, [ctypes.c_ulonglong, _P]),
@@ -312,6 +328,57 @@ def lr_block_bwd(dt, b, s, H, dh, f, ra, rm, eps, x, w: lr_block_weights, saved,
                  stream=None):
     _check(lib().lr_block_bwd(dt, b, s, H, dh, f, ra, rm, eps, _p(x), ctypes.byref(w), _p(saved), _nbytes(saved),
                               _p(dout), _p(dx), ctypes.byref(g), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def qk_shape(Hq, Hk, dh, rot, sec, layout=LR_PAIR_HALF, seq=0) -> lr_qk_shape:
+    """sec: pairs turned by each position axis (1 to 4 of them)."""
+    if not 1 <= len(sec) <= 4:
+        raise ValueError(f"{len(sec)} position axes: 1 to 4 needed")
+    return lr_qk_shape(Hq, Hk, dh, rot, layout, len(sec), (ctypes.c_int * 4)(*sec), seq)
+
+
+def lr_rot_turns(freq: Sequence[float]) -> list:
+    """The frequencies (radians per position) as integers in units of 2^-64 turn."""
+    n = len(freq)
+    out = (ctypes.c_ulonglong * max(n, 1))()
+    _check(lib().lr_rot_turns(n, (ctypes.c_double * max(n, 1))(*freq), out))
+    return list(out)[:n]
+
+
+def lr_qk_fwd(dt, T, sh: lr_qk_shape, eps, turns, pos, gq, gk, q, ldq, k, ldk, qo, ldqo, ko, ldko, stream=None):
+    _check(lib().lr_qk_fwd(dt, T, ctypes.byref(sh), eps, _p(turns), _p(pos), _p(gq), _p(gk), _p(q), ldq, _p(k), ldk,
+                           _p(qo), ldqo, _p(ko), ldko, _stream(stream)))
+
+
+def lr_qk_bwd_workspace_bytes(dt, T, sh: lr_qk_shape) -> int:
+    return lib().lr_qk_bwd_workspace_bytes(dt, T, ctypes.byref(sh))
+
+
+def lr_qk_bwd(dt, T, sh: lr_qk_shape, eps, turns, pos, gq, gk, q, ldq, k, ldk, dqo, lddqo, dko, lddko, dq, lddq, dk,
+              lddk, dgq, dgk, ws, stream=None):
+    _check(lib().lr_qk_bwd(dt, T, ctypes.byref(sh), eps, _p(turns), _p(pos), _p(gq), _p(gk), _p(q), ldq, _p(k), ldk,
+                           _p(dqo), lddqo, _p(dko), lddko, _p(dq), lddq, _p(dk), lddk, _p(dgq), _p(dgk), _p(ws),
+                           _nbytes(ws), _stream(stream)))
+
+
+def tensor_list(ts):
+    """A list of tensors as the host arrays lr_grad_norm and lr_grad_clip take: (pointers, element counts)."""
+    return _ptrs(ts), (ctypes.c_longlong * len(ts))(*[t.numel() for t in ts])
+
+
+def lr_grad_workspace_bytes(n) -> int:
+    return lib().lr_grad_workspace_bytes(n)
+
+
+def lr_grad_norm(dt, grads, numel, stat, ws, stream=None):
+    """grads, numel: the arrays of tensor_list."""
+    _check(lib().lr_grad_norm(dt, len(numel), grads, numel, _p(stat), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def lr_grad_clip(dt, grads, numel, max_norm, outs, stat, ws, stream=None):
+    """grads, numel: the arrays of tensor_list; outs: its pointers for the outputs (grads itself: in place)."""
+    _check(lib().lr_grad_clip(dt, len(numel), grads, numel, max_norm, outs, _p(stat), _p(ws), _nbytes(ws),
+                              _stream(stream)))
 
 
 def lr_btp_payload_floats(T, r, group) -> int:

@@ -1,17 +1,18 @@
 """Device-buffer plumbing around the C ABI for one MLP block, one projection
-group and one block stack.
+group, one block stack, attention with the norm and rotation of its queries and
+keys, one transformer block, and the clipping of their gradients.
 
 torch only allocates device memory and supplies the stream; every computation
 is a call into liblowrank.so through the ctypes binding.
 """
 from __future__ import annotations
 
-from typing import Dict, List, Optional
+from typing import Dict, List, Optional, Sequence
 
 import torch
 
 from . import lowrank as L
-from .inputs import MlpShape, ProjShape
+from .inputs import MlpShape, ProjShape, QkShape
 
 _U8 = torch.uint8
 
@@ -28,7 +29,73 @@ def _buf(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=_U8, device=device)
 
 
-class MlpBlock:
+def _span(t: torch.Tensor):
+    return t.data_ptr(), t.data_ptr() + L._nbytes(t)
+
+
+class GradClip:
+    """The norm over a list of gradient tensors, and the tensors scaled to at most max_norm.
+
+    grads: contiguous tensors of one type (fp32 as the backward passes write them, or bf16) on one
+    device, 16-byte aligned; outs: where the scaled tensors go (None: in place).  norm() leaves the
+    norm in self.norm [1]; clip() leaves it there, min(1, max_norm / (norm + 1e-6)) in self.scale [1]
+    and the scaled gradients in outs.  Device tensors: nothing waits for the GPU.
+    """
+
+    def __init__(self, grads: Sequence[torch.Tensor], max_norm: float = 1.0,
+                 outs: Optional[Sequence[torch.Tensor]] = None):
+        self.grads, self.max_norm = list(grads), float(max_norm)
+        self.outs = self.grads if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("no gradients")
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients but {len(self.outs)} outputs")
+        first = self.grads[0]
+        for g, o in zip(self.grads, self.outs):
+            for t in (g, o):
+                if t.dtype != first.dtype or t.device != first.device or not t.is_contiguous():
+                    raise ValueError("gradients and outputs must be contiguous, of one type and on one device")
+            if o.numel() != g.numel():
+                raise ValueError(f"an output has {o.numel()} elements, its gradient {g.numel()}")
+        self.dt = L.dtype_code(first)
+        # a written tensor is its own gradient, or overlaps nothing else of either list
+        spans = sorted([(*_span(o), 1) for o in self.outs if o.numel()] +
+                       [(*_span(g), 0) for g, o in zip(self.grads, self.outs)
+                        if g.numel() and o.data_ptr() != g.data_ptr()])
+        end = written = 0  # the furthest end so far, of any span and of a written one
+        for lo, hi, w in spans:
+            if lo < (end if w else written):
+                raise ValueError("an output overlaps another output or another gradient")
+            end, written = max(end, hi), max(written, hi if w else 0)
+        self._g, self._n = L.tensor_list(self.grads)
+        self._o = self._g if outs is None else L.tensor_list(self.outs)[0]
+        self.stat = torch.zeros(2, dtype=torch.float32, device=first.device)
+        self.norm, self.scale = self.stat[:1], self.stat[1:]
+        self.ws = _buf(L.lr_grad_workspace_bytes(len(self.grads)), first.device)
+
+    def measure(self, stream=None) -> torch.Tensor:
+        L.lr_grad_norm(self.dt, self._g, self._n, self.stat, self.ws, stream)
+        return self.norm
+
+    def clip(self, stream=None) -> torch.Tensor:
+        L.lr_grad_clip(self.dt, self._g, self._n, self.max_norm, self._o, self.stat, self.ws, stream)
+        return self.norm
+
+
+class _Clipped:
+    """clip_grads for the runners that hold gradients (they list them in grad_tensors)."""
+
+    _clip: Optional[GradClip] = None
+
+    def clip_grads(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Scale every gradient in place so that their common norm is at most max_norm; the norm [1]."""
+        if self._clip is None:
+            self._clip = GradClip(self.grad_tensors())
+        self._clip.max_norm = float(max_norm)
+        return self._clip.clip(stream)
+
+
+class MlpBlock(_Clipped):
     """One low-rank SwiGLU MLP block resident on the device (weights, saved set, workspaces, grads)."""
 
     def __init__(self, shape: MlpShape, case: Dict[str, torch.Tensor], mode: int = L.LR_SAVE_CKPT,
@@ -79,8 +146,11 @@ class MlpBlock:
         self.forward(stream=stream)
         self.backward(stream=stream)
 
+    def grad_tensors(self):
+        return [self.dg, *self.grads.values()]
 
-class DenseBlock:
+
+class DenseBlock(_Clipped):
     """The full-rank SwiGLU MLP block of the same d, f, resident on the device: the reference point
     the low-rank block is compared with."""
 
@@ -117,6 +187,9 @@ class DenseBlock:
     def step(self, stream=None):
         self.forward(stream=stream)
         self.backward(stream=stream)
+
+    def grad_tensors(self):
+        return [self.dg, *self.grads.values()]
 
 
 class HostPipeline:
@@ -220,7 +293,7 @@ class ProjGroup:
         self.backward(stream)
 
 
-class BlockStack:
+class BlockStack(_Clipped):
     """A residual stack of MLP blocks trained with an MSE loss (one call per step)."""
 
     def __init__(self, shape: MlpShape, case: Dict[str, object], mode: int = L.LR_SAVE_CKPT, device="cuda"):
@@ -255,6 +328,9 @@ class BlockStack:
         L.lr_stack_step(self.dt, self.mode, s.T, s.d, s.f, s.r, s.eps, self.x, self.target,
                         [b["g"] for b in self.blocks], pairs, self.loss, self.dx, self.dgs, grads, self.ws, stream)
         return self.loss
+
+    def grad_tensors(self):
+        return [*self.dgs, *(t for gr in self.grads for t in gr.values())]
 
 
 class GraphStep:
@@ -314,7 +390,77 @@ class Attention:
         self.backward(None, stream)
 
 
-class TransformerBlock:
+class QkRotary:
+    """Norm and position rotation of queries and keys between their projections and attention.
+
+    case: q [T, Hq*dh], k [T, Hk*dh] (rows may be further apart: columns of a packed matrix; None with 0
+    heads), gq, gk [dh] (None: no norm), pos int32 [axes, T] (None: position t mod shape.seq), freq (the
+    rot / 2 frequencies in radians per position) and, for backward(), dqo, dko.  forward() writes qo, ko;
+    backward() writes dq, dk and, with the norm, dgq, dgk [dh] fp32.
+    """
+
+    def __init__(self, shape: QkShape, case: Dict[str, object], device="cuda"):
+        s, self.s, self.dt = shape, shape, _dt(shape.dtype)
+        layouts = {"half": L.LR_PAIR_HALF, "pairs": L.LR_PAIR_ADJACENT}
+        self.sh = L.qk_shape(s.Hq, s.Hk, s.dh, s.rot, s.sec, layouts[s.layout], s.seq)
+        td = _tdt(s.dtype)
+
+        def on_device(name, size, dtype=td):
+            t = case.get(name)
+            if t is None:
+                return None
+            if tuple(t.shape) != size or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
+                raise ValueError(f"{name}: {list(size)} {dtype} with contiguous rows needed, not {list(t.shape)} "
+                                 f"{t.dtype} with strides {t.stride()}")
+            return t.to(device)
+
+        if len(case["freq"]) != s.rot // 2:
+            raise ValueError(f"{len(case['freq'])} frequencies for {s.rot // 2} pairs")
+        turns = L.lr_rot_turns([float(f) for f in case["freq"]])
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.pos = on_device("pos", (len(s.sec), s.T), torch.int32)
+        if self.pos is not None and not self.pos.is_contiguous():
+            raise ValueError("pos must be contiguous")
+        self.q, self.k = on_device("q", (s.T, s.Hq * s.dh)), on_device("k", (s.T, s.Hk * s.dh))
+        self.gq, self.gk = on_device("gq", (s.dh,)), on_device("gk", (s.dh,))
+        self.dqo, self.dko = on_device("dqo", (s.T, s.Hq * s.dh)), on_device("dko", (s.T, s.Hk * s.dh))
+
+        def fresh(H, wanted=True):
+            return torch.empty(s.T, H * s.dh, dtype=td, device=device) if H and wanted else None
+
+        self.qo, self.ko = fresh(s.Hq), fresh(s.Hk)
+        back = self.dqo is not None or self.dko is not None
+        self.dq, self.dk = fresh(s.Hq, back), fresh(s.Hk, back)
+        f32 = dict(dtype=torch.float32, device=device)
+        self.dgq = torch.empty(s.dh, **f32) if back and s.Hq and self.gq is not None else None
+        self.dgk = torch.empty(s.dh, **f32) if back and s.Hk and self.gk is not None else None
+        self.ws = _buf(L.lr_qk_bwd_workspace_bytes(self.dt, s.T, self.sh), device) if back else None
+
+        def rows(t):
+            return (L._p(t), 0 if t is None else t.stride(0) if s.T > 1 else t.shape[1])
+
+        common = (self.dt, s.T, self.sh, s.eps, L._p(self.turns), L._p(self.pos), L._p(self.gq), L._p(self.gk),
+                  *rows(self.q), *rows(self.k))
+        self._fwd = (*common, *rows(self.qo), *rows(self.ko))
+        self._bwd = (*common, *rows(self.dqo), *rows(self.dko), *rows(self.dq), *rows(self.dk), L._p(self.dgq),
+                     L._p(self.dgk), self.ws)
+
+    def forward(self, stream=None):
+        L.lr_qk_fwd(*self._fwd, stream)
+        return self.qo, self.ko
+
+    def backward(self, stream=None):
+        if self.ws is None:
+            raise ValueError("no upstream gradients dqo, dko were given")
+        L.lr_qk_bwd(*self._bwd, stream)
+        return self.dq, self.dk
+
+    def step(self, stream=None):
+        self.forward(stream)
+        self.backward(stream)
+
+
+class TransformerBlock(_Clipped):
     """One low-rank transformer block (q/k/v group, causal attention, o-projection with its
     residual, MLP block in checkpoint mode) resident on the device, bf16."""
 
@@ -352,3 +498,6 @@ class TransformerBlock:
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
+
+    def grad_tensors(self):
+        return [self.dg_attn, self.dg_mlp, *self.grads.values()]
