@@ -1518,7 +1518,7 @@ static QkArgs qk_args(int T, const lr_qk_shape& sh, float eps, const unsigned lo
 static lr_status qk_fwd_impl(const Ctx& c, const lr_qk_shape& sh, const QkArgs& a) {
   LaunchScope scope("qk_fwd", c.st, 0, 2.0 * c.es * a.T * (sh.Hq + sh.Hk) * a.dh);
   const bool adj = sh.layout == LR_PAIR_ADJACENT;
-  cudaError_t e = c.dt == LR_BF16 ? launch_qk_fwd<bf16>(a, adj, c.st) : launch_qk_fwd<float>(a, adj, c.st);
+  cudaError_t e = c.dt == LR_BF16 ? launch_qk_fwd<bf16>(a, adj, c.sms, c.st) : launch_qk_fwd<float>(a, adj, c.sms, c.st);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation: %s", cudaGetErrorString(e));
   return LR_OK;
 }
@@ -1531,7 +1531,7 @@ static lr_status qk_bwd_impl(const Ctx& c, const lr_qk_shape& sh, QkArgs& a, voi
   LaunchScope scope("qk_bwd", c.st, 0,
                     c.es * rows * (sh.Hq * (a.t[0].g ? 3.0 : 2.0) + sh.Hk * (a.t[1].g ? 3.0 : 2.0)));
   const bool adj = sh.layout == LR_PAIR_ADJACENT;
-  cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.st) : launch_qk_bwd<float>(a, adj, c.st);
+  cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.sms, c.st) : launch_qk_bwd<float>(a, adj, c.sms, c.st);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
   return LR_OK;
 }

@@ -37,11 +37,16 @@ struct QkArgs {
   float eps;
 };
 
+// How a launch cuts its work: blocks of q, then of k; each token's heads in `chunks` runs of `passes` passes.
+struct QkPlan {
+  int blocks[2], chunks[2], passes[2];
+};
+
 // adjacent: pairs are channels (2p, 2p + 1), else (p, p + rot / 2).
 template <typename ST>
-cudaError_t launch_qk_fwd(const QkArgs& a, bool adjacent, cudaStream_t st);
+cudaError_t launch_qk_fwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st);
 // Writes dx of both tensors and the partial sums of dg, then dg.
 template <typename ST>
-cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, cudaStream_t st);
+cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st);
 
 }  // namespace lr
