@@ -260,7 +260,7 @@ lr_status lr_attn_bwd(lr_dtype dt, int b, int s, int H, int dh, float scale, con
  * (the same pointer and row distance: qo = q, dq = dqo, ...); outputs must not overlap
  * anything else.  Elements between rows' ends are not touched.
  * dh and rot multiples of 8, 8 <= dh <= 256 (or dh <= 512 with dh and rot multiples of 16),
- * 0 <= rot <= dh, axes 1..4.  Sums over channels and the dg sums are fp32; y, dx are rounded
+ * 0 <= rot <= dh, axes 1..4, H*dh <= 2^24 and T*H <= 2^30 for each tensor.  Sums over channels and the dg sums are fp32; y, dx are rounded
  * once.  |x| must stay below 1e18 (the square sums are fp32).
  */
 typedef enum { LR_PAIR_HALF = 0, LR_PAIR_ADJACENT = 1 } lr_pair_layout;

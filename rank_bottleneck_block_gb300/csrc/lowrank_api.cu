@@ -2221,9 +2221,11 @@ static lr_status check_qk(lr_dtype dt, int T, const lr_qk_shape* sh) {
                 sh->rot);
   if (sh->Hq < 0 || sh->Hk < 0 || sh->Hq + 0LL + sh->Hk < 1)
     return fail(LR_ERR_SHAPE, "Hq = %d, Hk = %d: at least one head needed", sh->Hq, sh->Hk);
-  for (long long H : {sh->Hq, sh->Hk})
+  for (long long H : {sh->Hq, sh->Hk}) {
     if (H * sh->dh > (1 << 24))
       return fail(LR_ERR_SHAPE, "H*dh = %lld channels must not exceed 16777216", H * sh->dh);
+    if (H * T > (1 << 30)) return fail(LR_ERR_SHAPE, "T*H = %lld head vectors must not exceed 2^30", H * T);
+  }
   if (sh->layout != LR_PAIR_HALF && sh->layout != LR_PAIR_ADJACENT)
     return fail(LR_ERR_DTYPE, "unknown pair layout %d", sh->layout);
   if (sh->axes < 1 || sh->axes > kQkMaxAxes) return fail(LR_ERR_SHAPE, "axes = %d must be 1..4", sh->axes);

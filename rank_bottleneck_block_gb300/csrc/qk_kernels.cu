@@ -2,55 +2,53 @@
 // that both channels of every pair are in the same lane: two runs of U channels, rot / 2 apart (pairs (p, p + rot/2))
 // or adjacent (pairs (2p, 2p + 1)); slots past the turned channels hold 2 U neighbouring channels.  So a vector is
 // read once with 16-byte loads (8-byte ones for bf16 whose dh or rot is no multiple of 16), its sums take log2 G
-// shuffles, and an output may take its input's place.  A warp takes one token and a run of its heads, 32 / G at a
-// time: a lane's slot stays the same, so its angles are computed once for all of them and its gains stay in registers.
+// shuffles, and an output may take its input's place.  The vectors of a tensor are numbered token by token, head by
+// head; each warp takes an equal share of consecutive ones, 32 / G at a step, and computes a lane's angles once per
+// token.  Loads run kAhead steps ahead of the arithmetic through a ring in shared memory (asynchronous copies; a thread
+// reads back only what it copied itself, so it waits for nothing but its own copies).  The arithmetic is on two pairs
+// at a time (the f32x2 instructions).
 #include "qk_kernels.cuh"
+
+#include <algorithm>
 
 namespace lr {
 
-// A run of U channels as stored: kept packed while several vectors are in flight.
-template <typename ST, int U>
-struct alignas(sizeof(ST) * U < 16 ? sizeof(ST) * U : 16) Run {
-  ST v[U];
+// ------------------------------------------------------ two floats at a time
+struct alignas(8) f2 {
+  float x, y;
 };
+__device__ __forceinline__ unsigned long long bits(f2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ f2 of_bits(unsigned long long r) {
+  f2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+  return of_bits(r);
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return of_bits(r);
+}
+__device__ __forceinline__ f2 both(float a) { return {a, a}; }
+__device__ __forceinline__ f2 operator-(f2 a) { return {-a.x, -a.y}; }
 
-template <typename ST, int U>
-__device__ __forceinline__ void get(const ST* p, Run<ST, U>& r) {
-  r = *reinterpret_cast<const Run<ST, U>*>(p);
-}
-template <int U>
-__device__ __forceinline__ void unpack(const Run<bf16, U>& r, float* v) {
-#pragma unroll
-  for (int i = 0; i < U; i += 2) {
-    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.v[i]));
-    v[i] = f.x;
-    v[i + 1] = f.y;
-  }
-}
-template <int U>
-__device__ __forceinline__ void unpack(const Run<float, U>& r, float* v) {
-#pragma unroll
-  for (int i = 0; i < U; ++i) v[i] = r.v[i];
-}
-template <int U>
-__device__ __forceinline__ void put(bf16* p, const float* v) {
-  Run<bf16, U> r;
-#pragma unroll
-  for (int i = 0; i < U; i += 2)
-    *reinterpret_cast<__nv_bfloat162*>(&r.v[i]) = __floats2bfloat162_rn(v[i], v[i + 1]);
-  *reinterpret_cast<Run<bf16, U>*>(p) = r;
-}
-template <int U>
-__device__ __forceinline__ void put(float* p, const float* v) {
-#pragma unroll
-  for (int i = 0; i < U; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-
+// ------------------------------------------------------------ lanes and slots
 // The lane's slot: where its two runs start, and whether its channels are turned.
 struct Slot {
-  int o0, o1, pair;  // pair: the first of the slot's U pairs
+  int o0, o1, pair, axis;  // pair: the first of the slot's U pairs; axis: theirs, or -1 if they have several
   bool on, turned;
 };
+__device__ __forceinline__ int axis_of(const QkArgs& a, int p) {
+  return (p >= a.sec_end[0]) + (p >= a.sec_end[1]) + (p >= a.sec_end[2]);
+}
 template <int U, bool ADJ, int G>
 __device__ __forceinline__ Slot slot_of(const QkArgs& a) {
   const int j = threadIdx.x % G, n = a.rot / (2 * U);
@@ -58,41 +56,125 @@ __device__ __forceinline__ Slot slot_of(const QkArgs& a) {
   s.on = j < a.dh / (2 * U);
   s.turned = s.on && j < n;
   s.pair = j * U;
+  s.axis = axis_of(a, s.pair);
+  if (axis_of(a, s.pair + U - 1) != s.axis) s.axis = -1;
   s.o0 = ADJ ? 2 * U * j : s.turned ? U * j : a.rot + 2 * U * (j - n);
   s.o1 = !ADJ && s.turned ? s.o0 + a.rot / 2 : s.o0 + U;
   return s;
 }
 
-// Cosines and sines of the slot's pairs at token t.  pos * turns wraps at 2^64, a whole number of turns, so the
-// product is exact for any position; its top 32 bits, signed, are the angle in [-1/2, 1/2] turns.  For bf16 outputs
-// the hardware sine and cosine serve (off by 2^-21.2 at most on [-pi, pi], against a rounding of 2^-9).
+// The slot's channels as the first and second members of its pairs, X[i] and Y[i] (of a slot that is not turned: in
+// the same order of memory).  A run of U channels is W 32-bit words.
 template <typename ST, int U>
-__device__ __forceinline__ void slot_angles(const QkArgs& a, const Slot& sl, int t, float* c, float* s) {
-  if (!sl.turned) return;
-  if (a.pos == nullptr) t %= a.seq;
+constexpr int kWords = U * static_cast<int>(sizeof(ST)) / 4;
+
+template <typename ST, int U, bool ADJ>
+__device__ __forceinline__ void pairs_of(const uint32_t* w0, const uint32_t* w1, f2* X, f2* Y) {
+  float x[U], y[U];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int p = sl.pair + i;
-    const int axis = (p >= a.sec_end[0]) + (p >= a.sec_end[1]) + (p >= a.sec_end[2]);
-    const long long pos = a.pos ? a.pos[static_cast<long long>(axis) * a.T + t] : t;
-    const unsigned long long ph = static_cast<unsigned long long>(pos) * a.turns[p];
-    const float top = static_cast<float>(static_cast<int>((ph + 0x80000000ull) >> 32));
-    if constexpr (sizeof(ST) == 2) __sincosf(top * 1.46291807926715968e-9f /* 2 pi / 2^32 */, &s[i], &c[i]);
-    else sincospif(top * 0x1p-31f, &s[i], &c[i]);
+    if constexpr (sizeof(ST) == 4) {
+      x[i] = __uint_as_float(ADJ ? (2 * i < U ? w0[2 * i] : w1[2 * i - U]) : w0[i]);
+      y[i] = __uint_as_float(ADJ ? (2 * i < U ? w0[2 * i + 1] : w1[2 * i + 1 - U]) : w1[i]);
+    } else if constexpr (ADJ) {
+      const uint32_t w = 2 * i < U ? w0[i] : w1[i - U / 2];
+      x[i] = __uint_as_float(w << 16);
+      y[i] = __uint_as_float(w & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(i % 2 ? w0[i / 2] & 0xffff0000u : w0[i / 2] << 16);
+      y[i] = __uint_as_float(i % 2 ? w1[i / 2] & 0xffff0000u : w1[i / 2] << 16);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U / 2; ++i) {
+    X[i] = {x[2 * i], x[2 * i + 1]};
+    Y[i] = {y[2 * i], y[2 * i + 1]};
   }
 }
 
-// Turns the slot's pairs of (u, v), its two runs, by +angle (SIGN = 1) or -angle (-1).
-template <int U, bool ADJ, int SIGN>
-__device__ __forceinline__ void turn(float* u, float* v, const float* c, const float* s) {
+// Words next to one another: the widest loads and stores that fit.
+template <int N>
+__device__ __forceinline__ void get_words(const void* p, uint32_t* w) {
+  if constexpr (N == 2) {
+    const uint2 q = *static_cast<const uint2*>(p);
+    w[0] = q.x, w[1] = q.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 q = static_cast<const uint4*>(p)[i];
+      w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void put_words(void* p, const uint32_t* w) {
+  if constexpr (N == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      static_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename ST, int U, bool ADJ>
+__device__ __forceinline__ void get_pairs(const ST* p0, const ST* p1, f2* X, f2* Y) {
+  uint32_t w0[kWords<ST, U>], w1[kWords<ST, U>];
+  get_words<kWords<ST, U>>(p0, w0);
+  get_words<kWords<ST, U>>(p1, w1);
+  pairs_of<ST, U, ADJ>(w0, w1, X, Y);
+}
+
+// Rounds to ST and stores.
+template <typename ST, int U, bool ADJ>
+__device__ __forceinline__ void put_pairs(ST* p0, ST* p1, const f2* X, const f2* Y) {
+  float x[U], y[U];
+#pragma unroll
+  for (int i = 0; i < U / 2; ++i) {
+    x[2 * i] = X[i].x, x[2 * i + 1] = X[i].y;
+    y[2 * i] = Y[i].x, y[2 * i + 1] = Y[i].y;
+  }
+  uint32_t w[2 * kWords<ST, U>];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    float& x = ADJ ? (2 * i < U ? u[2 * i] : v[2 * i - U]) : u[i];
-    float& y = ADJ ? (2 * i < U ? u[2 * i + 1] : v[2 * i + 1 - U]) : v[i];
-    const float sn = SIGN > 0 ? s[i] : -s[i];
-    const float x1 = x * c[i] - y * sn;
-    y = x * sn + y * c[i];
-    x = x1;
+    if constexpr (sizeof(ST) == 4) {
+      w[ADJ ? 2 * i : i] = __float_as_uint(x[i]);
+      w[ADJ ? 2 * i + 1 : U + i] = __float_as_uint(y[i]);
+    } else if constexpr (ADJ) {
+      w[i] = pack(x[i], y[i]);
+    } else if (i % 2 == 0) {
+      w[i / 2] = pack(x[i], x[i + 1]);
+      w[U / 2 + i / 2] = pack(y[i], y[i + 1]);
+    }
+  }
+  put_words<kWords<ST, U>>(p0, w);
+  put_words<kWords<ST, U>>(p1, w + kWords<ST, U>);
+}
+
+// Cosines and sines of the slot's pairs at token t.  pos * turns wraps at 2^64, a whole number of turns, so the
+// product is exact for any position; its top 32 bits, signed, are the angle in [-1/2, 1/2) turns.  For bf16 outputs
+// the hardware sine and cosine serve (off by 2^-21.2 at most on [-pi, pi], against a rounding of 2^-9).
+template <typename ST, int U>
+__device__ __forceinline__ void slot_angles(const QkArgs& a, const Slot& sl, const unsigned long long* turns, int t,
+                                            int pos, f2* C, f2* S) {
+  float c[U], s[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const unsigned long long w = turns[sl.pair + i];
+    if (sl.axis < 0 && a.pos) pos = a.pos[static_cast<long long>(axis_of(a, sl.pair + i)) * a.T + t];
+    const float top = static_cast<float>(static_cast<int>((static_cast<unsigned long long>(1LL * pos) * w) >> 32));
+    if constexpr (sizeof(ST) == 2) __sincosf(top * 1.46291807926715968e-9f /* 2 pi / 2^32 */, &s[i], &c[i]);
+    else sincospif(top * 0x1p-31f, &s[i], &c[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < U / 2; ++i) {
+    C[i] = {c[2 * i], c[2 * i + 1]};
+    S[i] = {s[2 * i], s[2 * i + 1]};
   }
 }
 
@@ -103,187 +185,331 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-constexpr int kWarps = 8;   // most warps of a block
-constexpr int kFlight = 2;  // vectors of a lane in flight
-template <typename ST, int U>
-constexpr int kBwdBlocks = sizeof(ST) * U > 16 ? 1 : 2;  // backward blocks an SM holds
+// ---------------------------------------------------------------- the ring
+constexpr int kWarps = 4;  // of a block
+constexpr int kThreads = 32 * kWarps;
+constexpr int kAhead = 3;  // steps whose loads are in flight while one is computed
+constexpr int kRing = kAhead + 1;
 
+// Blocks an SM holds; es * u: bytes of a run.
+constexpr int fwd_blocks(int u, int es) { return es * u > 16 ? 4 : u == 8 ? 5 : 8; }
+constexpr int bwd_blocks(int u, int es) { return es * u > 16 ? 2 : u == 8 ? 4 : 5; }
+
+template <int B>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(from), "n"(B) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// For each step in flight, RUNS runs of every thread (in pieces of at most 16 bytes, a thread's pieces kThreads apart,
+// so that a warp's accesses are contiguous) and its position; then the turns [rot / 2] and the gain [dh] as stored.
+template <typename ST, int U, int RUNS>
+struct Ring {
+  static constexpr int kPiece = kWords<ST, U> < 4 ? 4 * kWords<ST, U> : 16, kPieces = 4 * kWords<ST, U> / kPiece;
+  alignas(16) unsigned char data[kRing][RUNS][kPieces][kThreads][kPiece];
+  int pos[kRing][kThreads];
+  alignas(16) unsigned long long turns[1];
+
+  __device__ __forceinline__ void load(int slot, int run, const ST* from) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      copy_async<kPiece>(data[slot][run][i][threadIdx.x], reinterpret_cast<const char*>(from) + i * kPiece);
+  }
+  template <bool ADJ>
+  __device__ __forceinline__ void read(int slot, int run, f2* X, f2* Y) const {
+    uint32_t w[2][kWords<ST, U>];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        get_words<kPiece / 4>(data[slot][run + r][i][threadIdx.x], w[r] + i * (kPiece / 4));
+    pairs_of<ST, U, ADJ>(w[0], w[1], X, Y);
+  }
+  // The turns and the gain; readable after the block's next barrier.
+  __device__ __forceinline__ ST* fill(const QkArgs& a, const ST* g) {
+    ST* gain = reinterpret_cast<ST*>(turns + a.rot / 2);
+    for (int p = threadIdx.x; p < a.rot / 2; p += kThreads) turns[p] = a.turns[p];
+    if (g)
+      for (int c = threadIdx.x; c < a.dh; c += kThreads) gain[c] = g[c];
+    return gain;
+  }
+  static size_t bytes(const QkArgs& a) {
+    return sizeof(Ring) - 16 + a.rot / 2 * sizeof(unsigned long long) + a.dh * sizeof(ST);
+  }
+};
+
+// Where a lane group's vector of a step lies in one tensor; a step moves it by `step` elements, and by `wrap` more when
+// it passes a token's last head.
+template <typename ST>
+struct Walk {
+  ST* p;
+  long long step, wrap;
+  __device__ __forceinline__ Walk(ST* base, long long ld, int t, int h, int dh, int H, int step_t, int step_h)
+      : p(base + t * ld + h * dh), step(step_t * ld + step_h * dh), wrap(ld - H * dh) {}
+  __device__ __forceinline__ void next(bool wraps) { p += step + (wraps ? wrap : 0); }
+};
+
+// A warp's steps and its groups' first vectors.
+struct Share {
+  int which, steps, t, h, step_t, step_h;
+  unsigned block, v, all;  // v: the group's vector, of `all`
+  __device__ __forceinline__ Share(const QkArgs& a, const QkPlan& pl, int P, int sub) {
+    which = blockIdx.x < static_cast<unsigned>(pl.blocks[0]) ? 0 : 1;
+    block = blockIdx.x - (which ? pl.blocks[0] : 0);
+    const unsigned w = block * kWarps + threadIdx.x / 32, more = pl.more[which];
+    steps = pl.steps[which] + (w < more);
+    v = (w * pl.steps[which] + min(w, more)) * P + sub;
+    const unsigned H = a.t[which].H;
+    all = H * a.T;
+    t = static_cast<int>(v / H);
+    h = static_cast<int>(v % H);
+    step_t = pl.step_t[which];
+    step_h = pl.step_h[which];
+  }
+};
+
+// ----------------------------------------------------------------- forward
+// y = r R(theta) (x g) with R(theta) g kept as four products per pair, renewed once per token.
 template <typename ST, int U, bool ADJ, int G>
-__global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const __grid_constant__ QkArgs a,
-                                                             const __grid_constant__ QkPlan pl) {
+__global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_kernel(
+    const __grid_constant__ QkArgs a, const __grid_constant__ QkPlan pl) {
   pdl_wait();
   pdl_trigger();
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ring<ST, U, 2>& ring = *reinterpret_cast<Ring<ST, U, 2>*>(smem);
   constexpr int P = 32 / G;
-  const int which = blockIdx.x < static_cast<unsigned>(pl.blocks[0]) ? 0 : 1;
-  const QkTensor& q = a.t[which];
-  const unsigned item = (blockIdx.x - (which ? pl.blocks[0] : 0)) * (blockDim.x / 32) + threadIdx.x / 32;
-  const unsigned chunks = pl.chunks[which];
-  const int t = static_cast<int>(item / chunks);
-  if (t >= a.T) return;
-  const int hn = pl.passes[which] * P, h0 = static_cast<int>(item % chunks) * hn;
-  const int h1 = min(q.H, h0 + hn);
-  const int sub = (threadIdx.x % 32) / G;
+  const Share sh(a, pl, P, threadIdx.x % 32 / G);
+  const QkTensor& q = a.t[sh.which];
   const Slot sl = slot_of<U, ADJ, G>(a);
-  const ST* x = static_cast<const ST*>(q.x) + t * q.ldx;
-  ST* y = static_cast<ST*>(q.out) + t * q.ldo;
   const ST* g = static_cast<const ST*>(q.g);
-  float c[U], s[U];
-  Run<ST, U> g0 = {}, g1 = {}, r0[kFlight] = {}, r1[kFlight] = {};
-  auto fetch = [&](int h, int f) {
-    if (h < h1 && sl.on) {
-      get(x + h * a.dh + sl.o0, r0[f]);
-      get(x + h * a.dh + sl.o1, r1[f]);
+  const bool fetch_pos = a.pos && sl.turned && sl.axis >= 0;
+  const int* pos = a.pos + static_cast<long long>(sl.axis) * a.T;
+  Walk<const ST> in(static_cast<const ST*>(q.x) + sl.o0, q.ldx, sh.t, sh.h, a.dh, q.H, sh.step_t, sh.step_h);
+  Walk<ST> out(static_cast<ST*>(q.out) + sl.o0, q.ldo, sh.t, sh.h, a.dh, q.H, sh.step_t, sh.step_h);
+  int in_h = sh.h, in_t = sh.t, h = sh.h, t = sh.t;
+  unsigned in_v = sh.v, v = sh.v;
+  int fetched = 0;
+  auto fetch = [&](int slot) {
+    if (fetched++ < sh.steps && in_v < sh.all && sl.on) {
+      ring.load(slot, 0, in.p);
+      ring.load(slot, 1, in.p + (sl.o1 - sl.o0));
+      if (fetch_pos) copy_async<4>(&ring.pos[slot][threadIdx.x], pos + in_t);
     }
+    copies_close();
+    in_v += P;
+    in_h += sh.step_h;
+    const bool wraps = in_h >= q.H;
+    if (wraps) in_h -= q.H;
+    in_t += sh.step_t + wraps;
+    in.next(wraps);
   };
 #pragma unroll
-  for (int f = 0; f < kFlight; ++f) fetch(h0 + f * P + sub, f);
-  if (g && sl.on) {
-    get(g + sl.o0, g0);
-    get(g + sl.o1, g1);
-  }
-  slot_angles<ST, U>(a, sl, t, c, s);
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+  const ST* gain = ring.fill(a, g);
+  __syncthreads();
   const float inv_dh = 1.f / static_cast<float>(a.dh);
-  for (int h = h0 + sub; h < h0 + hn; h += kFlight * P) {  // the same number of rounds for every lane
+  f2 A[U / 2], B[U / 2], C[U / 2], D[U / 2];
+  int now = -1;
+  for (int i = 0; i < sh.steps; i += kRing) {
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      float u[U], v[U];
-      unpack<U>(r0[f], u);
-      unpack<U>(r1[f], v);
-      const int hf = h + f * P;
-      fetch(hf + kFlight * P, f);
+    for (int slot = 0; slot < kRing; ++slot) {
+      if (i + slot >= sh.steps) break;  // the same for all lanes of the warp
+      fetch((slot + kAhead) % kRing);
+      copies_wait<kAhead>();
+      const bool on = v < sh.all && sl.on;
+      f2 X[U / 2], Y[U / 2];
+      ring.template read<ADJ>(slot, 0, X, Y);
+      if (on && t != now) {
+        now = t;
+        f2 gx[U / 2], gy[U / 2];
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) gx[k] = gy[k] = both(1.f);
+        if (g) get_pairs<ST, U, ADJ>(gain + sl.o0, gain + sl.o1, gx, gy);
+        if (sl.turned) {
+          f2 c[U / 2], s[U / 2];
+          slot_angles<ST, U>(a, sl, ring.turns, t, a.pos ? ring.pos[slot][threadIdx.x] : t % a.seq, c, s);
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            A[k] = gx[k] * c[k];
+            B[k] = -(gy[k] * s[k]);
+            C[k] = gx[k] * s[k];
+            D[k] = gy[k] * c[k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) A[k] = gx[k], D[k] = gy[k];
+        }
+      }
+      float r = 1.f;
       if (g) {
-        float ss = 0.f;
-        if (sl.on) {
+        f2 ss = both(0.f);
+        if (on) {
 #pragma unroll
-          for (int i = 0; i < U; ++i) ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+          for (int k = 0; k < U / 2; ++k) ss = fma2(X[k], X[k], fma2(Y[k], Y[k], ss));
         }
-        const float r = 1.f / sqrtf(group_sum<G>(ss) * inv_dh + a.eps);
+        r = rsqrtf(group_sum<G>(ss.x + ss.y) * inv_dh + a.eps);
+      }
+      if (on) {
+        const f2 r2 = both(r);
+        if (sl.turned) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          u[i] *= r * static_cast<float>(g0.v[i]);
-          v[i] *= r * static_cast<float>(g1.v[i]);
+          for (int k = 0; k < U / 2; ++k) {
+            const f2 x = X[k], y = Y[k];
+            X[k] = r2 * fma2(x, A[k], y * B[k]);
+            Y[k] = r2 * fma2(x, C[k], y * D[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) X[k] = r2 * X[k] * A[k], Y[k] = r2 * Y[k] * D[k];
         }
+        put_pairs<ST, U, ADJ>(out.p, out.p + (sl.o1 - sl.o0), X, Y);
       }
-      if (sl.turned) turn<U, ADJ, 1>(u, v, c, s);
-      if (hf < h1 && sl.on) {
-        put<U>(y + hf * a.dh + sl.o0, u);
-        put<U>(y + hf * a.dh + sl.o1, v);
-      }
+      v += P;
+      h += sh.step_h;
+      const bool wraps = h >= q.H;
+      if (wraps) h -= q.H;
+      t += sh.step_t + wraps;
+      out.next(wraps);
     }
   }
 }
 
-// A warp's items: tokens x runs of heads of one tensor, blocks[] warps apart, so its gain sums stay in registers; they
-// are added over the warp's lane groups, then over the block's warps, and each block leaves one row of partial sums.
-// The sums over a vector's channels, mean(x^2) and mean(w x), are independent of one another and reduced together.
+// ---------------------------------------------------------------- backward
+// The gain sums stay in registers over a warp's steps; they are added over the warp's lane groups, then over the
+// block's warps, and each block leaves one row of partial sums.  The sums over a vector's channels, mean(x^2) and
+// mean(w x), are independent of one another and reduced together.
 template <typename ST, int U, bool ADJ, int G>
-__global__ void __launch_bounds__(kWarps * 32, kBwdBlocks<ST, U>) qk_bwd_kernel(const __grid_constant__ QkArgs a,
-                                                                                const __grid_constant__ QkPlan pl) {
+__global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_kernel(
+    const __grid_constant__ QkArgs a, const __grid_constant__ QkPlan pl) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float4 sums4[];
-  float* sums = reinterpret_cast<float*>(sums4);  // [warps][dh]
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ring<ST, U, 4>& ring = *reinterpret_cast<Ring<ST, U, 4>*>(smem);
   constexpr int P = 32 / G;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-  const int which = blockIdx.x < static_cast<unsigned>(pl.blocks[0]) ? 0 : 1;
-  const QkTensor& q = a.t[which];
-  const unsigned block = blockIdx.x - (which ? pl.blocks[0] : 0);
-  const unsigned chunks = pl.chunks[which], items = chunks * a.T;
-  const int hn = pl.passes[which] * P, sub = (threadIdx.x % 32) / G;
+  const int sub = threadIdx.x % 32 / G;
+  const Share sh(a, pl, P, sub);
+  const QkTensor& q = a.t[sh.which];
   const Slot sl = slot_of<U, ADJ, G>(a);
   const ST* g = static_cast<const ST*>(q.g);
+  const bool fetch_pos = a.pos && sl.turned && sl.axis >= 0;
+  const int* pos = a.pos + static_cast<long long>(sl.axis) * a.T;
+  Walk<const ST> in(static_cast<const ST*>(q.dy) + sl.o0, q.lddy, sh.t, sh.h, a.dh, q.H, sh.step_t, sh.step_h);
+  Walk<const ST> in_x(static_cast<const ST*>(q.x) + sl.o0, q.ldx, sh.t, sh.h, a.dh, q.H, sh.step_t, sh.step_h);
+  Walk<ST> out(static_cast<ST*>(q.out) + sl.o0, q.ldo, sh.t, sh.h, a.dh, q.H, sh.step_t, sh.step_h);
+  int in_h = sh.h, in_t = sh.t, h = sh.h, t = sh.t;
+  unsigned in_v = sh.v, v = sh.v;
+  int fetched = 0;
+  auto fetch = [&](int slot) {
+    if (fetched++ < sh.steps && in_v < sh.all && sl.on) {
+      ring.load(slot, 0, in.p);
+      ring.load(slot, 1, in.p + (sl.o1 - sl.o0));
+      if (g) {
+        ring.load(slot, 2, in_x.p);
+        ring.load(slot, 3, in_x.p + (sl.o1 - sl.o0));
+      }
+      if (fetch_pos) copy_async<4>(&ring.pos[slot][threadIdx.x], pos + in_t);
+    }
+    copies_close();
+    in_v += P;
+    in_h += sh.step_h;
+    const bool wraps = in_h >= q.H;
+    if (wraps) in_h -= q.H;
+    in_t += sh.step_t + wraps;
+    in.next(wraps);
+    in_x.next(wraps);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(i);
+  const ST* gain = ring.fill(a, g);
+  __syncthreads();
   const float inv_dh = 1.f / static_cast<float>(a.dh);
-  Run<ST, U> g0 = {}, g1 = {};
-  float d0[U], d1[U];
+  f2 gx[U / 2], gy[U / 2], dgx[U / 2], dgy[U / 2], c[U / 2], s[U / 2];
 #pragma unroll
-  for (int i = 0; i < U; ++i) d0[i] = d1[i] = 0.f;
-  if (g && sl.on) {
-    get(g + sl.o0, g0);
-    get(g + sl.o1, g1);
-  }
-  for (unsigned item = block * warps + warp; item < items; item += pl.blocks[which] * warps) {
-    const int t = static_cast<int>(item / chunks);
-    const int h0 = static_cast<int>(item % chunks) * hn;
-    const int h1 = min(q.H, h0 + hn);
-    const ST* x = static_cast<const ST*>(q.x) + t * q.ldx;
-    const ST* dy = static_cast<const ST*>(q.dy) + t * q.lddy;
-    ST* dx = static_cast<ST*>(q.out) + t * q.ldo;
-    float c[U], s[U];
-    Run<ST, U> x0[kFlight] = {}, x1[kFlight] = {}, y0[kFlight] = {}, y1[kFlight] = {};
-    auto fetch = [&](int h, int f) {
-      if (h < h1 && sl.on) {
-        get(dy + h * a.dh + sl.o0, y0[f]);
-        get(dy + h * a.dh + sl.o1, y1[f]);
-        if (g) {
-          get(x + h * a.dh + sl.o0, x0[f]);
-          get(x + h * a.dh + sl.o1, x1[f]);
+  for (int k = 0; k < U / 2; ++k) gx[k] = gy[k] = both(1.f), dgx[k] = dgy[k] = both(0.f);
+  if (g && sl.on) get_pairs<ST, U, ADJ>(gain + sl.o0, gain + sl.o1, gx, gy);
+  int now = -1;
+  for (int i = 0; i < sh.steps; i += kRing) {
+#pragma unroll
+    for (int slot = 0; slot < kRing; ++slot) {
+      if (i + slot >= sh.steps) break;  // the same for all lanes of the warp
+      fetch((slot + kAhead) % kRing);
+      copies_wait<kAhead>();
+      const bool on = v < sh.all && sl.on;
+      f2 U0[U / 2], V0[U / 2];  // dn
+      ring.template read<ADJ>(slot, 0, U0, V0);
+      if (sl.turned && v < sh.all) {
+        if (t != now) {
+          now = t;
+          slot_angles<ST, U>(a, sl, ring.turns, t, a.pos ? ring.pos[slot][threadIdx.x] : t % a.seq, c, s);
+        }
+#pragma unroll
+        for (int k = 0; k < U / 2; ++k) {
+          const f2 x = U0[k], y = V0[k];
+          U0[k] = fma2(x, c[k], y * s[k]);
+          V0[k] = fma2(-x, s[k], y * c[k]);
         }
       }
-    };
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f) fetch(h0 + f * P + sub, f);
-    slot_angles<ST, U>(a, sl, t, c, s);
-    for (int h = h0 + sub; h < h0 + hn; h += kFlight * P) {
-#pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        const int hf = h + f * P;
-        const bool on = hf < h1 && sl.on;
-        float u[U], v[U], p[U], w[U];
-        unpack<U>(y0[f], u);
-        unpack<U>(y1[f], v);
-        unpack<U>(x0[f], p);
-        unpack<U>(x1[f], w);
-        fetch(hf + kFlight * P, f);
-        if (sl.turned) turn<U, ADJ, -1>(u, v, c, s);
-        if (g) {
-          float ss = 0.f, dot = 0.f;
-          if (on) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-              ss = fmaf(p[i], p[i], fmaf(w[i], w[i], ss));
-              dot = fmaf(u[i] * static_cast<float>(g0.v[i]), p[i],
-                         fmaf(v[i] * static_cast<float>(g1.v[i]), w[i], dot));
-            }
-          }
-          ss = group_sum<G>(ss);
-          dot = group_sum<G>(dot);
-          const float r = 1.f / sqrtf(ss * inv_dh + a.eps);
-          const float m = dot * inv_dh * r * r;
-          if (on) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-              d0[i] = fmaf(u[i], p[i] * r, d0[i]);
-              d1[i] = fmaf(v[i], w[i] * r, d1[i]);
-              u[i] = r * (u[i] * static_cast<float>(g0.v[i]) - p[i] * m);
-              v[i] = r * (v[i] * static_cast<float>(g1.v[i]) - w[i] * m);
-            }
-          }
-        }
+      if (g) {
+        f2 X[U / 2], Y[U / 2], ss = both(0.f), dot = both(0.f);
+        ring.template read<ADJ>(slot, 2, X, Y);
         if (on) {
-          put<U>(dx + hf * a.dh + sl.o0, u);
-          put<U>(dx + hf * a.dh + sl.o1, v);
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            ss = fma2(X[k], X[k], fma2(Y[k], Y[k], ss));
+            dot = fma2(U0[k] * gx[k], X[k], fma2(V0[k] * gy[k], Y[k], dot));
+          }
+        }
+        const float sum = group_sum<G>(ss.x + ss.y), wx = group_sum<G>(dot.x + dot.y);
+        const float r = rsqrtf(sum * inv_dh + a.eps);
+        const f2 r2 = both(r), m = both(-wx * inv_dh * r);
+        if (on) {
+#pragma unroll
+          for (int k = 0; k < U / 2; ++k) {
+            X[k] = X[k] * r2;
+            Y[k] = Y[k] * r2;
+            dgx[k] = fma2(U0[k], X[k], dgx[k]);
+            dgy[k] = fma2(V0[k], Y[k], dgy[k]);
+            U0[k] = r2 * fma2(X[k], m, U0[k] * gx[k]);
+            V0[k] = r2 * fma2(Y[k], m, V0[k] * gy[k]);
+          }
         }
       }
+      if (on) put_pairs<ST, U, ADJ>(out.p, out.p + (sl.o1 - sl.o0), U0, V0);
+      v += P;
+      h += sh.step_h;
+      const bool wraps = h >= q.H;
+      if (wraps) h -= q.H;
+      t += sh.step_t + wraps;
+      out.next(wraps);
     }
   }
   if (!g) return;
+  copies_wait<0>();
+  __syncthreads();  // the ring's memory takes the warps' sums
+  float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int k = 0; k < U / 2; ++k) {
 #pragma unroll
     for (int o = G; o < 32; o <<= 1) {
-      d0[i] += __shfl_xor_sync(0xffffffffu, d0[i], o);
-      d1[i] += __shfl_xor_sync(0xffffffffu, d1[i], o);
+      dgx[k].x += __shfl_xor_sync(0xffffffffu, dgx[k].x, o);
+      dgx[k].y += __shfl_xor_sync(0xffffffffu, dgx[k].y, o);
+      dgy[k].x += __shfl_xor_sync(0xffffffffu, dgy[k].x, o);
+      dgy[k].y += __shfl_xor_sync(0xffffffffu, dgy[k].y, o);
     }
   }
   if (sub == 0 && sl.on) {
-    put<U>(sums + warp * a.dh + sl.o0, d0);
-    put<U>(sums + warp * a.dh + sl.o1, d1);
+    float* mine = sums + threadIdx.x / 32 * a.dh;
+    put_pairs<float, U, ADJ>(mine + sl.o0, mine + sl.o1, dgx, dgy);
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < a.dh; c += blockDim.x) {
-    float v = 0.f;
-    for (int w = 0; w < warps; ++w) v += sums[w * a.dh + c];
-    q.part[static_cast<long long>(block) * a.dh + c] = v;
+  for (int ch = threadIdx.x; ch < a.dh; ch += kThreads) {
+    float sum = 0.f;
+    for (int w = 0; w < kWarps; ++w) sum += sums[w * a.dh + ch];
+    q.part[static_cast<long long>(sh.block) * a.dh + ch] = sum;
   }
 }
 
@@ -323,21 +549,20 @@ static QkVariant variant(const QkArgs& a, size_t es) {
 
 static int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
-// How the heads of each tensor are cut: as many passes to a warp as leave `warps` of them, so that angles and gains
-// are reused; never more than 64 runs a token (tokens x runs stay below 2^30).
-static void cut_heads(const QkArgs& a, int g, long long warps, QkPlan* pl) {
-  long long all = 0;
-  int full[2];
+// Blocks of each tensor by its share of the steps, at most as many as the SMs hold at once, and the steps of a warp.
+static void cut(const QkArgs& a, int g, int resident, int most, QkPlan* pl) {
+  const int P = 32 / g;
+  long long steps[2];
+  for (int i = 0; i < 2; ++i) steps[i] = (1LL * a.T * a.t[i].H + P - 1) / P;
   for (int i = 0; i < 2; ++i) {
-    full[i] = cdiv(a.t[i].H, 32 / g);
-    all += 1LL * a.T * full[i];
-  }
-  const long long n = all / warps;
-  for (int i = 0; i < 2; ++i) {
-    int passes = static_cast<int>(n < 1 ? 1 : n < full[i] ? n : full[i]);
-    if (passes < cdiv(full[i], 64)) passes = cdiv(full[i], 64);
-    pl->chunks[i] = full[i] ? cdiv(full[i], passes) : 0;
-    pl->passes[i] = full[i] ? cdiv(full[i], pl->chunks[i]) : 0;
+    const int H = a.t[i].H;
+    long long n = (steps[i] * resident + (steps[0] + steps[1]) / 2) / (steps[0] + steps[1]);
+    n = std::min(std::min(std::max(n, 1LL), static_cast<long long>(most)), (steps[i] + kWarps - 1) / kWarps);
+    pl->blocks[i] = static_cast<int>(n);
+    pl->steps[i] = n ? static_cast<unsigned>(steps[i] / (n * kWarps)) : 0;
+    pl->more[i] = n ? static_cast<unsigned>(steps[i] % (n * kWarps)) : 0;
+    pl->step_t[i] = H ? P / H : 0;
+    pl->step_h[i] = H ? P % H : 0;
   }
 }
 
@@ -364,38 +589,30 @@ static QkKernel pick(bool bwd, bool adj, QkVariant v) {
   return adj ? pick_g<ST, 4, true>(bwd, v.g) : pick_g<ST, 4, false>(bwd, v.g);
 }
 
+static cudaError_t launch(QkKernel kern, const QkArgs& a, const QkPlan& pl, size_t smem, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(pl.blocks[0] + pl.blocks[1]), dim3(kThreads), smem, st, a, pl);
+}
+
 template <typename ST>
 cudaError_t launch_qk_fwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st) {
   const QkVariant v = variant(a, sizeof(ST));
   QkPlan pl;
-  cut_heads(a, v.g, sms * 32LL, &pl);
-  const long long items = 1LL * a.T * (pl.chunks[0] + pl.chunks[1]);
-  const int warps = items >= sms * 8LL * kWarps ? kWarps : items >= sms * 8LL ? 4 : 1;
-  for (int i = 0; i < 2; ++i) pl.blocks[i] = cdiv(1LL * a.T * pl.chunks[i], warps);
-  return launch_pdl(pick<ST>(false, adjacent, v), dim3(pl.blocks[0] + pl.blocks[1]), dim3(32 * warps), 0, st, a, pl);
+  cut(a, v.g, sms * fwd_blocks(v.u, sizeof(ST)), 1 << 30, &pl);
+  return launch(pick<ST>(false, adjacent, v), a, pl, v.u == 8 ? Ring<ST, 8, 2>::bytes(a) : Ring<ST, 4, 2>::bytes(a), st);
 }
 
 template <typename ST>
 cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st) {
   const QkVariant v = variant(a, sizeof(ST));
   QkPlan pl;
-  cut_heads(a, v.g, sms * 16LL, &pl);
-  long long passes[2], items[2];
-  for (int i = 0; i < 2; ++i) {
-    items[i] = 1LL * a.T * pl.chunks[i];
-    passes[i] = items[i] * pl.passes[i];
-  }
-  const int warps = items[0] + items[1] >= sms * 2LL * kWarps ? kWarps : 2;
-  // two blocks an SM, shared between the tensors by their work
-  const int room = sms * 2;
-  for (int i = 0; i < 2; ++i) {
-    long long n = (passes[i] * room + (passes[0] + passes[1]) / 2) / (passes[0] + passes[1]);
-    if (n < 1) n = 1;
-    if (n > cdiv(items[i], warps)) n = cdiv(items[i], warps);
-    pl.blocks[i] = static_cast<int>(n < kQkMaxParts ? n : kQkMaxParts);
-  }
-  cudaError_t e = launch_pdl(pick<ST>(true, adjacent, v), dim3(pl.blocks[0] + pl.blocks[1]), dim3(32 * warps),
-                             sizeof(float) * warps * a.dh, st, a, pl);
+  cut(a, v.g, sms * bwd_blocks(v.u, sizeof(ST)), kQkMaxParts, &pl);
+  const cudaError_t e =
+      launch(pick<ST>(true, adjacent, v), a, pl, v.u == 8 ? Ring<ST, 8, 4>::bytes(a) : Ring<ST, 4, 4>::bytes(a), st);
   if (e != cudaSuccess || (!a.t[0].g && !a.t[1].g)) return e;
   return launch_pdl(qk_dg_kernel, dim3(cdiv(a.dh, 32), 2), dim3(32, 32), 0, st, a, pl);
 }

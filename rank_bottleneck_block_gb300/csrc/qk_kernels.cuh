@@ -37,9 +37,11 @@ struct QkArgs {
   float eps;
 };
 
-// How a launch cuts its work: blocks of q, then of k; each token's heads in `chunks` runs of `passes` passes.
+// How a launch cuts its work, for q and for k: blocks, the steps of a warp (one step: 32 / G vectors; the first `more`
+// warps take one more), and how far a step moves the token and the head.
 struct QkPlan {
-  int blocks[2], chunks[2], passes[2];
+  int blocks[2], step_t[2], step_h[2];
+  unsigned steps[2], more[2];
 };
 
 // adjacent: pairs are channels (2p, 2p + 1), else (p, p + rot / 2).

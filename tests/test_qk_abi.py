@@ -89,6 +89,13 @@ def test_shapes_are_refused(L, over, status):
     assert L.lr_qk_bwd_workspace_bytes(1, 16, sh) == 0
 
 
+def test_too_many_vectors_are_refused(L):
+    sh = _shape(L, Hq=64, Hk=1)  # 2^24 tokens of 64 heads: 2^30 vectors are the most
+    assert L.lr_qk_bwd_workspace_bytes(1, 1 << 24, sh) > 0
+    sh.Hq = 65
+    assert L.lr_qk_bwd_workspace_bytes(1, 1 << 24, sh) == 0
+
+
 def test_axes_are_refused(L):
     sh = _shape(L)
     for axes in (0, 5, -1):
