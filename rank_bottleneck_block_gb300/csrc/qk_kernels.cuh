@@ -15,7 +15,7 @@
 namespace lr {
 
 constexpr int kQkMaxAxes = 4;
-constexpr int kQkMaxParts = 1024;  // blocks per tensor that write a partial of dg
+constexpr int kQkMaxParts = 4096;  // blocks per tensor that write a partial of dg
 
 struct QkTensor {
   const void* x;   // [T, ldx], head h in columns h*dh .. h*dh + dh - 1 (may be null in a backward without norm)
@@ -37,11 +37,9 @@ struct QkArgs {
   float eps;
 };
 
-// How a launch cuts its work, for q and for k: blocks, the steps of a warp (one step: 32 / G vectors; the first `more`
-// warps take one more), and how far a step moves the token and the head.
+// How a launch cuts its work, for q and for k: blocks, and each token's heads into `chunks` items of `len` heads.
 struct QkPlan {
-  int blocks[2], step_t[2], step_h[2];
-  unsigned steps[2], more[2];
+  int blocks[2], chunks[2], len[2];
 };
 
 // adjacent: pairs are channels (2p, 2p + 1), else (p, p + rot / 2).
