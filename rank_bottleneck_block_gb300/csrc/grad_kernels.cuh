@@ -8,29 +8,39 @@
 
 namespace lr {
 
-constexpr int kGradTable = 1024;  // tensors of one launch
-constexpr int kGradChunk = 8192;  // elements one block takes at a time
-constexpr int kGradParts = 1216;  // most blocks of one launch, each writing one partial sum
+constexpr int kGradTable = 1024;  // most tensors of one launch
+constexpr int kGradChunk = 8192;  // elements a block takes at a time (32 a thread)
+constexpr int kGradParts = 4096;  // most blocks of one launch, each writing one partial sum
+constexpr int kGradFew = 512;     // partial sums that the scaling blocks add up themselves
 
 // The tensors of one launch, passed by value with it (no host-to-device copy, so a call can be captured).
-// Tensor i is cut into chunks first[i] .. first[i + 1] - 1.
+// Tensor i is cut into chunks first[i] .. first[i + 1] - 1; a block takes `each` consecutive ones.
 template <int N>
 struct GradTable {
   const void* src[N];
   void* dst[N];
   long long numel[N];
   int first[N + 1];
-  int n;
+  int n, each;
 };
 
-// part[0 .. blocks - 1]: sums of squares in fp64.  blocks = grad_blocks(chunks).
-int grad_blocks(int chunks);
+// What becomes of the sums: norm -> stat[0], scale -> stat[1] unless it has only been asked for the norm.
+struct GradStat {
+  const double* part;  // nparts partial sums, or nparts = 0: stat already holds the results
+  int nparts;
+  float max_norm;
+  float* stat;
+  bool norm_only;
+};
+
+// part[0 .. blocks - 1]: sums of squares in fp64, one for every `each` chunks.
+inline int grad_blocks(int chunks, int each) { return (chunks + each - 1) / each; }
 template <typename ST, int N>
 cudaError_t launch_grad_sumsq(const GradTable<N>& tab, double* part, cudaStream_t st);
-// norm and scale from the nparts partials: stat[0] = norm if write_stat > 0, stat[1] = scale if write_stat > 1;
-// then the tensors of `tab` scaled (none if tab.n == 0).
+// norm and scale from any number of partial sums, by one block.
+cudaError_t launch_grad_stat(const GradStat& gs, cudaStream_t st);
+// The tensors scaled; with gs.nparts > 0 every block first adds the partial sums up, and the first writes stat.
 template <typename ST, int N>
-cudaError_t launch_grad_scale(const GradTable<N>& tab, const double* part, int nparts, float max_norm, float* stat,
-                              int write_stat, cudaStream_t st);
+cudaError_t launch_grad_scale(const GradTable<N>& tab, const GradStat& gs, bool in_place, cudaStream_t st);
 
 }  // namespace lr

@@ -1537,65 +1537,86 @@ static lr_status qk_bwd_impl(const Ctx& c, const lr_qk_shape& sh, QkArgs& a, voi
 }
 
 // ============================================================ gradient norm and clipping
+// The workspace holds the launches' partial sums one after the other.
 static size_t grad_ws_bytes(int n) {
   const size_t launches = n > 0 ? (static_cast<size_t>(n) + kGradTable - 1) / kGradTable : 1;
   return launches * kGradParts * sizeof(double);
 }
 
-// Tensors i0 .. i0 + k - 1 as one launch's table; false if its chunks exceed an int.
+static long long grad_chunks(const long long* numel, int n) {
+  long long chunks = 0;
+  for (int i = 0; i < n; ++i) chunks += (numel[i] + kGradChunk - 1) / kGradChunk;
+  return chunks;
+}
+
 template <int N>
-static bool grad_table(int i0, int k, const void* const* grads, const long long* numel, void* const* outs,
+static void grad_table(const void* const* grads, const long long* numel, void* const* outs, int n, int chunks,
                        GradTable<N>* t) {
-  long long first = 0;
-  for (int i = 0; i < k; ++i) {
-    t->src[i] = grads[i0 + i];
-    t->dst[i] = outs ? outs[i0 + i] : nullptr;
-    t->numel[i] = numel[i0 + i];
-    t->first[i] = static_cast<int>(first);
-    first += (numel[i0 + i] + kGradChunk - 1) / kGradChunk;
-    if (first > 0x7fffffffLL) return false;
+  int first = 0;
+  for (int i = 0; i < n; ++i) {
+    t->src[i] = grads[i];
+    t->dst[i] = outs ? outs[i] : nullptr;
+    t->numel[i] = numel[i];
+    t->first[i] = first;
+    first += static_cast<int>((numel[i] + kGradChunk - 1) / kGradChunk);
   }
-  t->first[k] = static_cast<int>(first);
-  t->n = k;
-  return true;
+  t->first[n] = first;
+  t->n = n;
+  t->each = (chunks + kGradParts - 1) / kGradParts;
+}
+
+// One launch list: at most N tensors (the launch carries their table, so a short list takes a small one).
+template <typename ST, int N>
+static lr_status grad_lists(const Ctx& c, int n, const void* const* grads, const long long* numel, float max_norm,
+                            void* const* outs, float* stat, double* part) {
+  GradTable<N> tab;
+  GradStat gs{part, 0, max_norm, stat, outs == nullptr};
+  auto elems = [&](int i0, int k) {
+    double e = 0.0;
+    for (int i = i0; i < i0 + k; ++i) e += static_cast<double>(numel[i]);
+    return e;
+  };
+  bool in_place = outs != nullptr;
+  for (int i = 0; in_place && i < n; ++i) in_place = numel[i] == 0 || outs[i] == grads[i];
+  for (int i0 = 0; i0 < n; i0 += N) {
+    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k));
+    if (chunks == 0) continue;
+    grad_table(grads + i0, numel + i0, outs ? outs + i0 : nullptr, k, chunks, &tab);
+    LaunchScope scope("grad_sumsq", c.st, 0, c.es * elems(i0, k));
+    cudaError_t e = launch_grad_sumsq<ST>(tab, part + gs.nparts, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
+    gs.nparts += grad_blocks(chunks, tab.each);
+  }
+  // The blocks that scale add a few partial sums up themselves; many are added up by a launch of their own.
+  if (!outs || gs.nparts == 0 || gs.nparts > kGradFew || n > N) {
+    if (gs.nparts == 0) {  // no elements: one partial sum of zero
+      cudaError_t e = cudaMemsetAsync(part, 0, sizeof(double), c.st);
+      if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
+      gs.nparts = 1;
+    }
+    LaunchScope scope("grad_stat", c.st, 0, 8.0 * gs.nparts);
+    cudaError_t e = launch_grad_stat(gs, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
+    gs.nparts = 0;
+  }
+  if (!outs) return LR_OK;
+  for (int i0 = 0; i0 < n; i0 += N) {
+    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k));
+    if (chunks == 0) continue;
+    if (n > N) grad_table(grads + i0, numel + i0, outs + i0, k, chunks, &tab);
+    LaunchScope scope("grad_scale", c.st, 0, 2.0 * c.es * elems(i0, k));
+    cudaError_t e = launch_grad_scale<ST>(tab, gs, in_place, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient clipping: %s", cudaGetErrorString(e));
+  }
+  return LR_OK;
 }
 
 template <typename ST>
 static lr_status grad_impl(const Ctx& c, int n, const void* const* grads, const long long* numel, float max_norm,
                            void* const* outs, float* stat, double* part) {
-  GradTable<kGradTable> tab;
-  int nparts = 0;
-  double elems = 0.0;
-  for (int i = 0; i < n; ++i) elems += static_cast<double>(numel[i]);
-  for (int i0 = 0; i0 < n; i0 += kGradTable) {  // every list checked before the first launch
-    if (!grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab))
-      return fail(LR_ERR_SHAPE, "gradient tensors %d..: too many elements", i0);
-  }
-  for (int i0 = 0; i0 < n; i0 += kGradTable) {
-    grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab);
-    const int chunks = tab.first[tab.n];
-    if (chunks == 0) continue;
-    LaunchScope scope("grad_sumsq", c.st, 0, c.es * elems);
-    cudaError_t e = launch_grad_sumsq<ST>(tab, part + nparts, c.st);
-    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
-    nparts += grad_blocks(chunks);
-  }
-  bool stat_due = true;
-  for (int i0 = 0; i0 < n || stat_due; i0 += kGradTable) {
-    if (outs && i0 < n) {
-      grad_table(i0, std::min(kGradTable, n - i0), grads, numel, outs, &tab);
-    } else {
-      tab.n = 0;
-      tab.first[0] = 0;
-    }
-    if (tab.first[tab.n] == 0 && !stat_due) continue;
-    LaunchScope scope("grad_scale", c.st, 0, outs ? 2.0 * c.es * elems : 0.0);
-    cudaError_t e = launch_grad_scale<ST>(tab, part, nparts, max_norm, stat, !stat_due ? 0 : outs ? 2 : 1, c.st);
-    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient clipping: %s", cudaGetErrorString(e));
-    stat_due = false;
-    if (!outs) break;
-  }
-  return LR_OK;
+  if (n <= 16) return grad_lists<ST, 16>(c, n, grads, numel, max_norm, outs, stat, part);
+  if (n <= 256) return grad_lists<ST, 256>(c, n, grads, numel, max_norm, outs, stat, part);
+  return grad_lists<ST, kGradTable>(c, n, grads, numel, max_norm, outs, stat, part);
 }
 
 // ============================================================ block stack
@@ -2359,6 +2380,9 @@ static lr_status check_grads(lr_dtype dt, int n, const void* const* grads, const
     LR_TRY(check_ptr(grads[i], "grads[i]"));
     if (clip) LR_TRY(check_ptr(outs[i], "outs[i]"));
   }
+  for (int i = 0; i < n; i += kGradTable)  // chunks of a launch are counted in int
+    if (grad_chunks(numel + i, std::min(kGradTable, n - i)) > (1LL << 30))
+      return fail(LR_ERR_SHAPE, "tensors %d..: too many elements", i);
   LR_TRY(check_ptr(stat, "stat"));
   LR_TRY(check_ptr(ws, "ws"));
   return check_size(ws_bytes, grad_ws_bytes(n), "ws");

@@ -4,8 +4,8 @@
 namespace lr {
 
 // ---------------------------------------------------------------- backward
-// The gain sums stay in registers over a warp's steps; they are added over the warp's lane groups, then over the
-// block's warps, and each block leaves one row of partial sums.  The sums over a vector's channels, mean(x^2) and
+// The gain sums stay in registers over a warp's steps; they are added over the block's lane groups, and each
+// block leaves one row of partial sums.  The sums over a vector's channels, mean(x^2) and
 // mean(w x), are independent of one another and reduced together.
 template <typename ST, int U, bool ADJ, int G, bool FULL>
 __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_kernel(
@@ -112,25 +112,14 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_ke
   }
   if (!g) return;
   copies_wait<0>();
-  __syncthreads();  // the ring's memory takes the warps' sums
+  __syncthreads();  // the ring's memory takes the lane groups' sums, 512 floats a warp at most
   float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int k = 0; k < U / 2; ++k) {
-#pragma unroll
-    for (int o = G; o < 32; o <<= 1) {
-      dgx[k].x += __shfl_xor_sync(0xffffffffu, dgx[k].x, o);
-      dgx[k].y += __shfl_xor_sync(0xffffffffu, dgx[k].y, o);
-      dgy[k].x += __shfl_xor_sync(0xffffffffu, dgy[k].x, o);
-      dgy[k].y += __shfl_xor_sync(0xffffffffu, dgy[k].y, o);
-    }
-  }
-  if (sub == 0 && sl.on) {
-    // X and Y as floats at the channels they came from
-    float* mine = sums + threadIdx.x / 32 * a.dh;
+  constexpr int P = 32 / G, N = U / kPieces<ST, U>;
+  if (sl.on) {  // X and Y at the channels they came from
+    float* mine = sums + (threadIdx.x / 32 * P + sub) * a.dh;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      constexpr int N = U / kPieces<ST, U>;
-      const int x = ADJ ? 2 * i : i, y = ADJ ? 2 * i + 1 : U + i;  // places in the slot's 2 U channels
+      const int x = ADJ ? 2 * i : i, y = ADJ ? 2 * i + 1 : U + i;  // places among the slot's 2 U channels
       mine[sl.o + x / U * sl.apart + x % U / N * sl.hop + x % N] = i % 2 ? dgx[i / 2].y : dgx[i / 2].x;
       mine[sl.o + y / U * sl.apart + y % U / N * sl.hop + y % N] = i % 2 ? dgy[i / 2].y : dgy[i / 2].x;
     }
@@ -138,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_ke
   __syncthreads();
   for (int ch = threadIdx.x; ch < a.dh; ch += kThreads) {
     float sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) sum += sums[w * a.dh + ch];
+#pragma unroll 4
+    for (int w = 0; w < kWarps * P; ++w) sum += sums[w * a.dh + ch];
     q.part[static_cast<long long>(sh.block) * a.dh + ch] = sum;
   }
 }
@@ -173,7 +163,9 @@ static QkKernel pick_g(int g) {
     return qk_bwd_kernel<ST, U, ADJ, 32, FULL>;
   } else {
     if (sizeof(ST) == 2 && g == 4) return qk_bwd_kernel<ST, U, ADJ, sizeof(ST) == 2 ? 4 : 8, FULL>;
+    if (g == 5) return qk_bwd_kernel<ST, U, ADJ, 5, FULL>;
     if (g == 8) return qk_bwd_kernel<ST, U, ADJ, 8, FULL>;
+    if (g == 10) return qk_bwd_kernel<ST, U, ADJ, 10, FULL>;
     return g == 16 ? qk_bwd_kernel<ST, U, ADJ, 16, FULL> : qk_bwd_kernel<ST, U, ADJ, 32, FULL>;
   }
 }

@@ -80,9 +80,9 @@ __device__ __forceinline__ int pair_of(const Slot& s, int i) {
 template <typename ST, int U, bool ADJ, int G, bool FULL>
 __device__ __forceinline__ Slot slot_of(const QkArgs& a) {
   constexpr int N = U / kPieces<ST, U>;
-  const int j = threadIdx.x % G, n = a.rot / (2 * U);
+  const int j = threadIdx.x % 32 % G, n = a.rot / (2 * U);
   Slot s;
-  s.on = j < a.dh / (2 * U);
+  s.on = j < a.dh / (2 * U) && threadIdx.x % 32 < 32 / G * G;  // lanes past the last group have nothing to do
   s.turned = FULL ? s.on : s.on && j < n;
   const int all = s.turned ? a.rot : a.dh - a.rot;
   s.o = s.turned ? N * j : a.rot + N * (j - n);
@@ -220,11 +220,21 @@ __device__ __forceinline__ void slot_angles(const QkArgs& a, const Slot& sl, con
   }
 }
 
+// Sum over the lane's group, the same bits in each of its lanes.
 template <int G>
 __device__ __forceinline__ float group_sum(float v) {
+  if constexpr ((G & (G - 1)) == 0) {
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  } else {  // 5 or 10 lanes: opposite ones, then the group's first five in order
+    const int lane = threadIdx.x % 32, first = lane / G * G;
+    if constexpr (G == 10) v += __shfl_sync(0xffffffffu, v, first + (lane - first + 5) % 10);
+    float sum = __shfl_sync(0xffffffffu, v, first);
+#pragma unroll
+    for (int i = 1; i < 5; ++i) sum += __shfl_sync(0xffffffffu, v, first + i);
+    return sum;
+  }
 }
 
 // ---------------------------------------------------------------- the ring
@@ -342,13 +352,14 @@ struct QkVariant {
 inline QkVariant variant(const QkArgs& a, size_t es) {
   const bool wide = a.dh % 16 == 0 && a.rot % 16 == 0 && (es == 2 || a.dh > 256);
   const int u = wide ? 8 : 4, slots = a.dh / (2 * u);
+  if (slots == 5 || slots == 9 || slots == 10) return {u, slots == 5 ? 5 : 10};  // 6 and 3 vectors a warp, not 4 and 2
   return {u, slots <= 4 && es == 2 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32};
 }
 
 inline int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 constexpr int kMostHeads = 16;  // of an item: past it the angles cost nothing any more
-constexpr int kWaveSteps = 20;  // heads a lane group takes at least, where the launch has more blocks than run at once
+constexpr int kWaveSteps = 10;  // heads a lane group takes at least, where the launch has more blocks than run at once
 
 // Cuts each token's heads into items, and gives each tensor blocks by its share of the vectors.  Small launches: one
 // item a lane group, as short as fills the SMs.  Large ones: up to four blocks for each that runs at once, since SMs

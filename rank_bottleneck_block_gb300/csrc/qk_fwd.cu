@@ -100,7 +100,9 @@ static QkKernel pick_g(int g) {
     return qk_fwd_kernel<ST, U, ADJ, 32, FULL>;
   } else {
     if (sizeof(ST) == 2 && g == 4) return qk_fwd_kernel<ST, U, ADJ, sizeof(ST) == 2 ? 4 : 8, FULL>;
+    if (g == 5) return qk_fwd_kernel<ST, U, ADJ, 5, FULL>;
     if (g == 8) return qk_fwd_kernel<ST, U, ADJ, 8, FULL>;
+    if (g == 10) return qk_fwd_kernel<ST, U, ADJ, 10, FULL>;
     return g == 16 ? qk_fwd_kernel<ST, U, ADJ, 16, FULL> : qk_fwd_kernel<ST, U, ADJ, 32, FULL>;
   }
 }

@@ -163,11 +163,26 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+def _raw_stream():
+    """The function that names a device's current stream, without making a Stream object where torch has one."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_current = None
+
+
 def _stream(stream) -> Optional[int]:
+    global _current
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        if _current is None:
+            torch.cuda.init()
+            _current = (torch.cuda.current_device, _raw_stream())
+        return _current[1](_current[0]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -194,6 +209,29 @@ def pair(A, B) -> lr_pair:
 
 def pair_grad(dA, dB) -> lr_pair_grad:
     return lr_pair_grad(_p(dA), _p(dB))
+
+
+class Prepared:
+    """An entry point with every argument but the stream converted once, for callers that repeat a call on the
+    same buffers: call(stream).  It keeps its arguments, so the tensors whose pointers it holds stay alive."""
+
+    def __init__(self, name: str, *args):
+        self._fn, self._keep = getattr(lib(), name), args
+        types = _SIGS[name][1][:-1]
+        if len(types) != len(args):
+            raise TypeError(f"{name}: {len(args)} arguments, {len(types)} needed before the stream")
+        self._args = tuple(_typed(t, a) for t, a in zip(types, args))
+
+    def __call__(self, stream=None) -> None:
+        status = self._fn(*self._args, _stream(stream))
+        if status:
+            _check(status)
+
+
+def _typed(ctype, a):
+    if a is None or isinstance(a, (ctypes.Array, ctypes.Structure)) or isinstance(a, ctypes._Pointer):
+        return a
+    return ctype(_p(a) if ctype is _P else a)
 
 
 # ---------------------------------------------------------- entry points

@@ -72,14 +72,23 @@ class GradClip:
         self.stat = torch.zeros(2, dtype=torch.float32, device=first.device)
         self.norm, self.scale = self.stat[:1], self.stat[1:]
         self.ws = _buf(L.lr_grad_workspace_bytes(len(self.grads)), first.device)
+        self._made = None  # the last call's arguments, converted
 
     def measure(self, stream=None) -> torch.Tensor:
-        L.lr_grad_norm(self.dt, self._g, self._n, self.stat, self.ws, stream)
+        self._call("lr_grad_norm", stream)
         return self.norm
 
     def clip(self, stream=None) -> torch.Tensor:
-        L.lr_grad_clip(self.dt, self._g, self._n, self.max_norm, self._o, self.stat, self.ws, stream)
+        self._call("lr_grad_clip", stream)
         return self.norm
+
+    def _call(self, name, stream):
+        key = (name, self.max_norm, self.ws)
+        if self._made is None or self._made[0] != key[0] or self._made[1] != key[1] or self._made[2] is not key[2]:
+            args = (self.dt, len(self.grads), self._g, self._n)
+            args += (self.max_norm, self._o) if name == "lr_grad_clip" else ()
+            self._made = (*key, L.Prepared(name, *args, self.stat, self.ws, L._nbytes(self.ws)))
+        self._made[3](stream)
 
 
 class _Clipped:
@@ -437,22 +446,24 @@ class QkRotary:
         self.ws = _buf(L.lr_qk_bwd_workspace_bytes(self.dt, s.T, self.sh), device) if back else None
 
         def rows(t):
-            return (L._p(t), 0 if t is None else t.stride(0) if s.T > 1 else t.shape[1])
+            return (t, 0 if t is None else t.stride(0) if s.T > 1 else t.shape[1])
 
-        common = (self.dt, s.T, self.sh, s.eps, L._p(self.turns), L._p(self.pos), L._p(self.gq), L._p(self.gk),
+        common = (self.dt, s.T, L.ctypes.pointer(self.sh), s.eps, self.turns, self.pos, self.gq, self.gk,
                   *rows(self.q), *rows(self.k))
-        self._fwd = (*common, *rows(self.qo), *rows(self.ko))
-        self._bwd = (*common, *rows(self.dqo), *rows(self.dko), *rows(self.dq), *rows(self.dk), L._p(self.dgq),
-                     L._p(self.dgk), self.ws)
+        self._fwd = L.Prepared("lr_qk_fwd", *common, *rows(self.qo), *rows(self.ko))
+        self._bwd = None
+        if back:
+            self._bwd = L.Prepared("lr_qk_bwd", *common, *rows(self.dqo), *rows(self.dko), *rows(self.dq),
+                                   *rows(self.dk), self.dgq, self.dgk, self.ws, L._nbytes(self.ws))
 
     def forward(self, stream=None):
-        L.lr_qk_fwd(*self._fwd, stream)
+        self._fwd(stream)
         return self.qo, self.ko
 
     def backward(self, stream=None):
-        if self.ws is None:
+        if self._bwd is None:
             raise ValueError("no upstream gradients dqo, dko were given")
-        L.lr_qk_bwd(*self._bwd, stream)
+        self._bwd(stream)
         return self.dq, self.dk
 
     def step(self, stream=None):
