@@ -8,20 +8,26 @@
 
 namespace lr {
 
-constexpr int kGradTable = 1024;  // most tensors of one launch
-constexpr int kGradChunk = 8192;  // elements a block takes at a time (32 a thread)
-constexpr int kGradParts = 4096;  // most blocks of one launch, each writing one partial sum
-constexpr int kGradFew = 512;     // partial sums that the scaling blocks add up themselves
+constexpr int kGradTable = 1024;        // most tensors of one launch
+constexpr int kGradOwners = 256;        // entries that say where to look for a chunk's tensor
+constexpr int kGradChunkBytes = 32768;  // what 256 threads take at a time (8 16-byte words each)
+constexpr int kGradParts = 4096;        // most blocks of one launch, each writing one partial sum
+constexpr int kGradFew = 512;           // partial sums that the scaling blocks add up themselves
+constexpr int kGradKeepBytes = 64 << 20;  // the last of the sum's reads, which the scaling finds in L2
+constexpr int kGradSmall = 32;          // chunks that one cluster sums and scales in one launch
 
 // The tensors of one launch, passed by value with it (no host-to-device copy, so a call can be captured).
-// Tensor i is cut into chunks first[i] .. first[i + 1] - 1; a block takes `each` consecutive ones.
+// Tensor i is cut into chunks first[i] .. first[i + 1] - 1; a block that sums takes `each` consecutive ones, and
+// chunks before `keep` are read so that they leave L2 first.
+// A chunk's tensor is found from owner[chunk >> shift], the tensor of the first chunk with that prefix.
 template <int N>
 struct GradTable {
   const void* src[N];
   void* dst[N];
   long long numel[N];
   int first[N + 1];
-  int n, each;
+  unsigned short owner[kGradOwners];
+  int n, each, keep, shift;
 };
 
 // What becomes of the sums: norm -> stat[0], scale -> stat[1] unless it has only been asked for the norm.
@@ -39,6 +45,9 @@ template <typename ST, int N>
 cudaError_t launch_grad_sumsq(const GradTable<N>& tab, double* part, cudaStream_t st);
 // norm and scale from any number of partial sums, by one block.
 cudaError_t launch_grad_stat(const GradStat& gs, cudaStream_t st);
+// Sums and scaling of at most kGradSmall chunks (tab.dst null: the norm only).
+template <typename ST>
+cudaError_t launch_grad_small(const GradTable<16>& tab, const GradStat& gs, cudaStream_t st);
 // The tensors scaled; with gs.nparts > 0 every block first adds the partial sums up, and the first writes stat.
 template <typename ST, int N>
 cudaError_t launch_grad_scale(const GradTable<N>& tab, const GradStat& gs, bool in_place, cudaStream_t st);

@@ -1543,29 +1543,39 @@ static size_t grad_ws_bytes(int n) {
   return launches * kGradParts * sizeof(double);
 }
 
-static long long grad_chunks(const long long* numel, int n) {
+static long long grad_chunks(const long long* numel, int n, size_t es) {
+  const long long per = kGradChunkBytes / static_cast<long long>(es);
   long long chunks = 0;
-  for (int i = 0; i < n; ++i) chunks += (numel[i] + kGradChunk - 1) / kGradChunk;
+  for (int i = 0; i < n; ++i) chunks += (numel[i] + per - 1) / per;
   return chunks;
 }
 
 template <int N>
-static void grad_table(const void* const* grads, const long long* numel, void* const* outs, int n, int chunks,
+static void grad_table(const void* const* grads, const long long* numel, void* const* outs, int n, int chunks, size_t es,
                        GradTable<N>* t) {
+  const long long per = kGradChunkBytes / static_cast<long long>(es);
   int first = 0;
   for (int i = 0; i < n; ++i) {
     t->src[i] = grads[i];
     t->dst[i] = outs ? outs[i] : nullptr;
     t->numel[i] = numel[i];
     t->first[i] = first;
-    first += static_cast<int>((numel[i] + kGradChunk - 1) / kGradChunk);
+    first += static_cast<int>((numel[i] + per - 1) / per);
   }
   t->first[n] = first;
   t->n = n;
-  t->each = (chunks + kGradParts - 1) / kGradParts;
+  const int most = chunks <= 4 * kGradFew ? kGradFew : kGradParts;
+  t->each = (chunks + most - 1) / most;
+  t->keep = chunks - kGradKeepBytes / kGradChunkBytes;
+  t->shift = 0;
+  while (chunks > 0 && (chunks - 1) >> t->shift >= kGradOwners) ++t->shift;
+  for (int j = 0, i = 0; j << t->shift < chunks; ++j) {
+    while (t->first[i + 1] <= j << t->shift) ++i;
+    t->owner[j] = static_cast<unsigned short>(i);
+  }
 }
 
-// One launch list: at most N tensors (the launch carries their table, so a short list takes a small one).
+// At most N tensors a launch (the launch carries their table, so a short list takes a small one).
 template <typename ST, int N>
 static lr_status grad_lists(const Ctx& c, int n, const void* const* grads, const long long* numel, float max_norm,
                             void* const* outs, float* stat, double* part) {
@@ -1576,12 +1586,22 @@ static lr_status grad_lists(const Ctx& c, int n, const void* const* grads, const
     for (int i = i0; i < i0 + k; ++i) e += static_cast<double>(numel[i]);
     return e;
   };
+  if constexpr (N == 16) {
+    const long long chunks = n <= N ? grad_chunks(numel, n, c.es) : kGradSmall + 1;
+    if (chunks <= kGradSmall) {
+      grad_table(grads, numel, outs, n, static_cast<int>(chunks), c.es, &tab);
+      LaunchScope scope("grad_small", c.st, 0, (outs ? 2.0 : 1.0) * c.es * elems(0, n));
+      cudaError_t e = launch_grad_small<ST>(tab, gs, c.st);
+      if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
+      return LR_OK;
+    }
+  }
   bool in_place = outs != nullptr;
   for (int i = 0; in_place && i < n; ++i) in_place = numel[i] == 0 || outs[i] == grads[i];
   for (int i0 = 0; i0 < n; i0 += N) {
-    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k));
+    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k, c.es));
     if (chunks == 0) continue;
-    grad_table(grads + i0, numel + i0, outs ? outs + i0 : nullptr, k, chunks, &tab);
+    grad_table(grads + i0, numel + i0, outs ? outs + i0 : nullptr, k, chunks, c.es, &tab);
     LaunchScope scope("grad_sumsq", c.st, 0, c.es * elems(i0, k));
     cudaError_t e = launch_grad_sumsq<ST>(tab, part + gs.nparts, c.st);
     if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient norm: %s", cudaGetErrorString(e));
@@ -1601,9 +1621,9 @@ static lr_status grad_lists(const Ctx& c, int n, const void* const* grads, const
   }
   if (!outs) return LR_OK;
   for (int i0 = 0; i0 < n; i0 += N) {
-    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k));
+    const int k = std::min(N, n - i0), chunks = static_cast<int>(grad_chunks(numel + i0, k, c.es));
     if (chunks == 0) continue;
-    if (n > N) grad_table(grads + i0, numel + i0, outs + i0, k, chunks, &tab);
+    if (n > N) grad_table(grads + i0, numel + i0, outs + i0, k, chunks, c.es, &tab);
     LaunchScope scope("grad_scale", c.st, 0, 2.0 * c.es * elems(i0, k));
     cudaError_t e = launch_grad_scale<ST>(tab, gs, in_place, c.st);
     if (e != cudaSuccess) return fail(LR_ERR_CUDA, "gradient clipping: %s", cudaGetErrorString(e));
@@ -2381,7 +2401,7 @@ static lr_status check_grads(lr_dtype dt, int n, const void* const* grads, const
     if (clip) LR_TRY(check_ptr(outs[i], "outs[i]"));
   }
   for (int i = 0; i < n; i += kGradTable)  // chunks of a launch are counted in int
-    if (grad_chunks(numel + i, std::min(kGradTable, n - i)) > (1LL << 30))
+    if (grad_chunks(numel + i, std::min(kGradTable, n - i), esize(dt)) > (1LL << 30))
       return fail(LR_ERR_SHAPE, "tensors %d..: too many elements", i);
   LR_TRY(check_ptr(stat, "stat"));
   LR_TRY(check_ptr(ws, "ws"));

@@ -1,8 +1,8 @@
 """lr_grad_norm / lr_grad_clip on the GPU against fp64.
 
-Bounds, u = 2^-24: a block sums at most 64 squares of one thread in fp32 before it goes on in fp64, each square
-and each addition within u: 65 u of the sum of squares, half of that in the norm, and u for its last rounding:
-34 u.  scale = max_norm / (norm + 1e-6) adds 3 u, the product one, and the output half a step of its type.
+Bounds, u = 2^-24: fewer than 64 roundings on a square's way through the fp32 sums (32 in a row, the pairwise ones of
+a warp) before the sum goes on in fp64: 65 u of the sum of squares, half of that in the norm, and u for its last
+rounding: 34 u.  scale = max_norm / (norm + 1e-6) adds 3 u, the product one, and the output half a step of its type.
 """
 import numpy as np
 import pytest
