@@ -330,6 +330,33 @@ lr_status lr_block_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, 
                        const lr_block_weights* w, const void* saved, size_t saved_bytes, const void* dout, void* dx,
                        const lr_block_grads* g, void* ws, size_t ws_bytes, void* stream);
 
+/* The block with norm and position rotation of its queries and keys (as lr_qk_fwd) between
+ * the q/k/v group and attention:
+ *     [q; k; v] = LR_{q,k,v}(RMSNorm(x; g_attn)),  q', k' = norm and rotation of q, k,
+ *     o = causal attention(q', k', v), and on as above.
+ * shape: Hq = Hk = H and the block's dh; its seq is not used: without pos a token's position
+ * is its place in its sequence of s.  pos: [axes, b*s].  gq, gk: [dh] bf16, or NULL (that
+ * tensor is rotated without the norm); dgq, dgk [dh] fp32, ignored without their gain.
+ * saved additionally keeps q' and k'.  dh at most 512; otherwise the rules of lr_block_* and
+ * lr_qk_* apply.
+ */
+typedef struct {
+  lr_qk_shape shape;
+  const unsigned long long* turns;
+  const int* pos;
+  const void *gq, *gk;
+} lr_block_qk;
+
+size_t lr_block_qk_saved_bytes(int b, int s, int H, int dh, int f, int ra, int rm);
+size_t lr_block_qk_workspace_bytes(int b, int s, int H, int dh, int f, int ra, int rm);
+lr_status lr_block_qk_fwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                          const lr_block_weights* w, const lr_block_qk* qk, void* out, void* saved,
+                          size_t saved_bytes, void* ws, size_t ws_bytes, void* stream);
+lr_status lr_block_qk_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                          const lr_block_weights* w, const lr_block_qk* qk, const void* saved, size_t saved_bytes,
+                          const void* dout, void* dx, const lr_block_grads* g, float* dgq, float* dgk, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* -------------------------------------------------------------- block stack
  * One training step of `nblocks` residual MLP blocks (as lr_mlp_fwd, sigma = SiLU) and a
  * mean-squared-error loss against `target` [T, d]:

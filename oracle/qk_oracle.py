@@ -32,7 +32,7 @@ F64 = np.float64
 # 2 pi to 60 digits
 TWO_PI = Fraction(628318530717958647692528676655900576839433879875021164194988, 10 ** 59)
 
-__all__ = ["TWO_PI", "angles", "pairs", "qk_fwd", "qk_bwd", "magnitudes", "clip"]
+__all__ = ["TWO_PI", "angles", "pairs", "qk_fwd", "qk_bwd", "magnitudes", "clip", "block_fwd", "block_bwd"]
 
 
 def angles(pos: np.ndarray, freq: Sequence[float], sec: Sequence[int]) -> np.ndarray:
@@ -130,3 +130,50 @@ def clip(grads: List[np.ndarray], max_norm: float):
     norm = unit * np.sqrt(total)
     scale = min(1.0, max_norm / (norm + 1e-6))
     return norm, scale, [scale * np.asarray(g, dtype=F64) for g in grads]
+
+
+# ---------------------------------------------------------------------------
+# The low-rank transformer block with norm and rotation of q and k before attention.
+# ---------------------------------------------------------------------------
+def block_fwd(x, W: Dict, rot: Dict, b: int, s: int, H: int, dh: int, eps: float = 1e-6):
+    """attention_oracle.block_fwd with q, k normed and rotated; rot: theta [T, pairs], rot, layout, gq, gk."""
+    from . import attention_oracle as A
+    from . import lowrank_oracle as O
+
+    x = O.to64(x)
+    qkv, s_qkv = O.proj_group_fwd(x, W["g_attn"], [W["A_q"], W["A_k"], W["A_v"]],
+                                  [W["B_q"], W["B_k"], W["B_v"]], eps)
+    qr, kr = (qk_fwd(t, rot[g], rot["theta"], dh, rot["rot"], rot["layout"], eps)
+              for t, g in ((qkv[0], "gq"), (qkv[1], "gk")))
+    o, s_att = A.attention_fwd(qr, kr, qkv[2], b, s, H, dh, dh ** -0.5)
+    (y,), s_o = O.proj_group_fwd(o, None, [W["A_o"]], [W["B_o"]], eps)
+    x1 = x + y
+    mlp = {k: W[k] for k in ("A_gate", "B_gate", "A_up", "B_up", "A_down", "B_down")}
+    out, s_mlp = O.mlp_block_fwd(x1, W["g_mlp"], mlp, eps, O.FULL)
+    return out, dict(qkv=qkv, qr=qr, kr=kr, s_qkv=s_qkv, o=o, s_att=s_att, s_o=s_o, mlp=mlp, s_mlp=s_mlp)
+
+
+def block_bwd(W: Dict, saved: Dict, rot: Dict, G, b: int, s: int, H: int, dh: int, eps: float = 1e-6):
+    """Gradients of sum(out * G), with dgq and dgk where the gains are given."""
+    from . import attention_oracle as A
+    from . import lowrank_oracle as O
+
+    gm = O.mlp_block_bwd(W["g_mlp"], saved["mlp"], saved["s_mlp"], O.to64(G), eps)
+    dx1 = gm["dx"]
+    go = O.proj_group_bwd(None, [W["A_o"]], [W["B_o"]], saved["s_o"], [dx1])
+    ga = A.attention_bwd(saved["qr"], saved["kr"], saved["qkv"][2], saved["o"], saved["s_att"], go["dx"], b, s, H, dh,
+                         dh ** -0.5)
+    q, k = (qk_bwd(saved["qkv"][i], rot[g], rot["theta"], ga[d], dh, rot["rot"], rot["layout"], eps)
+            for i, g, d in ((0, "gq", "dq"), (1, "gk", "dk")))
+    gq = O.proj_group_bwd(W["g_attn"], [W["A_q"], W["A_k"], W["A_v"]], [W["B_q"], W["B_k"], W["B_v"]],
+                          saved["s_qkv"], [q["dx"], k["dx"], ga["dv"]])
+    out = {"dx": dx1 + gq["dx"], "dg_attn": gq["dg"], "dg_mlp": gm["dg"]}
+    for n, g in (("dgq", q), ("dgk", k)):
+        if "dg" in g:
+            out[n] = g["dg"]
+    for i, n in enumerate("qkv"):
+        out[f"dA_{n}"], out[f"dB_{n}"] = gq["dA"][i], gq["dB"][i]
+    out["dA_o"], out["dB_o"] = go["dA"][0], go["dB"][0]
+    for n in ("gate", "up", "down"):
+        out[f"dA_{n}"], out[f"dB_{n}"] = gm[f"dA_{n}"], gm[f"dB_{n}"]
+    return out

@@ -1396,94 +1396,6 @@ static lr_status attn_bwd_impl(const Ctx& c, int b, int s, int H, int dh, float 
   return attn_gemm(c, EPI_STORE, a, s, dh, s, {W.dS, s}, true, false, {q, d}, true, true, dk, d, true, 3);
 }
 
-// ============================================================ transformer block
-// Pre-norm low-rank transformer block: [q; k; v] = normed group (gain g_attn), causal attention,
-// x1 = x + LR_o(o) (residual fused into the o-projection's B GEMM), out = MLP block(x1) in
-// checkpoint mode.  bf16.  The saved set keeps q, k, v, o and x1 besides the pieces' own sets.
-struct BlockSaved {
-  void *qkv, *q, *k, *v, *o, *oproj, *x1, *mlp;
-  float* lse;
-};
-
-static size_t block_saved_layout(int b, int s, int H, int dh, int f, int ra, int rm, void* base, BlockSaved* S) {
-  Arena ar(base);
-  BlockSaved tmp;
-  if (!S) S = &tmp;
-  const int T = b * s, d = H * dh;
-  const size_t act = sizeof(bf16) * static_cast<size_t>(T) * d;
-  S->qkv = ar.take(proj_saved_layout(LR_BF16, T, ra, 3, 1, nullptr, nullptr));
-  S->q = ar.take(act);
-  S->k = ar.take(act);
-  S->v = ar.take(act);
-  S->o = ar.take(act);
-  S->lse = static_cast<float*>(ar.take(sizeof(float) * static_cast<size_t>(b) * H * s));
-  S->oproj = ar.take(proj_saved_layout(LR_BF16, T, ra, 1, 0, nullptr, nullptr));
-  S->x1 = ar.take(act);
-  S->mlp = ar.take(mlp_saved_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr));
-  return ar.size();
-}
-
-struct BlockWs {
-  void* sub;  // the workspace of whichever piece runs
-  void *dx1, *dO, *dq, *dk, *dv;
-};
-
-static size_t block_ws_layout(int b, int s, int H, int dh, int f, int ra, int rm, void* base, BlockWs* W) {
-  Arena ar(base);
-  BlockWs tmp;
-  if (!W) W = &tmp;
-  const int T = b * s, d = H * dh;
-  const size_t act = sizeof(bf16) * static_cast<size_t>(T) * d;
-  const size_t sub = std::max({proj_ws_layout(LR_BF16, true, T, d, d, ra, 3, 1, nullptr, nullptr),
-                               proj_ws_layout(LR_BF16, true, T, d, d, ra, 1, 0, nullptr, nullptr),
-                               attn_ws_layout(b, s, H, dh, nullptr, nullptr),
-                               mlp_fwd_ws_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr),
-                               mlp_bwd_ws_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr)});
-  W->sub = ar.take(sub);
-  void** bufs[5] = {&W->dx1, &W->dO, &W->dq, &W->dk, &W->dv};
-  for (void** p : bufs) *p = ar.take(act);
-  return ar.size();
-}
-
-static lr_status block_fwd_impl(const Ctx& c, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
-                                const void* x, const lr_block_weights& w, void* out, void* saved, void* ws) {
-  BlockSaved S;
-  BlockWs W;
-  block_saved_layout(b, s, H, dh, f, ra, rm, saved, &S);
-  block_ws_layout(b, s, H, dh, f, ra, rm, ws, &W);
-  const int T = b * s, d = H * dh;
-  const lr_pair qkv[3] = {w.q, w.k, w.v};
-  void* const outs[3] = {S.q, S.k, S.v};
-  LR_TRY(proj_fwd_impl(c, T, d, d, ra, 3, qkv, w.g_attn, eps, x, outs, S.qkv, W.sub));
-  LR_TRY(attn_fwd_impl(c, b, s, H, dh, 1.f / sqrtf(static_cast<float>(dh)), S.q, S.k, S.v, S.o, S.lse, W.sub));
-  void* const x1[1] = {S.x1};
-  LR_TRY(proj_fwd_impl(c, T, d, d, ra, 1, &w.o, nullptr, eps, S.o, x1, S.oproj, W.sub, x));
-  return mlp_fwd_impl(c, LR_SAVE_CKPT, T, d, f, rm, eps, S.x1, w.g_mlp, w.gate, w.up, w.down, out, S.mlp, W.sub);
-}
-
-static lr_status block_bwd_impl(const Ctx& c, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
-                                const void* x, const lr_block_weights& w, const void* saved, const void* dout,
-                                void* dx, const lr_block_grads& gr, void* ws) {
-  BlockSaved S;
-  BlockWs W;
-  block_saved_layout(b, s, H, dh, f, ra, rm, const_cast<void*>(saved), &S);
-  block_ws_layout(b, s, H, dh, f, ra, rm, ws, &W);
-  const int T = b * s, d = H * dh;
-  // MLP block: dx1 already holds the gradient its residual passes through
-  LR_TRY(mlp_bwd_impl(c, LR_SAVE_CKPT, T, d, f, rm, eps, S.x1, w.g_mlp, w.gate, w.up, w.down, S.mlp, dout, W.dx1,
-                      gr.dg_mlp, gr.gate, gr.up, gr.down, W.sub));
-  // o-projection: its output's gradient is dx1; its dx is dL/do
-  const void* const d1[1] = {W.dx1};
-  LR_TRY(proj_bwd_impl(c, T, d, d, ra, 1, &w.o, nullptr, S.o, S.oproj, d1, W.dO, nullptr, &gr.o, W.sub));
-  LR_TRY(attn_bwd_impl(c, b, s, H, dh, 1.f / sqrtf(static_cast<float>(dh)), S.q, S.k, S.v, S.o, S.lse, W.dO, W.dq,
-                       W.dk, W.dv, W.sub));
-  // q/k/v group, with the residual's gradient dx1 added into dx
-  const lr_pair qkv[3] = {w.q, w.k, w.v};
-  const void* const dqkv[3] = {W.dq, W.dk, W.dv};
-  const lr_pair_grad gq[3] = {gr.q, gr.k, gr.v};
-  return proj_bwd_impl(c, T, d, d, ra, 3, qkv, w.g_attn, x, S.qkv, dqkv, dx, gr.dg_attn, gq, W.sub, W.dx1);
-}
-
 // ============================================================ query / key norm and rotation
 struct QkWs {
   float* part[2];  // partial sums of dgq, dgk
@@ -1534,6 +1446,120 @@ static lr_status qk_bwd_impl(const Ctx& c, const lr_qk_shape& sh, QkArgs& a, voi
   cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.sms, c.st) : launch_qk_bwd<float>(a, adj, c.sms, c.st);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
   return LR_OK;
+}
+
+// ============================================================ transformer block
+// Pre-norm low-rank transformer block: [q; k; v] = normed group (gain g_attn), causal attention,
+// x1 = x + LR_o(o) (residual fused into the o-projection's B GEMM), out = MLP block(x1) in
+// checkpoint mode.  bf16.  The saved set keeps q, k, v, o and x1 besides the pieces' own sets.
+struct BlockSaved {
+  void *qkv, *q, *k, *v, *o, *oproj, *x1, *mlp;
+  void *qr, *kr;  // what attention reads: q and k, or with `rotated` their normed, rotated copies
+  float* lse;
+};
+
+static size_t block_saved_layout(int b, int s, int H, int dh, int f, int ra, int rm, bool rotated, void* base,
+                                 BlockSaved* S) {
+  Arena ar(base);
+  BlockSaved tmp;
+  if (!S) S = &tmp;
+  const int T = b * s, d = H * dh;
+  const size_t act = sizeof(bf16) * static_cast<size_t>(T) * d;
+  S->qkv = ar.take(proj_saved_layout(LR_BF16, T, ra, 3, 1, nullptr, nullptr));
+  S->q = ar.take(act);
+  S->k = ar.take(act);
+  S->v = ar.take(act);
+  S->o = ar.take(act);
+  S->lse = static_cast<float*>(ar.take(sizeof(float) * static_cast<size_t>(b) * H * s));
+  S->oproj = ar.take(proj_saved_layout(LR_BF16, T, ra, 1, 0, nullptr, nullptr));
+  S->x1 = ar.take(act);
+  S->mlp = ar.take(mlp_saved_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr));
+  S->qr = rotated ? ar.take(act) : S->q;
+  S->kr = rotated ? ar.take(act) : S->k;
+  return ar.size();
+}
+
+struct BlockWs {
+  void* sub;  // the workspace of whichever piece runs
+  void *dx1, *dO, *dq, *dk, *dv;
+};
+
+static size_t block_ws_layout(int b, int s, int H, int dh, int f, int ra, int rm, bool rotated, void* base,
+                              BlockWs* W) {
+  Arena ar(base);
+  BlockWs tmp;
+  if (!W) W = &tmp;
+  const int T = b * s, d = H * dh;
+  const size_t act = sizeof(bf16) * static_cast<size_t>(T) * d;
+  const size_t sub = std::max({proj_ws_layout(LR_BF16, true, T, d, d, ra, 3, 1, nullptr, nullptr),
+                               proj_ws_layout(LR_BF16, true, T, d, d, ra, 1, 0, nullptr, nullptr),
+                               attn_ws_layout(b, s, H, dh, nullptr, nullptr),
+                               rotated ? qk_ws_layout(dh, nullptr, nullptr) : size_t(0),
+                               mlp_fwd_ws_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr),
+                               mlp_bwd_ws_layout(LR_BF16, LR_SAVE_CKPT, T, d, f, rm, nullptr, nullptr)});
+  W->sub = ar.take(sub);
+  void** bufs[5] = {&W->dx1, &W->dO, &W->dq, &W->dk, &W->dv};
+  for (void** p : bufs) *p = ar.take(act);
+  return ar.size();
+}
+
+static QkArgs block_qk_args(int T, int s, const lr_block_qk& qk, float eps) {
+  QkArgs a = qk_args(T, qk.shape, eps, qk.turns, qk.pos);
+  a.seq = s;
+  return a;
+}
+
+static lr_status block_fwd_impl(const Ctx& c, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
+                                const void* x, const lr_block_weights& w, const lr_block_qk* qk, void* out,
+                                void* saved, void* ws) {
+  BlockSaved S;
+  BlockWs W;
+  block_saved_layout(b, s, H, dh, f, ra, rm, qk != nullptr, saved, &S);
+  block_ws_layout(b, s, H, dh, f, ra, rm, qk != nullptr, ws, &W);
+  const int T = b * s, d = H * dh;
+  const lr_pair qkv[3] = {w.q, w.k, w.v};
+  void* const outs[3] = {S.q, S.k, S.v};
+  LR_TRY(proj_fwd_impl(c, T, d, d, ra, 3, qkv, w.g_attn, eps, x, outs, S.qkv, W.sub));
+  if (qk) {
+    QkArgs a = block_qk_args(T, s, *qk, eps);
+    a.t[0] = QkTensor{S.q, nullptr, S.qr, qk->gq, nullptr, nullptr, d, 0, d, H};
+    a.t[1] = QkTensor{S.k, nullptr, S.kr, qk->gk, nullptr, nullptr, d, 0, d, H};
+    LR_TRY(qk_fwd_impl(c, qk->shape, a));
+  }
+  LR_TRY(attn_fwd_impl(c, b, s, H, dh, 1.f / sqrtf(static_cast<float>(dh)), S.qr, S.kr, S.v, S.o, S.lse, W.sub));
+  void* const x1[1] = {S.x1};
+  LR_TRY(proj_fwd_impl(c, T, d, d, ra, 1, &w.o, nullptr, eps, S.o, x1, S.oproj, W.sub, x));
+  return mlp_fwd_impl(c, LR_SAVE_CKPT, T, d, f, rm, eps, S.x1, w.g_mlp, w.gate, w.up, w.down, out, S.mlp, W.sub);
+}
+
+static lr_status block_bwd_impl(const Ctx& c, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
+                                const void* x, const lr_block_weights& w, const lr_block_qk* qk, const void* saved,
+                                const void* dout, void* dx, const lr_block_grads& gr, float* dgq, float* dgk,
+                                void* ws) {
+  BlockSaved S;
+  BlockWs W;
+  block_saved_layout(b, s, H, dh, f, ra, rm, qk != nullptr, const_cast<void*>(saved), &S);
+  block_ws_layout(b, s, H, dh, f, ra, rm, qk != nullptr, ws, &W);
+  const int T = b * s, d = H * dh;
+  // MLP block: dx1 already holds the gradient its residual passes through
+  LR_TRY(mlp_bwd_impl(c, LR_SAVE_CKPT, T, d, f, rm, eps, S.x1, w.g_mlp, w.gate, w.up, w.down, S.mlp, dout, W.dx1,
+                      gr.dg_mlp, gr.gate, gr.up, gr.down, W.sub));
+  // o-projection: its output's gradient is dx1; its dx is dL/do
+  const void* const d1[1] = {W.dx1};
+  LR_TRY(proj_bwd_impl(c, T, d, d, ra, 1, &w.o, nullptr, S.o, S.oproj, d1, W.dO, nullptr, &gr.o, W.sub));
+  LR_TRY(attn_bwd_impl(c, b, s, H, dh, 1.f / sqrtf(static_cast<float>(dh)), S.qr, S.kr, S.v, S.o, S.lse, W.dO, W.dq,
+                       W.dk, W.dv, W.sub));
+  if (qk) {  // dq and dk of the rotated tensors become those of the projections' outputs, in place
+    QkArgs a = block_qk_args(T, s, *qk, eps);
+    a.t[0] = QkTensor{S.q, W.dq, W.dq, qk->gq, dgq, nullptr, d, d, d, H};
+    a.t[1] = QkTensor{S.k, W.dk, W.dk, qk->gk, dgk, nullptr, d, d, d, H};
+    LR_TRY(qk_bwd_impl(c, qk->shape, a, W.sub));
+  }
+  // q/k/v group, with the residual's gradient dx1 added into dx
+  const lr_pair qkv[3] = {w.q, w.k, w.v};
+  const void* const dqkv[3] = {W.dq, W.dk, W.dv};
+  const lr_pair_grad gq[3] = {gr.q, gr.k, gr.v};
+  return proj_bwd_impl(c, T, d, d, ra, 3, qkv, w.g_attn, x, S.qkv, dqkv, dx, gr.dg_attn, gq, W.sub, W.dx1);
 }
 
 // ============================================================ gradient norm and clipping
@@ -2147,12 +2173,12 @@ static lr_status check_block(lr_dtype dt, int b, int s, int H, int dh, int f, in
 
 size_t lr_block_saved_bytes(int b, int s, int H, int dh, int f, int ra, int rm) {
   if (check_block(LR_BF16, b, s, H, dh, f, ra, rm)) return 0;
-  return block_saved_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr);
+  return block_saved_layout(b, s, H, dh, f, ra, rm, false, nullptr, nullptr);
 }
 
 size_t lr_block_workspace_bytes(int b, int s, int H, int dh, int f, int ra, int rm) {
   if (check_block(LR_BF16, b, s, H, dh, f, ra, rm)) return 0;
-  return block_ws_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr);
+  return block_ws_layout(b, s, H, dh, f, ra, rm, false, nullptr, nullptr);
 }
 
 static lr_status check_block_weights(const lr_block_weights* w) {
@@ -2163,31 +2189,29 @@ static lr_status check_block_weights(const lr_block_weights* w) {
   return LR_OK;
 }
 
-lr_status lr_block_fwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
-                       const lr_block_weights* w, void* out, void* saved, size_t saved_bytes, void* ws,
-                       size_t ws_bytes, void* stream) {
-  t_last_error.clear();
-  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+// Both forms of the block; qk null: without norm and rotation of q and k.
+static lr_status block_fwd_checked(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
+                                   const void* x, const lr_block_weights* w, const lr_block_qk* qk, void* out,
+                                   void* saved, size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
   LR_TRY(check_block_weights(w));
   LR_TRY(check_ptr(x, "x"));
   LR_TRY(check_ptr(out, "out"));
   LR_TRY(check_ptr(saved, "saved"));
   LR_TRY(check_ptr(ws, "ws"));
-  LR_TRY(check_size(saved_bytes, block_saved_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr), "saved"));
-  LR_TRY(check_size(ws_bytes, block_ws_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr), "ws"));
+  LR_TRY(check_size(saved_bytes, block_saved_layout(b, s, H, dh, f, ra, rm, qk != nullptr, nullptr, nullptr), "saved"));
+  LR_TRY(check_size(ws_bytes, block_ws_layout(b, s, H, dh, f, ra, rm, qk != nullptr, nullptr, nullptr), "ws"));
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c));
   // Without programmatic dependent launch: with it, three fwd+bwd steps of the block issued back to
   // back stopped making progress on the GPU (one or two did not; the cause is not known).
   PdlOff serial;
-  return block_fwd_impl(c, b, s, H, dh, f, ra, rm, eps, x, *w, out, saved, ws);
+  return block_fwd_impl(c, b, s, H, dh, f, ra, rm, eps, x, *w, qk, out, saved, ws);
 }
 
-lr_status lr_block_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
-                       const lr_block_weights* w, const void* saved, size_t saved_bytes, const void* dout, void* dx,
-                       const lr_block_grads* g, void* ws, size_t ws_bytes, void* stream) {
-  t_last_error.clear();
-  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+static lr_status block_bwd_checked(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps,
+                                   const void* x, const lr_block_weights* w, const lr_block_qk* qk, const void* saved,
+                                   size_t saved_bytes, const void* dout, void* dx, const lr_block_grads* g, float* dgq,
+                                   float* dgk, void* ws, size_t ws_bytes, void* stream) {
   LR_TRY(check_block_weights(w));
   LR_TRY(check_ptr(g, "g"));
   const void* gp[] = {g->dg_attn, g->q.dA, g->q.dB, g->k.dA, g->k.dB, g->v.dA, g->v.dB, g->o.dA, g->o.dB,
@@ -2198,12 +2222,30 @@ lr_status lr_block_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, 
   LR_TRY(check_ptr(dout, "dout"));
   LR_TRY(check_ptr(dx, "dx"));
   LR_TRY(check_ptr(ws, "ws"));
-  LR_TRY(check_size(saved_bytes, block_saved_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr), "saved"));
-  LR_TRY(check_size(ws_bytes, block_ws_layout(b, s, H, dh, f, ra, rm, nullptr, nullptr), "ws"));
+  LR_TRY(check_size(saved_bytes, block_saved_layout(b, s, H, dh, f, ra, rm, qk != nullptr, nullptr, nullptr), "saved"));
+  LR_TRY(check_size(ws_bytes, block_ws_layout(b, s, H, dh, f, ra, rm, qk != nullptr, nullptr, nullptr), "ws"));
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c));
-  PdlOff serial;  // see lr_block_fwd
-  return block_bwd_impl(c, b, s, H, dh, f, ra, rm, eps, x, *w, saved, dout, dx, *g, ws);
+  PdlOff serial;  // see block_fwd_checked
+  return block_bwd_impl(c, b, s, H, dh, f, ra, rm, eps, x, *w, qk, saved, dout, dx, *g, dgq, dgk, ws);
+}
+
+lr_status lr_block_fwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                       const lr_block_weights* w, void* out, void* saved, size_t saved_bytes, void* ws,
+                       size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+  return block_fwd_checked(dt, b, s, H, dh, f, ra, rm, eps, x, w, nullptr, out, saved, saved_bytes, ws, ws_bytes,
+                           stream);
+}
+
+lr_status lr_block_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                       const lr_block_weights* w, const void* saved, size_t saved_bytes, const void* dout, void* dx,
+                       const lr_block_grads* g, void* ws, size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+  return block_bwd_checked(dt, b, s, H, dh, f, ra, rm, eps, x, w, nullptr, saved, saved_bytes, dout, dx, g, nullptr,
+                           nullptr, ws, ws_bytes, stream);
 }
 
 size_t lr_btp_payload_floats(int T, int r, int group) {
@@ -2384,6 +2426,53 @@ lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const 
   a.t[0] = QkTensor{q, dqo, dq, gq, dgq, nullptr, ldq, lddqo, lddq, sh->Hq};
   a.t[1] = QkTensor{k, dko, dk, gk, dgk, nullptr, ldk, lddko, lddk, sh->Hk};
   return qk_bwd_impl(c, *sh, a, ws);
+}
+
+// The block's own head count and width, whatever the pointers.
+static lr_status check_block_qk(lr_dtype dt, int b, int s, int H, int dh, const lr_block_qk* qk, float eps) {
+  if (!qk) return fail(LR_ERR_NULL, "qk is NULL");
+  if (qk->shape.Hq != H || qk->shape.Hk != H || qk->shape.dh != dh)
+    return fail(LR_ERR_SHAPE, "qk has Hq = %d, Hk = %d, dh = %d; the block has H = %d, dh = %d", qk->shape.Hq,
+                qk->shape.Hk, qk->shape.dh, H, dh);
+  LR_TRY(check_qk(dt, b * s, &qk->shape));
+  lr_qk_shape sh = qk->shape;
+  sh.seq = s;
+  return check_qk_common(&sh, eps, qk->turns, qk->pos, qk->gq, qk->gk);
+}
+
+static bool block_qk_sizes_ok(int b, int s, int H, int dh, int f, int ra, int rm) {
+  return !check_block(LR_BF16, b, s, H, dh, f, ra, rm) && dh <= 512 && 1LL * b * s * H <= (1 << 30);
+}
+
+size_t lr_block_qk_saved_bytes(int b, int s, int H, int dh, int f, int ra, int rm) {
+  return block_qk_sizes_ok(b, s, H, dh, f, ra, rm) ? block_saved_layout(b, s, H, dh, f, ra, rm, true, nullptr, nullptr)
+                                                   : 0;
+}
+
+size_t lr_block_qk_workspace_bytes(int b, int s, int H, int dh, int f, int ra, int rm) {
+  return block_qk_sizes_ok(b, s, H, dh, f, ra, rm) ? block_ws_layout(b, s, H, dh, f, ra, rm, true, nullptr, nullptr) : 0;
+}
+
+lr_status lr_block_qk_fwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                          const lr_block_weights* w, const lr_block_qk* qk, void* out, void* saved,
+                          size_t saved_bytes, void* ws, size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+  LR_TRY(check_block_qk(dt, b, s, H, dh, qk, eps));
+  return block_fwd_checked(dt, b, s, H, dh, f, ra, rm, eps, x, w, qk, out, saved, saved_bytes, ws, ws_bytes, stream);
+}
+
+lr_status lr_block_qk_bwd(lr_dtype dt, int b, int s, int H, int dh, int f, int ra, int rm, float eps, const void* x,
+                          const lr_block_weights* w, const lr_block_qk* qk, const void* saved, size_t saved_bytes,
+                          const void* dout, void* dx, const lr_block_grads* g, float* dgq, float* dgk, void* ws,
+                          size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_block(dt, b, s, H, dh, f, ra, rm));
+  LR_TRY(check_block_qk(dt, b, s, H, dh, qk, eps));
+  if (qk->gq) LR_TRY(check_ptr(dgq, "dgq"));
+  if (qk->gk) LR_TRY(check_ptr(dgk, "dgk"));
+  return block_bwd_checked(dt, b, s, H, dh, f, ra, rm, eps, x, w, qk, saved, saved_bytes, dout, dx, g, dgq, dgk, ws,
+                           ws_bytes, stream);
 }
 
 static constexpr int kGradMaxTensors = 65536;

@@ -35,6 +35,7 @@ EXPORTED = [
     "lr_btp_finish", "lr_attn_saved_bytes", "lr_attn_workspace_bytes", "lr_attn_fwd", "lr_attn_bwd",
     "lr_block_saved_bytes", "lr_block_workspace_bytes", "lr_block_fwd", "lr_block_bwd", "lr_rot_turns", "lr_qk_fwd",
     "lr_qk_bwd_workspace_bytes", "lr_qk_bwd", "lr_grad_workspace_bytes", "lr_grad_norm", "lr_grad_clip",
+    "lr_block_qk_saved_bytes", "lr_block_qk_workspace_bytes", "lr_block_qk_fwd", "lr_block_qk_bwd",
 ]
 
 
@@ -66,6 +67,11 @@ class lr_block_grads(ctypes.Structure):
 class lr_qk_shape(ctypes.Structure):
     _fields_ = [("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("dh", ctypes.c_int), ("rot", ctypes.c_int),
                 ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("sec", ctypes.c_int * 4), ("seq", ctypes.c_int)]
+
+
+class lr_block_qk(ctypes.Structure):
+    _fields_ = [("shape", lr_qk_shape), ("turns", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("gq", ctypes.c_void_p),
+                ("gk", ctypes.c_void_p)]
 
 
 _lib = None
@@ -102,6 +108,13 @@ _SIGS = {
                           _SZ, _P]),
     "lr_block_bwd": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _F, _P, ctypes.POINTER(lr_block_weights), _P, _SZ, _P, _P,
                           ctypes.POINTER(lr_block_grads), _P, _SZ, _P]),
+    "lr_block_qk_saved_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "lr_block_qk_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "lr_block_qk_fwd": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _F, _P, ctypes.POINTER(lr_block_weights),
+                             ctypes.POINTER(lr_block_qk), _P, _P, _SZ, _P, _SZ, _P]),
+    "lr_block_qk_bwd": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, _F, _P, ctypes.POINTER(lr_block_weights),
+                             ctypes.POINTER(lr_block_qk), _P, _SZ, _P, _P, ctypes.POINTER(lr_block_grads), _P, _P, _P,
+                             _SZ, _P]),
     "lr_attn_saved_bytes": (_SZ, [_I, _I, _I, _I]),
     "lr_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
     "lr_attn_fwd": (_I, [_I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _SZ, _P, _SZ, _P]),
@@ -368,6 +381,27 @@ def lr_block_bwd(dt, b, s, H, dh, f, ra, rm, eps, x, w: lr_block_weights, saved,
                               _p(dout), _p(dx), ctypes.byref(g), _p(ws), _nbytes(ws), _stream(stream)))
 
 
+def lr_block_qk_saved_bytes(b, s, H, dh, f, ra, rm) -> int:
+    return lib().lr_block_qk_saved_bytes(b, s, H, dh, f, ra, rm)
+
+
+def lr_block_qk_workspace_bytes(b, s, H, dh, f, ra, rm) -> int:
+    return lib().lr_block_qk_workspace_bytes(b, s, H, dh, f, ra, rm)
+
+
+def lr_block_qk_fwd(dt, b, s, H, dh, f, ra, rm, eps, x, w: lr_block_weights, qk: lr_block_qk, out, saved, ws,
+                    stream=None):
+    _check(lib().lr_block_qk_fwd(dt, b, s, H, dh, f, ra, rm, eps, _p(x), ctypes.byref(w), ctypes.byref(qk), _p(out),
+                                 _p(saved), _nbytes(saved), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def lr_block_qk_bwd(dt, b, s, H, dh, f, ra, rm, eps, x, w: lr_block_weights, qk: lr_block_qk, saved, dout, dx,
+                    g: lr_block_grads, dgq, dgk, ws, stream=None):
+    _check(lib().lr_block_qk_bwd(dt, b, s, H, dh, f, ra, rm, eps, _p(x), ctypes.byref(w), ctypes.byref(qk), _p(saved),
+                                 _nbytes(saved), _p(dout), _p(dx), ctypes.byref(g), _p(dgq), _p(dgk), _p(ws),
+                                 _nbytes(ws), _stream(stream)))
+
+
 def qk_shape(Hq, Hk, dh, rot, sec, layout=LR_PAIR_HALF, seq=0) -> lr_qk_shape:
     """sec: pairs turned by each position axis (1 to 4 of them)."""
     if not 1 <= len(sec) <= 4:
@@ -381,6 +415,14 @@ def lr_rot_turns(freq: Sequence[float]) -> list:
     out = (ctypes.c_ulonglong * max(n, 1))()
     _check(lib().lr_rot_turns(n, (ctypes.c_double * max(n, 1))(*freq), out))
     return list(out)[:n]
+
+
+def turns_tensor(freq: Sequence[float], device):
+    """lr_rot_turns as a device tensor (int64 holding the bits of the unsigned values)."""
+    import torch
+
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in lr_rot_turns([float(f) for f in freq])],
+                        dtype=torch.int64, device=device)
 
 
 def lr_qk_fwd(dt, T, sh: lr_qk_shape, eps, turns, pos, gq, gk, q, ldq, k, ldk, qo, ldqo, ko, ldko, stream=None):

@@ -399,6 +399,11 @@ class Attention:
         self.backward(None, stream)
 
 
+def _qk_shape(s: QkShape) -> L.lr_qk_shape:
+    layouts = {"half": L.LR_PAIR_HALF, "pairs": L.LR_PAIR_ADJACENT}
+    return L.qk_shape(s.Hq, s.Hk, s.dh, s.rot, s.sec, layouts[s.layout], s.seq)
+
+
 class QkRotary:
     """Norm and position rotation of queries and keys between their projections and attention.
 
@@ -410,8 +415,7 @@ class QkRotary:
 
     def __init__(self, shape: QkShape, case: Dict[str, object], device="cuda"):
         s, self.s, self.dt = shape, shape, _dt(shape.dtype)
-        layouts = {"half": L.LR_PAIR_HALF, "pairs": L.LR_PAIR_ADJACENT}
-        self.sh = L.qk_shape(s.Hq, s.Hk, s.dh, s.rot, s.sec, layouts[s.layout], s.seq)
+        self.sh = _qk_shape(s)
         td = _tdt(s.dtype)
 
         def on_device(name, size, dtype=td):
@@ -425,8 +429,7 @@ class QkRotary:
 
         if len(case["freq"]) != s.rot // 2:
             raise ValueError(f"{len(case['freq'])} frequencies for {s.rot // 2} pairs")
-        turns = L.lr_rot_turns([float(f) for f in case["freq"]])
-        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.turns = L.turns_tensor(case["freq"], device)
         self.pos = on_device("pos", (len(s.sec), s.T), torch.int32)
         if self.pos is not None and not self.pos.is_contiguous():
             raise ValueError("pos must be contiguous")
@@ -473,12 +476,30 @@ class QkRotary:
 
 class TransformerBlock(_Clipped):
     """One low-rank transformer block (q/k/v group, causal attention, o-projection with its
-    residual, MLP block in checkpoint mode) resident on the device, bf16."""
+    residual, MLP block in checkpoint mode) resident on the device, bf16.
 
-    def __init__(self, shape, case: Dict[str, torch.Tensor], device="cuda"):
+    qk: the heads' position rotation (its T, Hq, Hk, dh those of the block), with case["freq"], case["pos"]
+    (int32 [axes, b*s]; None or missing: positions within each sequence) and the gains case["gq"], case["gk"]
+    [dh] of the queries' and keys' norms (None or missing: no norm)."""
+
+    def __init__(self, shape, case: Dict[str, object], device="cuda", qk: Optional[QkShape] = None):
         self.sh = shape
-        self.t = {k: v.to(device).contiguous() for k, v in case.items()}
+        self.t = {k: v.to(device).contiguous() for k, v in case.items() if isinstance(v, torch.Tensor)}
         t = self.t
+        self.qk = self.dgq = self.dgk = None
+        if qk is not None:
+            if (qk.T, qk.Hq, qk.Hk, qk.dh, qk.dtype) != (shape.T, shape.H, shape.H, shape.dh, "bf16"):
+                raise ValueError("the rotation's tokens, heads or type are not those of the block")
+            if len(case["freq"]) != qk.rot // 2:
+                raise ValueError(f"{len(case['freq'])} frequencies for {qk.rot // 2} pairs")
+            for n, size, dtype in (("pos", (len(qk.sec), qk.T), torch.int32), ("gq", (qk.dh,), torch.bfloat16),
+                                   ("gk", (qk.dh,), torch.bfloat16)):
+                if n in t and (tuple(t[n].shape) != size or t[n].dtype != dtype):
+                    raise ValueError(f"{n}: {list(size)} {dtype} needed, not {list(t[n].shape)} {t[n].dtype}")
+            self.turns = L.turns_tensor(case["freq"], device)
+            self.qk = L.lr_block_qk(_qk_shape(qk), L._p(self.turns), *(L._p(t.get(n)) for n in ("pos", "gq", "gk")))
+            self.dgq, self.dgk = (torch.empty(qk.dh, dtype=torch.float32, device=device) if n in t else None
+                                  for n in ("gq", "gk"))
         self.w = L.lr_block_weights(
             L._p(t["g_attn"]), *(L.pair(t[f"A_{n}"], t[f"B_{n}"]) for n in "qkvo"), L._p(t["g_mlp"]),
             *(L.pair(t[f"A_{n}"], t[f"B_{n}"]) for n in ("gate", "up", "down")))
@@ -496,19 +517,29 @@ class TransformerBlock(_Clipped):
         self.dims = dims
         self.out = torch.empty_like(t["x"])
         self.dx = torch.empty_like(t["x"])
-        self.saved = _buf(L.lr_block_saved_bytes(*dims), device)
-        self.ws = _buf(L.lr_block_workspace_bytes(*dims), device)
+        rotated = self.qk is not None
+        self.saved = _buf((L.lr_block_qk_saved_bytes if rotated else L.lr_block_saved_bytes)(*dims), device)
+        self.ws = _buf((L.lr_block_qk_workspace_bytes if rotated else L.lr_block_workspace_bytes)(*dims), device)
 
     def forward(self, stream=None):
-        L.lr_block_fwd(L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w, self.out, self.saved, self.ws, stream)
+        common = (L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w)
+        if self.qk is None:
+            L.lr_block_fwd(*common, self.out, self.saved, self.ws, stream)
+        else:
+            L.lr_block_qk_fwd(*common, self.qk, self.out, self.saved, self.ws, stream)
 
     def backward(self, stream=None):
-        L.lr_block_bwd(L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w, self.saved, self.t["G"], self.dx,
-                       self.g, self.ws, stream)
+        common = (L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w)
+        if self.qk is None:
+            L.lr_block_bwd(*common, self.saved, self.t["G"], self.dx, self.g, self.ws, stream)
+        else:
+            L.lr_block_qk_bwd(*common, self.qk, self.saved, self.t["G"], self.dx, self.g, self.dgq, self.dgk, self.ws,
+                              stream)
 
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
 
     def grad_tensors(self):
-        return [self.dg_attn, self.dg_mlp, *self.grads.values()]
+        gains = [g for g in (self.dg_attn, self.dg_mlp, self.dgq, self.dgk) if g is not None]
+        return [*gains, *self.grads.values()]

@@ -219,3 +219,59 @@ def test_rotary_runner_refuses_mismatched_inputs():
             QkRotary(sh, dict(case, **{name: bad}), device="cpu")
     with pytest.raises(KeyError):
         QkRotary(dataclasses.replace(sh, layout="other"), case, device="cpu")
+
+
+def test_block_with_rotation_shape_rules_and_refusals(L):
+    dims = (1, 256, 2, 128, 344, 32, 48)
+    act = 256 * 256 * 2
+    assert L.lr_block_qk_saved_bytes(*dims) >= L.lr_block_saved_bytes(*dims) + 2 * act  # q' and k' too
+    assert L.lr_block_qk_workspace_bytes(*dims) >= L.lr_block_workspace_bytes(*dims)
+    assert L.lr_block_qk_saved_bytes(1, 200, 2, 128, 344, 32, 48) == 0  # s not a multiple of 256
+    assert L.lr_block_qk_workspace_bytes(1, 256, 2, 640, 344, 32, 48) == 0  # dh above 512
+    lib = L.lib()
+    w, g = L.lr_block_weights(), L.lr_block_grads()
+
+    def qk(H=2, dh=128, rot=64, sec=(32,), turns=P, pos=None, gq=P, gk=P):
+        return L.lr_block_qk(L.qk_shape(H, H, dh, rot, sec), turns, pos, gq, gk)
+
+    def fwd(q, dt=L.LR_BF16, eps=1e-6):
+        return lib.lr_block_qk_fwd(dt, *dims, eps, P, ctypes.byref(w), ctypes.byref(q) if q else None, P, P, 1 << 30, P,
+                                   1 << 30, None)
+
+    def bwd(q, dgq=P, dgk=P):
+        return lib.lr_block_qk_bwd(L.LR_BF16, *dims, 1e-6, P, ctypes.byref(w), ctypes.byref(q), P, 1 << 30, P, P,
+                                   ctypes.byref(g), dgq, dgk, P, 1 << 30, None)
+
+    assert fwd(qk(), dt=L.LR_F32) == 8
+    assert fwd(None) == 1
+    assert fwd(qk(H=1)) == 2 and "the block has" in L.lr_last_error()
+    assert fwd(qk(dh=64)) == 2
+    assert fwd(qk(rot=60, sec=(30,))) == 2
+    assert fwd(qk(turns=None)) == 1
+    assert fwd(qk(pos=P + 4)) == 3
+    assert fwd(qk(gq=P + 2)) == 3
+    assert fwd(qk(), eps=float("nan")) == 2
+    assert fwd(qk()) == 1 and "weight" in L.lr_last_error()  # the rotation is accepted, the weights are missing
+    assert bwd(qk(), dgq=None) == 1 and "dgq" in L.lr_last_error()
+    assert bwd(qk(), dgk=P + 4) == 3
+    assert bwd(qk(gq=None, gk=None), dgq=None, dgk=None) == 1 and "weight" in L.lr_last_error()
+
+
+def test_block_runner_refuses_a_rotation_of_other_sizes():
+    import dataclasses
+
+    from rank_bottleneck_block_gb300 import inputs as I
+    from rank_bottleneck_block_gb300.runner import TransformerBlock
+
+    shape = I.BlockShape(1, 256, 2, 128, 344, 32, 48)
+    case = dict(I.make_block_case(shape), freq=I.rotary_freq(128))
+    qk = I.QkShape(T=256, Hq=2, Hk=2, dh=128, rot=128, sec=(64,))
+    TransformerBlock(shape, case, device="cpu", qk=qk)
+    for bad in (dict(T=512), dict(Hk=1), dict(dh=64), dict(dtype="f32"), dict(rot=64, sec=(32,))):
+        with pytest.raises(ValueError):
+            TransformerBlock(shape, case, device="cpu", qk=dataclasses.replace(qk, **bad))
+    import torch
+
+    for bad in (dict(pos=torch.zeros(1, 256)), dict(gq=torch.ones(128)), dict(gk=torch.ones(64, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            TransformerBlock(shape, dict(case, **bad), device="cpu", qk=qk)

@@ -86,3 +86,37 @@ def test_clip_by_hand():
     assert out[2][1] == pytest.approx(0.8, rel=1e-6)
     assert Q.clip([np.array([3.0, 4.0])], 7.0)[1] == 1.0
     assert Q.clip([np.full(4, 1e200)], 1.0)[0] == pytest.approx(2e200)
+
+
+def test_block_gradients_match_finite_differences():
+    """The block with norm and rotation of q and k: dx, both norms' gains and sampled weights by central differences."""
+    rng = np.random.default_rng(3)
+    b, s, H, dh, f, ra, rm = 1, 4, 2, 8, 12, 6, 5
+    d, T, eps = H * dh, b * s, 1e-3
+    W = {"g_attn": 1 + 0.1 * rng.standard_normal(d), "g_mlp": 1 + 0.1 * rng.standard_normal(d)}
+    for n in "qkvo":
+        W[f"A_{n}"], W[f"B_{n}"] = rng.standard_normal((ra, d)) / d ** 0.5, rng.standard_normal((d, ra)) / ra ** 0.5
+    for n, i, o in (("gate", d, f), ("up", d, f), ("down", f, d)):
+        W[f"A_{n}"], W[f"B_{n}"] = rng.standard_normal((rm, i)) / i ** 0.5, rng.standard_normal((o, rm)) / rm ** 0.5
+    x, G = rng.standard_normal((T, d)), rng.standard_normal((T, d))
+    pos = np.stack([np.arange(T) % s, rng.integers(0, 9, T)])
+    rot = dict(theta=Q.angles(pos, [1.0, 0.3, 0.1], (2, 1)), rot=6, layout="half",
+               gq=1 + 0.1 * rng.standard_normal(dh), gk=1 + 0.1 * rng.standard_normal(dh))
+
+    def loss():
+        return float(np.sum(Q.block_fwd(x, W, rot, b, s, H, dh, eps)[0] * G))
+
+    gr = Q.block_bwd(W, Q.block_fwd(x, W, rot, b, s, H, dh, eps)[1], rot, G, b, s, H, dh, eps)
+    h = 1e-6
+    places = {"dx": x, "dgq": rot["gq"], "dgk": rot["gk"], "dg_attn": W["g_attn"]}
+    places.update({f"d{m}_{n}": W[f"{m}_{n}"] for m in "AB" for n in "qkv"})
+    for name, arr in places.items():
+        for i in rng.choice(arr.size, min(12, arr.size), replace=False):
+            idx = np.unravel_index(i, arr.shape)
+            keep = arr[idx]
+            arr[idx] = keep + h
+            up = loss()
+            arr[idx] = keep - h
+            down = loss()
+            arr[idx] = keep
+            assert gr[name][idx] == pytest.approx((up - down) / (2 * h), rel=2e-5, abs=2e-6), (name, idx)
