@@ -1440,11 +1440,22 @@ static lr_status qk_bwd_impl(const Ctx& c, const lr_qk_shape& sh, QkArgs& a, voi
   qk_ws_layout(a.dh, ws, &W);
   for (int i = 0; i < 2; ++i) a.t[i].part = W.part[i];
   const double rows = static_cast<double>(a.T) * a.dh;
-  LaunchScope scope("qk_bwd", c.st, 0,
-                    c.es * rows * (sh.Hq * (a.t[0].g ? 3.0 : 2.0) + sh.Hk * (a.t[1].g ? 3.0 : 2.0)));
   const bool adj = sh.layout == LR_PAIR_ADJACENT;
-  cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.sms, c.st) : launch_qk_bwd<float>(a, adj, c.sms, c.st);
-  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
+  QkPlan plan;
+  {
+    LaunchScope scope("qk_bwd", c.st, 0,
+                      c.es * rows * (sh.Hq * (a.t[0].g ? 3.0 : 2.0) + sh.Hk * (a.t[1].g ? 3.0 : 2.0)));
+    cudaError_t e = c.dt == LR_BF16 ? launch_qk_bwd<bf16>(a, adj, c.sms, &plan, c.st)
+                                    : launch_qk_bwd<float>(a, adj, c.sms, &plan, c.st);
+    if (e != cudaSuccess)
+      return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
+  }
+  if ((a.t[0].H && a.t[0].g) || (a.t[1].H && a.t[1].g)) {
+    LaunchScope scope("qk_dg", c.st, 0, 4.0 * a.dh * (plan.blocks[0] + plan.blocks[1]));
+    cudaError_t e = launch_qk_dg(a, plan, c.st);
+    if (e != cudaSuccess)
+      return fail(LR_ERR_CUDA, "query/key norm and rotation backward: %s", cudaGetErrorString(e));
+  }
   return LR_OK;
 }
 

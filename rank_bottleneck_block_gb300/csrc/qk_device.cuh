@@ -6,7 +6,9 @@
 // head by head, and computes its angles once per item; the 32 / G groups of a warp keep step.  Loads run kAhead steps
 // ahead of the arithmetic through a ring in shared memory (asynchronous copies; a thread reads back only what it
 // copied itself, so it waits for nothing but its own copies).  The arithmetic is on two pairs at a time (the f32x2
-// instructions).
+// instructions).  Steps that led here, 16384 tokens, 32 + 32 heads of 128, bf16, forward / backward: a warp per vector
+// with 2-byte loads 427 / 1000 us; lane groups with 16-byte loads, a warp's groups sharing a token 102 / 154; the ring
+// and f32x2 92 / 128; a token for each group, and more blocks than run at once 82 / 124.
 #pragma once
 
 #include <algorithm>
@@ -91,7 +93,7 @@ __device__ __forceinline__ Slot slot_of(const QkArgs& a) {
   s.axis_a = s.axis_b = s.turned ? axis_of(a, pair_of<ST, U, ADJ>(s, 0)) : 0;
   s.on_b = 0;
   s.more_axes = false;
-  if (s.turned) {
+  if (s.turned && a.sec_end[0] < a.rot / 2) {  // more axes than the first
 #pragma unroll
     for (int i = 1; i < U; ++i) {
       const int x = axis_of(a, pair_of<ST, U, ADJ>(s, i));
@@ -352,24 +354,28 @@ struct QkVariant {
 inline QkVariant variant(const QkArgs& a, size_t es) {
   const bool wide = a.dh % 16 == 0 && a.rot % 16 == 0 && (es == 2 || a.dh > 256);
   const int u = wide ? 8 : 4, slots = a.dh / (2 * u);
-  if (slots == 5 || slots == 9 || slots == 10) return {u, slots == 5 ? 5 : 10};  // 6 and 3 vectors a warp, not 4 and 2
+  // 6 and 3 vectors a warp, not 4 and 2: 16 + 2 heads of 72 in bf16, 40003 tokens: 46 us against 61
+  if (slots == 5 || slots == 9 || slots == 10) return {u, slots == 5 ? 5 : 10};
   return {u, slots <= 4 && es == 2 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32};
 }
 
 inline int cdiv(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 constexpr int kMostHeads = 16;  // of an item: past it the angles cost nothing any more
-constexpr int kWaveSteps = 10;  // heads a lane group takes at least, where the launch has more blocks than run at once
+constexpr int kMostWaves = 4;   // blocks of a launch for each that runs at once
+constexpr int kWaveSteps = 12;  // heads a lane group takes at least, where the launch has more blocks than run at once
 
 // Cuts each token's heads into items, and gives each tensor blocks by its share of the vectors.  Small launches: one
-// item a lane group, as short as fills the SMs.  Large ones: up to four blocks for each that runs at once, since SMs
-// do not get the same share of the memory's bandwidth and a block that ends early makes room for another.
+// item a lane group, as short as fills the SMs.  Large ones: up to kMostWaves blocks for each that runs at once, since
+// SMs do not get the same share of the memory's bandwidth and a block that ends early makes room for another (16384
+// tokens, 64 heads: 95 us with one block for each that runs at once, 90, 85 and 82 us with two, three and four; a launch
+// of 300,000 vectors gains nothing, 33 us either way, and pays for the blocks' starts).
 inline void cut(const QkArgs& a, int g, int resident, QkPlan* pl) {
   const long long groups = 32 / g * kWarps;  // of a block
   long long vectors[2];
   for (int i = 0; i < 2; ++i) vectors[i] = 1LL * a.T * a.t[i].H;
   const long long all = vectors[0] + vectors[1], each = (all + resident * groups - 1) / (resident * groups);
-  const long long waves = std::max(1LL, std::min(4LL, each / kWaveSteps));
+  const long long waves = std::max(1LL, std::min<long long>(kMostWaves, each / kWaveSteps));
   for (int i = 0; i < 2; ++i) {
     const int H = a.t[i].H;
     pl->chunks[i] = cdiv(H, std::min<long long>(kMostHeads, each));

@@ -1,10 +1,12 @@
-// Norm and rotation of queries and keys, forward.
+// Norm and rotation of queries and keys, forward: y = r R(theta) (x g), with R(theta) g kept as four products per pair
+// that are renewed once per item.
+// Bound by memory: x read, y written.  Measured, 16384 tokens, 32 + 32 heads of 128: bf16 537 MB in 81.5 us (6.59 TB/s,
+// 98% of the copy rate); 12483 tokens with three position axes, 20 + 4 heads: 153 MB in 28 us (82%: with so few heads
+// to a token the angles weigh more, and the instructions issue in 60% of the cycles).
 #include "qk_device.cuh"
 
 namespace lr {
 
-// ----------------------------------------------------------------- forward
-// y = r R(theta) (x g) with R(theta) g kept as four products per pair, renewed once per item.
 template <typename ST, int U, bool ADJ, int G, bool FULL>
 __global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_kernel(
     const __grid_constant__ QkArgs a, const __grid_constant__ QkPlan pl) {
@@ -45,52 +47,49 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_ke
   const float inv_dh = 1.f / static_cast<float>(a.dh);
   f2 A[U / 2], B[U / 2], C[U / 2], D[U / 2];
   const int steps = sh.rounds * sh.len;
-  for (int i = 0; i < steps; i += kRing) {
+#pragma unroll 1
+  for (int i = 0; i < steps; ++i) {
+    const int slot = i % kRing;
+    fetch((slot + kAhead) % kRing);
+    copies_wait<kAhead>();
+    if (h == 0) {
+      const Item it(sh, item, q.H);
+      out = static_cast<ST*>(q.out) + it.t * q.ldo + it.h0 * a.dh + sl.o;
+      heads = sl.on ? it.heads : 0;
+      item += sh.stride;
+      f2 gx[U / 2], gy[U / 2], c[U / 2], s[U / 2];
 #pragma unroll
-    for (int slot = 0; slot < kRing; ++slot) {
-      if (i + slot >= steps) break;
-      fetch((slot + kAhead) % kRing);
-      copies_wait<kAhead>();
-      if (h == 0) {
-        const Item it(sh, item, q.H);
-        out = static_cast<ST*>(q.out) + it.t * q.ldo + it.h0 * a.dh + sl.o;
-        heads = sl.on ? it.heads : 0;
-        item += sh.stride;
-        f2 gx[U / 2], gy[U / 2], c[U / 2], s[U / 2];
-#pragma unroll
-        for (int k = 0; k < U / 2; ++k) gx[k] = gy[k] = c[k] = both(1.f);
-        if (g && sl.on) get_pairs<ST, U, ADJ>(gain, sl, gx, gy);
-        if (sl.turned && heads > 0)
-          ring.template angles<ADJ>(slot, a, sl, it.t, c, s);
-#pragma unroll
-        for (int k = 0; k < U / 2; ++k) {
-          A[k] = gx[k] * c[k];
-          B[k] = gy[k] * -s[k];
-          C[k] = gx[k] * s[k];
-          D[k] = gy[k] * c[k];
-        }
-      }
-      f2 X[U / 2], Y[U / 2];
-      ring.template read<ADJ>(slot, 0, X, Y);
-      float r = 1.f;
-      if (g) {
-        f2 ss = both(0.f);
-#pragma unroll
-        for (int k = 0; k < U / 2; ++k) ss = fma2(X[k], X[k], fma2(Y[k], Y[k], ss));
-        r = rsqrtf(group_sum<G>(ss.x + ss.y) * inv_dh + a.eps);
-      }
-      const f2 r2 = both(r);
+      for (int k = 0; k < U / 2; ++k) gx[k] = gy[k] = c[k] = both(1.f);
+      if (g && sl.on) get_pairs<ST, U, ADJ>(gain, sl, gx, gy);
+      if (sl.turned && heads > 0) ring.template angles<ADJ>(slot, a, sl, it.t, c, s);
 #pragma unroll
       for (int k = 0; k < U / 2; ++k) {
-        const f2 x = X[k] * r2, y = Y[k] * r2;
-        const f2 p = x * A[k], q = y * D[k];  // all of it where the slot is not turned
-        X[k] = pick2<FULL>(sl.turned, fma2(y, B[k], p), p);
-        Y[k] = pick2<FULL>(sl.turned, fma2(x, C[k], q), q);
+        A[k] = gx[k] * c[k];
+        B[k] = gy[k] * -s[k];
+        C[k] = gx[k] * s[k];
+        D[k] = gy[k] * c[k];
       }
-      if (h < heads) put_pairs<ST, U, ADJ>(out, sl, X, Y);
-      out += a.dh;
-      if (++h == sh.len) h = 0;
     }
+    f2 X[U / 2], Y[U / 2];
+    ring.template read<ADJ>(slot, 0, X, Y);
+    float r = 1.f;
+    if (g) {
+      f2 ss = both(0.f);
+#pragma unroll
+      for (int k = 0; k < U / 2; ++k) ss = fma2(X[k], X[k], fma2(Y[k], Y[k], ss));
+      r = rsqrtf(group_sum<G>(ss.x + ss.y) * inv_dh + a.eps);
+    }
+    const f2 r2 = both(r);
+#pragma unroll
+    for (int k = 0; k < U / 2; ++k) {
+      const f2 x = X[k] * r2, y = Y[k] * r2;
+      const f2 p = x * A[k], q = y * D[k];  // all of it where the slot is not turned
+      X[k] = pick2<FULL>(sl.turned, fma2(y, B[k], p), p);
+      Y[k] = pick2<FULL>(sl.turned, fma2(x, C[k], q), q);
+    }
+    if (h < heads) put_pairs<ST, U, ADJ>(out, sl, X, Y);
+    out += a.dh;
+    if (++h == sh.len) h = 0;
   }
 }
 

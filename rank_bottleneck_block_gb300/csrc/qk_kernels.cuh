@@ -45,8 +45,10 @@ struct QkPlan {
 // adjacent: pairs are channels (2p, 2p + 1), else (p, p + rot / 2).
 template <typename ST>
 cudaError_t launch_qk_fwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st);
-// Writes dx of both tensors and the partial sums of dg, then dg.
+// Writes dx of both tensors and the partial sums of dg (`plan`: how it cut the work) ...
 template <typename ST>
-cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, int sms, cudaStream_t st);
+cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, int sms, QkPlan* plan, cudaStream_t st);
+// ... and this adds them up.
+cudaError_t launch_qk_dg(const QkArgs& a, const QkPlan& plan, cudaStream_t st);
 
 }  // namespace lr

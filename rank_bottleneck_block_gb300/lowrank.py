@@ -441,9 +441,11 @@ def lr_qk_bwd(dt, T, sh: lr_qk_shape, eps, turns, pos, gq, gk, q, ldq, k, ldk, d
                            _nbytes(ws), _stream(stream)))
 
 
-def tensor_list(ts):
-    """A list of tensors as the host arrays lr_grad_norm and lr_grad_clip take: (pointers, element counts)."""
-    return _ptrs(ts), (ctypes.c_longlong * len(ts))(*[t.numel() for t in ts])
+def tensor_list(ts, numel=None):
+    """A list of tensors (or of pointers, with their element counts) as the host arrays that lr_grad_norm and
+    lr_grad_clip take: (pointers, element counts)."""
+    counts = [t.numel() for t in ts] if numel is None else numel
+    return _ptrs(ts), (ctypes.c_longlong * len(counts))(*counts)
 
 
 def lr_grad_workspace_bytes(n) -> int:

@@ -29,15 +29,11 @@ def _buf(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=_U8, device=device)
 
 
-def _span(t: torch.Tensor):
-    return t.data_ptr(), t.data_ptr() + L._nbytes(t)
-
-
 class GradClip:
     """The norm over a list of gradient tensors, and the tensors scaled to at most max_norm.
 
     grads: contiguous tensors of one type (fp32 as the backward passes write them, or bf16) on one
-    device, 16-byte aligned; outs: where the scaled tensors go (None: in place).  norm() leaves the
+    device, 16-byte aligned; outs: where the scaled tensors go (None: in place).  measure() leaves the
     norm in self.norm [1]; clip() leaves it there, min(1, max_norm / (norm + 1e-6)) in self.scale [1]
     and the scaled gradients in outs.  Device tensors: nothing waits for the GPU.
     """
@@ -51,24 +47,26 @@ class GradClip:
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients but {len(self.outs)} outputs")
         first = self.grads[0]
-        for g, o in zip(self.grads, self.outs):
-            for t in (g, o):
-                if t.dtype != first.dtype or t.device != first.device or not t.is_contiguous():
-                    raise ValueError("gradients and outputs must be contiguous, of one type and on one device")
-            if o.numel() != g.numel():
-                raise ValueError(f"an output has {o.numel()} elements, its gradient {g.numel()}")
-        self.dt = L.dtype_code(first)
+        self.dt, es = L.dtype_code(first), first.element_size()
+        for t in self.grads if outs is None else self.grads + self.outs:
+            if t.dtype != first.dtype or t.device != first.device or not t.is_contiguous():
+                raise ValueError("gradients and outputs must be contiguous, of one type and on one device")
+        n = [t.numel() for t in self.grads]
+        to = at = [t.data_ptr() for t in self.grads]
+        if outs is not None:
+            to = [t.data_ptr() for t in self.outs]
+            if [t.numel() for t in self.outs] != n:
+                raise ValueError("an output has another number of elements than its gradient")
         # a written tensor is its own gradient, or overlaps nothing else of either list
-        spans = sorted([(*_span(o), 1) for o in self.outs if o.numel()] +
-                       [(*_span(g), 0) for g, o in zip(self.grads, self.outs)
-                        if g.numel() and o.data_ptr() != g.data_ptr()])
+        spans = [(o, o + k * es, 1) for o, k in zip(to, n) if k]
+        spans += [(g, g + k * es, 0) for g, o, k in zip(at, to, n) if k and g != o]
         end = written = 0  # the furthest end so far, of any span and of a written one
-        for lo, hi, w in spans:
+        for lo, hi, w in sorted(spans):
             if lo < (end if w else written):
                 raise ValueError("an output overlaps another output or another gradient")
             end, written = max(end, hi), max(written, hi if w else 0)
-        self._g, self._n = L.tensor_list(self.grads)
-        self._o = self._g if outs is None else L.tensor_list(self.outs)[0]
+        self._g, self._n = L.tensor_list(at, n)
+        self._o = self._g if outs is None else L.tensor_list(to, n)[0]
         self.stat = torch.zeros(2, dtype=torch.float32, device=first.device)
         self.norm, self.scale = self.stat[:1], self.stat[1:]
         self.ws = _buf(L.lr_grad_workspace_bytes(len(self.grads)), first.device)

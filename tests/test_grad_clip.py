@@ -102,6 +102,50 @@ def test_more_tensors_than_one_launch_takes():
     _check(keep, empty, c, 0.25)
 
 
+def test_lists_without_elements():
+    from rank_bottleneck_block_gb300.runner import GradClip
+
+    for n in (1, 16, 17, 300, 1500):
+        c = GradClip([torch.empty(0, device="cuda") for _ in range(n)], 1.0)
+        c.stat.fill_(-1.0)
+        c.clip()
+        assert float(c.norm) == 0.0 and float(c.scale) == 1.0
+
+
+@pytest.mark.parametrize("n", [31 * 8192, 32 * 8192, 32 * 8192 + 1, 40 * 8192, 512 * 8192 + 5, 2100 * 8192])
+def test_around_the_borders_of_the_kernels_choices(n):
+    """One cluster up to 32 chunks of 32 KB, blocks that add the partial sums up themselves, a launch for that."""
+    from rank_bottleneck_block_gb300.runner import GradClip
+
+    for dtype, m in ((torch.float32, n), (torch.bfloat16, 2 * n)):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(n)
+        g = torch.randn(m, generator=gen, device="cuda").to(dtype)
+        out = torch.empty_like(g)
+        c = GradClip([g[:m // 2 // 8 * 8], g[m // 2 // 8 * 8:]], 3.0, [out[:m // 2 // 8 * 8], out[m // 2 // 8 * 8:]])
+        c.clip()
+        norm = float(g.double().square().sum().sqrt())
+        assert abs(float(c.norm) - norm) <= 34 * U * norm
+        want = g.double() * (3.0 / (norm + 1e-6))
+        assert ((out.double() - want).abs() <= (HALF[dtype] + 40 * U) * want.abs() + 1e-40).all()
+
+
+def test_a_tensor_of_more_than_2_to_the_31_elements():
+    from rank_bottleneck_block_gb300.runner import GradClip
+
+    n = (1 << 31) + 12345
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[-1] = 64.0
+    c = GradClip([torch.ones(8, dtype=torch.bfloat16, device="cuda"), g], 1.0)
+    c.clip()
+    norm = (8 + (n - 1) * 0.25 + 4096.0) ** 0.5
+    assert abs(float(c.norm) - norm) <= 34 * U * norm
+    want = torch.tensor([0.5 / norm, 64.0 / norm], dtype=torch.float64)
+    got = torch.stack([g[-2], g[-1]]).double().cpu()
+    assert ((got - want).abs() <= (HALF[torch.bfloat16] + 40 * U) * want).all()
+    assert (g[:-1] == g[0]).all()
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e-19, 1e15, 1e18, 1e25, 1e37])
 def test_squares_beyond_the_fp32_range_are_kept(scale):
     from rank_bottleneck_block_gb300.runner import GradClip

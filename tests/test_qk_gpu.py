@@ -90,6 +90,13 @@ SHAPES = [
     _shape(5, 100, 1, 16),
     _shape(1000, 16, 4, 128),
     _shape(7, 3, 2, 248, 8, layout="pairs"),
+    _shape(31, 7, 3, 40),                                   # 5, 9 and 10 lanes to a vector
+    _shape(29, 5, 2, 80, 80, 2),
+    _shape(45, 3, 1, 144, 96, 3, layout="pairs"),
+    _shape(23, 4, 2, 160),
+    _shape(21, 3, 1, 16, 16, 4),                            # more than two axes in one lane
+    _shape(21, 3, 1, 64, 24, 4, layout="pairs"),
+    _shape(11, 2, 2, 336, 320, 4, layout="pairs"),
 ]
 
 
@@ -270,6 +277,65 @@ def test_repeats_bitwise_and_in_a_graph_and_on_another_stream():
     run.step(side)
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(ref, outs()))
+
+
+def test_sections_of_no_pairs():
+    """An axis may own no pairs: the others' positions alone count."""
+    from rank_bottleneck_block_gb300.runner import QkRotary
+
+    for sec in ((0, 32), (32, 0), (0, 0, 32), (5, 0, 20, 7)):
+        shape = dataclasses.replace(_shape(19, 2, 1, 64, dtype="f32"), sec=sec)
+        case = I.make_qk_case(shape, seed=14)
+        run = QkRotary(shape, case)
+        run.step()
+        _check_fwd(shape, case, run.qo, run.ko)
+        _check_bwd(shape, case, run)
+
+
+def test_launches_are_counted():
+    from rank_bottleneck_block_gb300 import lowrank as L
+    from rank_bottleneck_block_gb300.runner import QkRotary
+
+    shape = _shape(40, 4, 2, 64)
+    for norm, want in ((True, 3), (False, 2)):
+        run = QkRotary(shape, I.make_qk_case(shape, seed=15, norm=norm))
+        before = L.lr_launch_count()
+        run.step()
+        assert L.lr_launch_count() - before == want
+    L.lr_profile_start()
+    run.step()
+    assert {"qk_fwd", "qk_bwd"} <= set(L.lr_profile_stop())
+
+
+def test_rows_past_2_to_the_31_elements():
+    """Rows so far apart that the last ones start past element 2^31 of their tensor."""
+    from rank_bottleneck_block_gb300 import lowrank as L
+
+    T, dh, ld = 40000, 64, 65536
+    shape = _shape(T, 1, 0, dh, seq=T)
+    case = I.make_qk_case(shape, seed=16)
+    wide = [torch.empty(T, ld, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for m, n in zip(wide, ("q", "dqo")):
+        m[:, :dh] = case[n].cuda()
+    sh = L.qk_shape(1, 0, dh, dh, (dh // 2,), seq=T)
+    turns, g = L.turns_tensor(case["freq"], "cuda"), case["gq"].cuda()
+    dg = torch.empty(dh, device="cuda")
+    ws = torch.empty(L.lr_qk_bwd_workspace_bytes(L.LR_BF16, T, sh), dtype=torch.uint8, device="cuda")
+    x, d = wide
+    L.lr_qk_bwd(L.LR_BF16, T, sh, shape.eps, turns, None, g, None, x, ld, None, 0, d, ld, None, 0, d, ld, None, 0, dg, None,
+                ws)
+    L.lr_qk_fwd(L.LR_BF16, T, sh, shape.eps, turns, None, g, None, x, ld, None, 0, x, ld, None, 0)
+    rows = I.sample_rows(T, 64)
+    part = dataclasses.replace(shape, T=len(rows))
+    sub = {n: case[n][rows] for n in ("q", "dqo")}
+    sub.update(gq=case["gq"], freq=case["freq"])
+    pos = rows.numpy()[None]
+    _check_fwd(part, sub, x[:, :dh][rows.cuda()], None, pos)
+    th = Q.angles(pos, case["freq"], shape.sec)
+    args = (dh, dh, "half", shape.eps)
+    want = Q.qk_bwd(as64(sub["q"]), as64(case["gq"]), th, as64(sub["dqo"]), *args)
+    mag = Q.magnitudes(as64(sub["q"]), as64(case["gq"]), as64(sub["dqo"]), *args)
+    _close(d[:, :dh][rows.cuda()], want["dx"], mag["dx"], "bf16", 100, "dq")
 
 
 def test_two_runs_at_once_on_two_streams():
