@@ -1,11 +1,16 @@
 // Both passes are bound by memory: a thread has 128 bytes in flight (16-byte loads), a block takes consecutive chunks of
 // the tensors' concatenation, and there are several times as many blocks as run at once, since SMs do not get the same
 // share of the bandwidth.  The scaling pass goes through the chunks backwards, so that it finds in L2 what the sum
-// read last.
+// read last: all but the last 64 MB of the sum's reads and all of the outputs are marked to leave L2 first.
+// Measured, fp32, clipped into other tensors: 283 million elements (168 tensors) 478 us, of which the sum 154 us
+// (1.13 GB at 7.3 TB/s); 80 million (16 tensors) 135 us; what both passes move at the copy rate is 509 and 144 us
+// less the part found in L2, and reading and writing once would be 339 and 96 us.  20 million bf16 elements in 613
+// tensors of uneven sizes 21 us; 181,000 fp32 elements in one launch 5 us.
 #include "grad_kernels.cuh"
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cfloat>
 
 namespace lr {
@@ -207,10 +212,9 @@ __global__ void __launch_bounds__(kThreads) grad_stat_kernel(const __grid_consta
   scale_of(gs, true);
 }
 
-constexpr int kScaleEach = 2;  // chunks of a block
 template <typename ST, int N>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ GradTable<N> tab,
-                                                              const __grid_constant__ GradStat gs, bool in_place) {
+                                                              const __grid_constant__ GradStat gs, int each, bool in_place) {
   pdl_wait();
   pdl_trigger();
   float scale = 1.f;
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
     scale = scale_of(gs, blockIdx.x == 0);
     if (scale == 1.f) return;  // nothing changes
   }
-  const int c1 = tab.first[tab.n] - blockIdx.x * kScaleEach, c0 = max(0, c1 - kScaleEach);
+  const int c1 = tab.first[tab.n] - blockIdx.x * each, c0 = max(0, c1 - each);
   int i = owner_of(tab, c0);
   bool known = in_place;
   for (int ch = c0; ch < c1; ++ch) {
@@ -291,7 +295,11 @@ cudaError_t launch_grad_stat(const GradStat& gs, cudaStream_t st) {
 
 template <typename ST, int N>
 cudaError_t launch_grad_scale(const GradTable<N>& tab, const GradStat& gs, bool in_place, cudaStream_t st) {
-  return launch_pdl(grad_scale_kernel<ST, N>, dim3(grad_blocks(tab.first[tab.n], kScaleEach)), dim3(kThreads), 0, st, tab, gs,
+  // Chunks of a block.  In place the launch often finds a scale of 1, and then only starts and ends its blocks: of 283
+  // million fp32 elements, two chunks to a block take 169 us with the sum (484 where they are scaled), four 161 (488).
+  constexpr int kInPlaceEach = 4;
+  const int chunks = tab.first[tab.n], each = in_place ? std::min(kInPlaceEach, std::max(2, chunks / 2432)) : 2;
+  return launch_pdl(grad_scale_kernel<ST, N>, dim3(grad_blocks(chunks, each)), dim3(kThreads), 0, st, tab, gs, each,
                     in_place);
 }
 

@@ -11,7 +11,7 @@ namespace lr {
 constexpr int kGradTable = 1024;        // most tensors of one launch
 constexpr int kGradOwners = 256;        // entries that say where to look for a chunk's tensor
 constexpr int kGradChunkBytes = 32768;  // what 256 threads take at a time (8 16-byte words each)
-constexpr int kGradParts = 4096;        // most blocks of one launch, each writing one partial sum
+constexpr int kGradParts = 3040;        // most blocks of one launch that sums, each writing one partial sum
 constexpr int kGradFew = 512;           // partial sums that the scaling blocks add up themselves
 constexpr int kGradKeepBytes = 64 << 20;  // the last of the sum's reads, which the scaling finds in L2
 constexpr int kGradSmall = 32;          // chunks that one cluster sums and scales in one launch
