@@ -7,6 +7,7 @@ is a call into liblowrank.so through the ctypes binding.
 """
 from __future__ import annotations
 
+import operator
 from typing import Dict, List, Optional, Sequence
 
 import torch
@@ -96,8 +97,9 @@ class _Clipped:
 
     def clip_grads(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale every gradient in place so that their common norm is at most max_norm; the norm [1]."""
-        if self._clip is None:
-            self._clip = GradClip(self.grad_tensors())
+        grads = self.grad_tensors()
+        if self._clip is None or not all(map(operator.is_, self._clip.grads, grads)):
+            self._clip = GradClip(grads)
         self._clip.max_norm = float(max_norm)
         return self._clip.clip(stream)
 
@@ -255,7 +257,7 @@ class HostPipeline:
         comp.wait_stream(self.h2d)
 
 
-class ProjGroup:
+class ProjGroup(_Clipped):
     """A group of low-rank pairs sharing one input, optionally behind an RMSNorm."""
 
     def __init__(self, shape: ProjShape, case: Dict[str, object], device="cuda", act: int = L.LR_ACT_SILU):
@@ -298,6 +300,9 @@ class ProjGroup:
     def step(self, stream=None):
         self.forward(stream)
         self.backward(stream)
+
+    def grad_tensors(self):
+        return [t for t in (self.dg, *self.dA, *self.dB) if t is not None]
 
 
 class BlockStack(_Clipped):

@@ -155,3 +155,15 @@ def test_the_pieces_one_after_another_are_the_block():
     # y is rounded to bf16 before the residual here (2^-8 of |y|, which is below the output's scale), and the
     # block adds it to x in fp32: the outputs agree to a few bf16 roundings
     assert C.metrics(out, blk.out.float().cpu().numpy())["maxrel"] < 2e-2
+
+
+def test_the_readme_example_runs():
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    code = re.search(r"and clipping:\n\n((?:    .*\n|\n)+)", text).group(1)
+    names = {}
+    exec("\n".join(line[4:] for line in code.splitlines()), names)
+    assert torch.isfinite(names["norm"]).all() and torch.isfinite(names["blk"].dx.float()).all()

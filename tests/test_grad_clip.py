@@ -248,3 +248,25 @@ def test_the_mlp_block_clips_its_gradients():
     stack.clip_grads(1e-3)
     assert len(keep) == 21
     _check(keep, stack.grad_tensors(), stack._clip, 1e-3)
+
+
+def test_clipping_follows_replaced_gradients_and_covers_the_group():
+    from rank_bottleneck_block_gb300 import inputs as I
+    from rank_bottleneck_block_gb300.runner import MlpBlock, ProjGroup
+
+    shape = I.MlpShape(T=128, d=256, f=688, r=64, dtype="f32")
+    blk = MlpBlock(shape, I.make_mlp_case(shape, seed=0))
+    blk.step()
+    blk.clip_grads(1.0)
+    blk.grads["dA_up"] = torch.empty_like(blk.grads["dA_up"])
+    blk.step()
+    keep = [t.clone() for t in blk.grad_tensors()]
+    blk.clip_grads(1.0)
+    _check(keep, blk.grad_tensors(), blk._clip, 1.0)
+    shape = I.ProjShape(T=100, d_in=128, d_out=64, r=32, group=2)
+    group = ProjGroup(shape, I.make_proj_case(shape, seed=1))
+    group.step()
+    keep = [t.clone() for t in group.grad_tensors()]
+    assert len(keep) == 5
+    group.clip_grads(0.5)
+    _check(keep, group.grad_tensors(), group._clip, 0.5)
