@@ -1419,6 +1419,7 @@ static QkArgs qk_args(int T, const lr_qk_shape& sh, float eps, const unsigned lo
   a.rot = sh.rot;
   a.seq = sh.seq;
   a.eps = eps;
+  a.inv_dh = 1.f / static_cast<float>(sh.dh);
   int end = 0;
   for (int i = 0; i < kQkMaxAxes - 1; ++i) {
     if (i < sh.axes) end += sh.sec[i];

@@ -12,8 +12,6 @@ namespace lr {
 template <typename ST, int U, bool ADJ, int G, bool FULL>
 __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_kernel(
     const __grid_constant__ QkArgs a, const __grid_constant__ QkPlan pl) {
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ __align__(16) unsigned char smem[];
   Ring<ST, U, 4>& ring = *reinterpret_cast<Ring<ST, U, 4>*>(smem);
   const int sub = threadIdx.x % 32 / G;
@@ -21,6 +19,8 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_ke
   const QkTensor& q = a.t[sh.which];
   const Slot sl = slot_of<ST, U, ADJ, G, FULL>(a);
   const ST* g = static_cast<const ST*>(q.g);
+  pdl_wait();  // what comes before reads nothing but the arguments
+  pdl_trigger();
   unsigned in_item = sh.item, item = sh.item;
   int in_left = sh.rounds, in_h = 0, in_heads = 0, h = 0, heads = 0;
   const ST *in = nullptr, *in_x = nullptr;
@@ -52,7 +52,6 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_ke
   for (int i = 0; i < kAhead; ++i) fetch(i);
   const ST* gain = ring.fill(a, g, sl);
   __syncthreads();
-  const float inv_dh = 1.f / static_cast<float>(a.dh);
   f2 gx[U / 2], gy[U / 2], dgx[U / 2], dgy[U / 2], c[U / 2], s[U / 2];
 #pragma unroll
   for (int k = 0; k < U / 2; ++k) {
@@ -91,8 +90,8 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(U, sizeof(ST))) qk_bwd_ke
         dot = fma2(U0[k] * gx[k], X[k], fma2(V0[k] * gy[k], Y[k], dot));
       }
       const float sum = group_sum<G>(ss.x + ss.y), wx = group_sum<G>(dot.x + dot.y);
-      const float r = rsqrtf(sum * inv_dh + a.eps);
-      const f2 r2 = both(r), m = both(-wx * inv_dh * r);
+      const float r = rsqrtf(sum * a.inv_dh + a.eps);
+      const f2 r2 = both(r), m = both(-wx * a.inv_dh * r);
 #pragma unroll
       for (int k = 0; k < U / 2; ++k) X[k] = X[k] * r2, Y[k] = Y[k] * r2;
       if (on) {

@@ -315,18 +315,20 @@ struct Ring {
 
 // A block's items: the lane group's first one, their distance, and how many rounds of them.
 struct Share {
-  int which, rounds, len, chunks;
-  unsigned block, item, stride, items;
+  int which, rounds, len, chunks, shift;
+  unsigned block, item, stride, items, magic;
   __device__ __forceinline__ Share(const QkArgs& a, const QkPlan& pl, int P, int sub) {
     which = blockIdx.x < static_cast<unsigned>(pl.blocks[0]) ? 0 : 1;
     block = blockIdx.x - (which ? pl.blocks[0] : 0);
     len = pl.len[which];
     chunks = pl.chunks[which];
+    shift = pl.shift[which];
+    magic = pl.magic[which];
     items = static_cast<unsigned>(chunks) * a.T;
     const unsigned first = block * kWarps * P;  // the same rounds for all warps of a block
     stride = pl.blocks[which] * kWarps * P;
     item = first + threadIdx.x / 32 * P + sub;
-    rounds = first < items ? (items - first + stride - 1) / stride : 0;
+    rounds = pl.rounds[which] - (first + (pl.rounds[which] - 1) * stride >= items);
   }
 };
 
@@ -337,7 +339,7 @@ struct Item {
     t = static_cast<int>(item);
     h0 = 0;
     if (sh.chunks > 1) {
-      t = static_cast<int>(item / sh.chunks);
+      t = static_cast<int>(__umulhi(item, sh.magic) >> sh.shift);
       h0 = static_cast<int>(item - static_cast<unsigned>(t) * sh.chunks) * sh.len;
     }
     heads = item < sh.items ? min(sh.len, H - h0) : 0;
@@ -383,6 +385,12 @@ inline void cut(const QkArgs& a, int g, int resident, QkPlan* pl) {
     const long long want = (vectors[i] * resident * waves + all / 2) / all;
     const long long room = (1LL * a.T * pl->chunks[i] + groups - 1) / groups;
     pl->blocks[i] = static_cast<int>(std::min(std::max(want, 1LL), room));
+    pl->rounds[i] = pl->blocks[i] ? cdiv(room, pl->blocks[i]) : 0;
+    // 2^(31 + L) / chunks rounded up, L = log2 of chunks rounded up: exact for 31-bit dividends
+    int log = 1;
+    while ((1LL << log) < pl->chunks[i]) ++log;
+    pl->shift[i] = log - 1;
+    pl->magic[i] = pl->chunks[i] > 1 ? static_cast<unsigned>(((1ULL << (31 + log)) + pl->chunks[i] - 1) / pl->chunks[i]) : 0;
   }
 }
 

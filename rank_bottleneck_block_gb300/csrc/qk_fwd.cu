@@ -10,14 +10,14 @@ namespace lr {
 template <typename ST, int U, bool ADJ, int G, bool FULL>
 __global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_kernel(
     const __grid_constant__ QkArgs a, const __grid_constant__ QkPlan pl) {
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ __align__(16) unsigned char smem[];
   Ring<ST, U, 2>& ring = *reinterpret_cast<Ring<ST, U, 2>*>(smem);
   const Share sh(a, pl, 32 / G, threadIdx.x % 32 / G);
   const QkTensor& q = a.t[sh.which];
   const Slot sl = slot_of<ST, U, ADJ, G, FULL>(a);
   const ST* g = static_cast<const ST*>(q.g);
+  pdl_wait();  // what comes before reads nothing but the arguments
+  pdl_trigger();
   unsigned in_item = sh.item, item = sh.item;
   int in_left = sh.rounds, in_h = 0, in_heads = 0, h = 0, heads = 0;
   const ST* in = nullptr;
@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_ke
   for (int i = 0; i < kAhead; ++i) fetch(i);
   const ST* gain = ring.fill(a, g, sl);
   __syncthreads();
-  const float inv_dh = 1.f / static_cast<float>(a.dh);
   f2 A[U / 2], B[U / 2], C[U / 2], D[U / 2];
   const int steps = sh.rounds * sh.len;
 #pragma unroll 1
@@ -77,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, fwd_blocks(U, sizeof(ST))) qk_fwd_ke
       f2 ss = both(0.f);
 #pragma unroll
       for (int k = 0; k < U / 2; ++k) ss = fma2(X[k], X[k], fma2(Y[k], Y[k], ss));
-      r = rsqrtf(group_sum<G>(ss.x + ss.y) * inv_dh + a.eps);
+      r = rsqrtf(group_sum<G>(ss.x + ss.y) * a.inv_dh + a.eps);
     }
     const f2 r2 = both(r);
 #pragma unroll

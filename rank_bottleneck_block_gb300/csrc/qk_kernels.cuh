@@ -34,12 +34,14 @@ struct QkArgs {
   const int* pos;                   // [axes, T], or null: position t mod seq on every axis
   int T, dh, rot, seq;
   int sec_end[kQkMaxAxes - 1];      // first pair past axis 0, 1, 2 (rot / 2 when the axis is the last)
-  float eps;
+  float eps, inv_dh;
 };
 
-// How a launch cuts its work, for q and for k: blocks, and each token's heads into `chunks` items of `len` heads.
+// How a launch cuts its work, for q and for k: blocks, the items of a lane group at most, and each token's heads into
+// `chunks` items of `len` heads; item / chunks is the high word of item * magic, shifted (items are below 2^31).
 struct QkPlan {
-  int blocks[2], chunks[2], len[2];
+  int blocks[2], rounds[2], chunks[2], len[2], shift[2];
+  unsigned magic[2];
 };
 
 // adjacent: pairs are channels (2p, 2p + 1), else (p, p + rot / 2).

@@ -176,26 +176,30 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
-def _raw_stream():
-    """The function that names a device's current stream, without making a Stream object where torch has one."""
-    import torch
-
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_torch_cuda = None  # (current device, its current stream's handle)
 
 
-_current = None
+def _lookups():
+    """torch's functions that name the current device and a device's current stream, the latter without making a
+    Stream object where torch has one that does not."""
+    global _torch_cuda
+    if _torch_cuda is None:
+        import torch
+
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch_cuda = (torch.cuda.current_device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _torch_cuda
+
+
+def _current_device() -> int:
+    return _lookups()[0]()
 
 
 def _stream(stream) -> Optional[int]:
-    global _current
     if stream is None:
-        import torch
-
-        if _current is None:
-            torch.cuda.init()
-            _current = (torch.cuda.current_device, _raw_stream())
-        return _current[1](_current[0]())
+        device, raw = _lookups()
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -226,7 +230,8 @@ def pair_grad(dA, dB) -> lr_pair_grad:
 
 class Prepared:
     """An entry point with every argument but the stream converted once, for callers that repeat a call on the
-    same buffers: call(stream).  It keeps its arguments, so the tensors whose pointers it holds stay alive."""
+    same buffers: call(stream).  It keeps its arguments, so the tensors whose pointers it holds stay alive.  The
+    tensors must be on one GPU, and that GPU must be the current one when the call is made."""
 
     def __init__(self, name: str, *args):
         self._fn, self._keep = getattr(lib(), name), args
@@ -234,8 +239,15 @@ class Prepared:
         if len(types) != len(args):
             raise TypeError(f"{name}: {len(args)} arguments, {len(types)} needed before the stream")
         self._args = tuple(_typed(t, a) for t, a in zip(types, args))
+        devices = {a.device for a in args if hasattr(a, "data_ptr")}
+        if len(devices) > 1:
+            raise ValueError(f"{name}: tensors on several devices: {sorted(map(str, devices))}")
+        self._device = next(iter(devices)) if devices else None
 
     def __call__(self, stream=None) -> None:
+        device, current = self._device, _current_device()
+        if device is not None and device.index != current:
+            raise ValueError(f"tensors on {device}, but the current device is cuda:{current}")
         status = self._fn(*self._args, _stream(stream))
         if status:
             _check(status)

@@ -292,6 +292,24 @@ def test_sections_of_no_pairs():
         _check_bwd(shape, case, run)
 
 
+def test_tensors_elsewhere_are_refused():
+    """Buffers that are not on the current GPU are refused before anything is launched."""
+    from rank_bottleneck_block_gb300 import lowrank as L
+    from rank_bottleneck_block_gb300.runner import GradClip, QkRotary
+
+    shape = _shape(5, 2, 1, 64)
+    case = I.make_qk_case(shape, seed=18)
+    run = QkRotary(shape, case, device="cpu")
+    before = L.lr_launch_count()
+    with pytest.raises(ValueError, match="current device"):
+        run.forward()
+    with pytest.raises(ValueError, match="current device"):
+        GradClip([torch.zeros(64)]).clip()
+    assert L.lr_launch_count() == before
+    with pytest.raises(ValueError, match="several devices"):
+        L.Prepared("lr_grad_norm", L.LR_F32, 0, None, None, torch.zeros(4, device="cuda"), torch.zeros(4), 16)
+
+
 def test_launches_are_counted():
     from rank_bottleneck_block_gb300 import lowrank as L
     from rank_bottleneck_block_gb300.runner import QkRotary
@@ -336,6 +354,35 @@ def test_rows_past_2_to_the_31_elements():
     want = Q.qk_bwd(as64(sub["q"]), as64(case["gq"]), th, as64(sub["dqo"]), *args)
     mag = Q.magnitudes(as64(sub["q"]), as64(case["gq"]), as64(sub["dqo"]), *args)
     _close(d[:, :dh][rows.cuda()], want["dx"], mag["dx"], "bf16", 100, "dq")
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured backward passes with one workspace, replayed one after the other on one stream."""
+    from rank_bottleneck_block_gb300 import lowrank as L
+    from rank_bottleneck_block_gb300.runner import GraphStep, QkRotary
+
+    runs = [QkRotary(s, I.make_qk_case(s, seed=17)) for s in (_shape(500, 6, 2, 128), _shape(90, 3, 3, 64, 48, 2))]
+    ref = []
+    for r in runs:
+        r.backward()
+        ref.append([t.clone() for t in (r.dq, r.dk, r.dgq, r.dgk)])
+    ws = max((r.ws for r in runs), key=lambda t: t.numel())
+
+    def call(r):
+        rows = [v for t in (r.dqo, r.dko, r.dq, r.dk) for v in (t, t.stride(0))]
+        s = r.s
+        return lambda: L.lr_qk_bwd(r.dt, s.T, r.sh, s.eps, r.turns, r.pos, r.gq, r.gk, r.q, r.q.stride(0), r.k,
+                                   r.k.stride(0), *rows, r.dgq, r.dgk, ws)
+
+    graphs = [GraphStep(call(r)) for r in runs]
+    for _ in range(3):
+        for r in runs:
+            for t in (r.dq, r.dk, r.dgq, r.dgk):
+                t.zero_()
+        for g in graphs:
+            g()
+        for r, want in zip(runs, ref):
+            assert all(torch.equal(a, b) for a, b in zip(want, (r.dq, r.dk, r.dgq, r.dgk)))
 
 
 def test_two_runs_at_once_on_two_streams():
