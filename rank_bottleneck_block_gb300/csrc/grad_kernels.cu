@@ -102,7 +102,8 @@ struct Part {
   }
   // Adds the squares to the warp's sum: lane 0's, but for what the slow path and the tail leave in other lanes
   // (`spread`).  The warp's words are summed in fp32 (16 or 32 in a row, then pairwise), and from there on in fp64; where
-  // that sum is no number, beyond fp32 or so small that squares have lost digits, the same squares are summed in fp64.
+  // that sum is no number, beyond fp32 or so small that squares have lost digits, the same squares are summed in fp64
+  // (2048 squares and sums below 2^-126 are off by 2^-139 together: a 2^-29th of 2^-110).
   __device__ __forceinline__ void add_squares(const ST* g, double& sum, bool& spread) const {
     float a = 0.f, b = 0.f;
     int k = 0;
@@ -113,7 +114,7 @@ struct Part {
     float s = a + b;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (s >= 0x1p-75f && s <= FLT_MAX) {  // the same in every lane
+    if (s >= 0x1p-110f && s <= FLT_MAX) {  // the same in every lane
       if (threadIdx.x % 32 == 0) sum += static_cast<double>(s);
     } else {
       uint32_t any = 0;

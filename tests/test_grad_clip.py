@@ -146,7 +146,7 @@ def test_a_tensor_of_more_than_2_to_the_31_elements():
     assert (g[:-1] == g[0]).all()
 
 
-@pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e-19, 1e15, 1e18, 1e25, 1e37])
+@pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e-19, 1e-18, 1e-17, 1e-16, 1e-14, 1e15, 1e18, 1e25, 1e37])
 def test_squares_beyond_the_fp32_range_are_kept(scale):
     from rank_bottleneck_block_gb300.runner import GradClip
 
@@ -173,6 +173,22 @@ def test_scales_that_differ_by_forty_orders_of_magnitude():
     c.measure()
     norm = Q.clip([as64(g) for g in grads], 1.0)[0]
     assert abs(float(c.norm) - norm) <= 34 * U * norm
+
+
+@pytest.mark.parametrize("low", [-17, -18, -19])
+def test_squares_around_the_smallest_normal_number(low):
+    """Elements from 10^low over six orders of magnitude upwards: many squares are fp32 denormals, few carry the sum."""
+    from rank_bottleneck_block_gb300.runner import GradClip
+
+    for top in (0.0, 1.0, 2.5, 6.0):
+        gen = torch.Generator()
+        gen.manual_seed(int(10 * top) - low)
+        g = 10.0 ** (low + top * torch.rand(50000, generator=gen, dtype=torch.float64) ** 8)
+        grads = [g.float().cuda()]
+        c = GradClip(grads, 1.0)
+        c.measure()
+        norm = Q.clip([as64(grads[0])], 1.0)[0]
+        assert abs(float(c.norm) - norm) <= 34 * U * norm
 
 
 def test_zeros_and_a_bound_of_zero():
