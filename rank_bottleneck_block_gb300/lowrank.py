@@ -180,20 +180,17 @@ _torch_cuda = None  # (current device, its current stream's handle)
 
 
 def _lookups():
-    """torch's functions that name the current device and a device's current stream, the latter without making a
-    Stream object where torch has one that does not."""
+    """Functions that name the current device and a device's current stream: torch's own inner ones where it has them
+    (its public ones initialise what is initialised, and make a Stream object, at each call)."""
     global _torch_cuda
     if _torch_cuda is None:
         import torch
 
         torch.cuda.init()
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _torch_cuda = (torch.cuda.current_device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+        _torch_cuda = (device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
     return _torch_cuda
-
-
-def _current_device() -> int:
-    return _lookups()[0]()
 
 
 def _stream(stream) -> Optional[int]:
@@ -240,15 +237,17 @@ class Prepared:
             raise TypeError(f"{name}: {len(args)} arguments, {len(types)} needed before the stream")
         self._args = tuple(_typed(t, a) for t, a in zip(types, args))
         devices = {a.device for a in args if hasattr(a, "data_ptr")}
-        if len(devices) > 1:
-            raise ValueError(f"{name}: tensors on several devices: {sorted(map(str, devices))}")
-        self._device = next(iter(devices)) if devices else None
+        if len(devices) != 1:
+            raise ValueError(f"{name}: tensors on one device needed, not on {sorted(map(str, devices))}")
+        self._device = devices.pop()
+        self._index = self._device.index if self._device.type == "cuda" else None
 
     def __call__(self, stream=None) -> None:
-        device, current = self._device, _current_device()
-        if device is not None and device.index != current:
-            raise ValueError(f"tensors on {device}, but the current device is cuda:{current}")
-        status = self._fn(*self._args, _stream(stream))
+        device, raw = _torch_cuda or _lookups()
+        current = device()
+        if current != self._index:
+            raise ValueError(f"tensors on {self._device}, but the current device is cuda:{current}")
+        status = self._fn(*self._args, raw(current) if stream is None else _stream(stream))
         if status:
             _check(status)
 

@@ -71,23 +71,23 @@ class GradClip:
         self.stat = torch.zeros(2, dtype=torch.float32, device=first.device)
         self.norm, self.scale = self.stat[:1], self.stat[1:]
         self.ws = _buf(L.lr_grad_workspace_bytes(len(self.grads)), first.device)
-        self._made = None  # the last call's arguments, converted
+        self._measure = self._clip = None  # the last calls' arguments, converted
 
     def measure(self, stream=None) -> torch.Tensor:
-        self._call("lr_grad_norm", stream)
+        if self._measure is None or self._measure[0] is not self.ws:
+            self._measure = (self.ws, L.Prepared("lr_grad_norm", self.dt, len(self.grads), self._g, self._n, self.stat,
+                                                 self.ws, L._nbytes(self.ws)))
+        self._measure[1](stream)
         return self.norm
 
     def clip(self, stream=None) -> torch.Tensor:
-        self._call("lr_grad_clip", stream)
+        made = self._clip
+        if made is None or made[0] is not self.ws or made[1] != self.max_norm:
+            made = self._clip = (self.ws, self.max_norm, L.Prepared(
+                "lr_grad_clip", self.dt, len(self.grads), self._g, self._n, self.max_norm, self._o, self.stat, self.ws,
+                L._nbytes(self.ws)))
+        made[2](stream)
         return self.norm
-
-    def _call(self, name, stream):
-        key = (name, self.max_norm, self.ws)
-        if self._made is None or self._made[0] != key[0] or self._made[1] != key[1] or self._made[2] is not key[2]:
-            args = (self.dt, len(self.grads), self._g, self._n)
-            args += (self.max_norm, self._o) if name == "lr_grad_clip" else ()
-            self._made = (*key, L.Prepared(name, *args, self.stat, self.ws, L._nbytes(self.ws)))
-        self._made[3](stream)
 
 
 class _Clipped:

@@ -306,7 +306,7 @@ def test_tensors_elsewhere_are_refused():
     with pytest.raises(ValueError, match="current device"):
         GradClip([torch.zeros(64)]).clip()
     assert L.lr_launch_count() == before
-    with pytest.raises(ValueError, match="several devices"):
+    with pytest.raises(ValueError, match="one device"):
         L.Prepared("lr_grad_norm", L.LR_F32, 0, None, None, torch.zeros(4, device="cuda"), torch.zeros(4), 16)
 
 
