@@ -183,7 +183,12 @@ static QkKernel pick(const QkArgs& a, bool adj, QkVariant v) {
 
 template <typename ST>
 cudaError_t launch_qk_bwd(const QkArgs& a, bool adjacent, int sms, QkPlan* plan, cudaStream_t st) {
-  const QkVariant v = variant(a, sizeof(ST));
+  QkVariant v = variant(a, sizeof(ST));
+  // Small launches take the shorter runs, whose kernel needs fewer registers and twice the warps (32 + 8 heads of 128 in
+  // bf16, with the launch that adds the rows: 130 tokens 5.1 us against 5.8, 600 tokens 7.6 against 8.9, 1000 tokens 9.5
+  // against 10.0; 2000 tokens 14.2 against 13.9, 16384 tokens and 64 heads 126.4 against 124.4).
+  const long long at_once = sms * bwd_blocks(8, 2) * (32LL / v.g) * kWarps;
+  if (1LL * a.T * (a.t[0].H + a.t[1].H) <= 5 * at_once) v = variant(a, sizeof(ST), false);
   cut(a, v.g, std::min(sms * bwd_blocks(v.u, sizeof(ST)), kQkMaxParts / kMostWaves), plan);
   return launch_qk(pick<ST>(a, adjacent, v), a, *plan,
                    v.u == 8 ? Ring<ST, 8, 4>::bytes(a) : Ring<ST, 4, 4>::bytes(a), st);

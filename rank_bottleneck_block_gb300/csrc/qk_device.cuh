@@ -351,10 +351,10 @@ struct QkVariant {
   int u, g;  // channels of a run, lanes of a vector
 };
 
-// Runs of 8 channels where a bf16 vector divides into them (16-byte loads), else of 4; fp32 takes 4 (16 bytes too)
-// but for vectors of more than 256 channels, which then fill a warp.
-inline QkVariant variant(const QkArgs& a, size_t es) {
-  const bool wide = a.dh % 16 == 0 && a.rot % 16 == 0 && (es == 2 || a.dh > 256);
+// Runs of 8 channels where a bf16 vector divides into them (16-byte loads) and `wide` allows, else of 4; fp32 takes 4
+// (16 bytes too).  Vectors of more than 256 channels take runs of 8 in both types, and then fill a warp.
+inline QkVariant variant(const QkArgs& a, size_t es, bool wide = true) {
+  wide = a.dh > 256 || (wide && es == 2 && a.dh % 16 == 0 && a.rot % 16 == 0);
   const int u = wide ? 8 : 4, slots = a.dh / (2 * u);
   // 6 and 3 vectors a warp, not 4 and 2: 16 + 2 heads of 72 in bf16, 40003 tokens: 46 us against 61
   if (slots == 5 || slots == 9 || slots == 10) return {u, slots == 5 ? 5 : 10};
@@ -367,30 +367,50 @@ constexpr int kMostHeads = 16;  // of an item: past it the angles cost nothing a
 constexpr int kMostWaves = 4;   // blocks of a launch for each that runs at once
 constexpr int kWaveSteps = 12;  // heads a lane group takes at least, where the launch has more blocks than run at once
 
-// Cuts each token's heads into items, and gives each tensor blocks by its share of the vectors.  Small launches: one
-// item a lane group, as short as fills the SMs.  Large ones: up to kMostWaves blocks for each that runs at once, since
-// SMs do not get the same share of the memory's bandwidth and a block that ends early makes room for another (16384
-// tokens, 64 heads: 95 us with one block for each that runs at once, 90, 85 and 82 us with two, three and four; a launch
-// of 300,000 vectors gains nothing, 33 us either way, and pays for the blocks' starts).
+// Cuts each token's heads into items, and gives each tensor blocks by its share of the work.  Small launches: all
+// blocks run at once and a lane group takes one item, as short as lets them.  Large ones: up to kMostWaves blocks for
+// each that runs at once, since SMs do not get the same share of the memory's bandwidth and a block that ends early
+// makes room for another (16384 tokens, 64 heads: 95 us with one block for each that runs at once, 90, 85 and 82 us with
+// two, three and four; a launch of 300,000 vectors gains nothing and pays for the blocks' starts).  Items are then as
+// long as gives the fewest steps to the longest block, an item's angles counted as a step and a half.
 inline void cut(const QkArgs& a, int g, int resident, QkPlan* pl) {
   const long long groups = 32 / g * kWarps;  // of a block
   long long vectors[2];
   for (int i = 0; i < 2; ++i) vectors[i] = 1LL * a.T * a.t[i].H;
   const long long all = vectors[0] + vectors[1], each = (all + resident * groups - 1) / (resident * groups);
   const long long waves = std::max(1LL, std::min<long long>(kMostWaves, each / kWaveSteps));
+  const long long most = resident * waves;
+  long long least = 0;
+  for (int e = static_cast<int>(each <= kMostHeads ? each : kMostHeads / 2); e <= kMostHeads; ++e) {
+    QkPlan p;
+    long long room[2], work[2], cost = 0;
+    for (int i = 0; i < 2; ++i) {
+      const int H = a.t[i].H;
+      p.chunks[i] = cdiv(H, e);
+      p.len[i] = H ? cdiv(H, p.chunks[i]) : 0;
+      room[i] = (1LL * a.T * p.chunks[i] + groups - 1) / groups;
+      work[i] = room[i] * (2 * p.len[i] + 3);
+    }
+    const bool fits = room[0] + room[1] <= most;
+    const long long share = (work[0] * most + (work[0] + work[1]) / 2) / (work[0] + work[1]);
+    for (int i = 0; i < 2; ++i) {
+      p.blocks[i] = static_cast<int>(fits ? room[i] : std::min(std::max(i ? most - share : share, 1LL), room[i]));
+      p.rounds[i] = room[i] ? cdiv(room[i], p.blocks[i]) : 0;
+      cost = std::max(cost, 1LL * p.rounds[i] * (2 * p.len[i] + 3));
+    }
+    if (least == 0 || cost <= least) {
+      least = cost;
+      *pl = p;
+    }
+    if (fits) break;  // longer items only leave SMs idle
+  }
   for (int i = 0; i < 2; ++i) {
-    const int H = a.t[i].H;
-    pl->chunks[i] = cdiv(H, std::min<long long>(kMostHeads, each));
-    pl->len[i] = H ? cdiv(H, pl->chunks[i]) : 0;
-    const long long want = (vectors[i] * resident * waves + all / 2) / all;
-    const long long room = (1LL * a.T * pl->chunks[i] + groups - 1) / groups;
-    pl->blocks[i] = static_cast<int>(std::min(std::max(want, 1LL), room));
-    pl->rounds[i] = pl->blocks[i] ? cdiv(room, pl->blocks[i]) : 0;
     // 2^(31 + L) / chunks rounded up, L = log2 of chunks rounded up: exact for 31-bit dividends
     int log = 1;
     while ((1LL << log) < pl->chunks[i]) ++log;
     pl->shift[i] = log - 1;
-    pl->magic[i] = pl->chunks[i] > 1 ? static_cast<unsigned>(((1ULL << (31 + log)) + pl->chunks[i] - 1) / pl->chunks[i]) : 0;
+    pl->magic[i] =
+        pl->chunks[i] > 1 ? static_cast<unsigned>(((1ULL << (31 + log)) + pl->chunks[i] - 1) / pl->chunks[i]) : 0;
   }
 }
 
