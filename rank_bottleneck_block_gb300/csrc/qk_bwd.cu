@@ -3,8 +3,8 @@
 // The two sums over a vector's channels, of x^2 and w x, do not depend on one another and are reduced together.  The
 // gain sums stay in registers over a group's steps; they are added over the block's lane groups, each block leaves one
 // row of partial sums, and a second launch adds the rows in a fixed order.
-// Bound by memory: x and dy read, dx written.  Measured, 16384 tokens, 32 + 32 heads of 128: bf16 805 MB in 124.3 us
-// (6.48 TB/s, 97% of the copy rate), of which the second launch takes 3 us; rotation alone 537 MB in 81 us.
+// Bound by memory: x and dy read, dx written.  Measured, 16384 tokens, 32 + 32 heads of 128: bf16 805 MB in 124.0 us
+// (6.49 TB/s, 97% of the copy rate), of which the second launch takes 3 us; rotation alone 537 MB in 81 us.
 #include "qk_device.cuh"
 
 namespace lr {

@@ -1,8 +1,8 @@
 // Norm and rotation of queries and keys, forward: y = r R(theta) (x g), with R(theta) g kept as four products per pair
 // that are renewed once per item.
 // Bound by memory: x read, y written.  Measured, 16384 tokens, 32 + 32 heads of 128: bf16 537 MB in 81.5 us (6.59 TB/s,
-// 98% of the copy rate); 12483 tokens with three position axes, 20 + 4 heads: 153 MB in 28 us (82%: with so few heads
-// to a token the angles weigh more, and the instructions issue in 60% of the cycles).
+// 98% of the copy rate); 12483 tokens with three position axes, 20 + 4 heads: 153 MB in 26.4 us (87%: with so few heads
+// to a token the angles weigh more).
 #include "qk_device.cuh"
 
 namespace lr {
