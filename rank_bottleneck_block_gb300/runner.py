@@ -483,7 +483,7 @@ class TransformerBlock(_Clipped):
 
     qk: the heads' position rotation (its T, Hq, Hk, dh those of the block), with case["freq"], case["pos"]
     (int32 [axes, b*s]; None or missing: positions within each sequence) and the gains case["gq"], case["gk"]
-    [dh] of the queries' and keys' norms (None or missing: no norm)."""
+    [dh] of the queries' and keys' norms (None or missing: no norm).  The block's eps serves these norms too."""
 
     def __init__(self, shape, case: Dict[str, object], device="cuda", qk: Optional[QkShape] = None):
         self.sh = shape
