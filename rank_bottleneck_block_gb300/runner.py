@@ -7,6 +7,7 @@ is a call into liblowrank.so through the ctypes binding.
 """
 from __future__ import annotations
 
+import contextlib
 import operator
 from typing import Dict, List, Optional, Sequence
 
@@ -30,33 +31,50 @@ def _buf(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=_U8, device=device)
 
 
+def _current(stream):
+    """Makes the stream that a call names (None: the current one) torch's current stream: torch hands memory out in the
+    order of that stream's work."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class GradClip:
     """The norm over a list of gradient tensors, and the tensors scaled to at most max_norm.
 
     grads: contiguous tensors of one type (fp32 as the backward passes write them, or bf16) on one
     device, 16-byte aligned; outs: where the scaled tensors go (None: in place).  measure() leaves the
     norm in self.norm [1]; clip() leaves it there, min(1, max_norm / (norm + 1e-6)) in self.scale [1]
-    and the scaled gradients in outs.  Device tensors: nothing waits for the GPU.
+    and the scaled gradients in outs (all of them unset before).  Device tensors: nothing waits for the
+    GPU.  stream: the one for which the results' and the workspace's memory is made (None: the current one);
+    calls on others are to be ordered after it, and the object kept until they have ended.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], max_norm: float = 1.0,
-                 outs: Optional[Sequence[torch.Tensor]] = None):
-        self.grads, self.max_norm = list(grads), float(max_norm)
-        self.outs = self.grads if outs is None else list(outs)
-        if not self.grads:
+                 outs: Optional[Sequence[torch.Tensor]] = None, stream=None):
+        self.max_norm = float(max_norm)
+        self.stat = self.ws = None
+        self._retired = []  # buffers that graphs captured before may still write to
+        self._bind(grads, outs, stream)
+
+    def _bind(self, grads, outs=None, stream=None):
+        """Takes a list of tensors; the results and, where it is long enough, the workspace stay where they are."""
+        grads = list(grads)
+        to_tensors = grads if outs is None else list(outs)
+        if not grads:
             raise ValueError("no gradients")
-        if len(self.outs) != len(self.grads):
-            raise ValueError(f"{len(self.grads)} gradients but {len(self.outs)} outputs")
-        first = self.grads[0]
-        self.dt, es = L.dtype_code(first), first.element_size()
-        for t in self.grads if outs is None else self.grads + self.outs:
+        if len(to_tensors) != len(grads):
+            raise ValueError(f"{len(grads)} gradients but {len(to_tensors)} outputs")
+        first = grads[0]
+        dt, es = L.dtype_code(first), first.element_size()
+        for t in grads if outs is None else grads + to_tensors:
             if t.dtype != first.dtype or t.device != first.device or not t.is_contiguous():
                 raise ValueError("gradients and outputs must be contiguous, of one type and on one device")
-        n = [t.numel() for t in self.grads]
-        to = at = [t.data_ptr() for t in self.grads]
+        n = [t.numel() for t in grads]
+        to = at = [t.data_ptr() for t in grads]
         if outs is not None:
-            to = [t.data_ptr() for t in self.outs]
-            if [t.numel() for t in self.outs] != n:
+            to = [t.data_ptr() for t in to_tensors]
+            if [t.numel() for t in to_tensors] != n:
                 raise ValueError("an output has another number of elements than its gradient")
         # a written tensor is its own gradient, or overlaps nothing else of either list
         spans = [(o, o + k * es, 1) for o, k in zip(to, n) if k]
@@ -66,11 +84,18 @@ class GradClip:
             if lo < (end if w else written):
                 raise ValueError("an output overlaps another output or another gradient")
             end, written = max(end, hi), max(written, hi if w else 0)
+        size, stat, ws = L.lr_grad_workspace_bytes(len(grads)), self.stat, self.ws
+        with _current(stream):
+            if stat is None or stat.device != first.device:
+                stat = torch.empty(2, dtype=torch.float32, device=first.device)
+            if ws is None or ws.device != first.device or ws.numel() < size:
+                ws = _buf(size, first.device)
+        self._retired += [b for b, now in ((self.stat, stat), (self.ws, ws)) if b is not None and b is not now]
+        self.grads, self.outs, self.dt = grads, to_tensors, dt
         self._g, self._n = L.tensor_list(at, n)
         self._o = self._g if outs is None else L.tensor_list(to, n)[0]
-        self.stat = torch.zeros(2, dtype=torch.float32, device=first.device)
-        self.norm, self.scale = self.stat[:1], self.stat[1:]
-        self.ws = _buf(L.lr_grad_workspace_bytes(len(self.grads)), first.device)
+        self.stat, self.ws = stat, ws
+        self.norm, self.scale = stat[:1], stat[1:]
         self._measure = self._clip = None  # the last calls' arguments, converted
 
     def measure(self, stream=None) -> torch.Tensor:
@@ -98,8 +123,10 @@ class _Clipped:
     def clip_grads(self, max_norm: float, stream=None) -> torch.Tensor:
         """Scale every gradient in place so that their common norm is at most max_norm; the norm [1]."""
         grads = self.grad_tensors()
-        if self._clip is None or not all(map(operator.is_, self._clip.grads, grads)):
-            self._clip = GradClip(grads)
+        if self._clip is None:
+            self._clip = GradClip(grads, stream=stream)
+        elif not all(map(operator.is_, self._clip.grads, grads)):
+            self._clip._bind(grads, stream=stream)
         self._clip.max_norm = float(max_norm)
         return self._clip.clip(stream)
 

@@ -1,0 +1,138 @@
+"""clip_grads of the runners: the buffers it makes inside a call, on whatever stream the call names."""
+import contextlib
+import weakref
+
+import pytest
+import torch
+
+from rank_bottleneck_block_gb300 import runner as R
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from rank_bottleneck_block_gb300 import build
+
+    build.build()
+
+
+class Holder(R._Clipped):
+    def __init__(self, grads):
+        self.tensors = list(grads)
+
+    def grad_tensors(self):
+        return list(self.tensors)
+
+
+class Stream:
+    """Stands in for a stream where there is no GPU."""
+
+    cuda_stream = 1234
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Prepared calls that only note their name, arguments and stream."""
+    made = []
+
+    class Prepared:
+        def __init__(self, *args):
+            self.args = args
+
+        def __call__(self, stream=None):
+            made.append((self.args, stream))
+
+    monkeypatch.setattr(R.L, "Prepared", Prepared)
+    return made
+
+
+def test_buffers_are_made_on_the_stream_of_the_call(monkeypatch, calls):
+    """Memory that torch hands out, and anything it fills, is ordered after the work of torch's current stream; the
+    kernels run on the stream of the call.  So that one has to be current while the buffers are made."""
+    made, current = [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("empty", "zeros", "full", "ones"):
+        def make(*args, _real=getattr(torch, name), **kw):
+            made.append(current[-1] if current else None)
+            return _real(*args, **kw)
+
+        monkeypatch.setattr(torch, name, make)
+    side, first, second = Stream(), torch.randn(64), torch.randn(32)
+    h = Holder([first])
+    h.clip_grads(1.0, stream=side)
+    assert made and all(s is side for s in made)
+    h.tensors = [second] + [torch.randn(8) for _ in range(1100)]  # another list, and a longer workspace
+    made.clear()
+    h.clip_grads(1.0, stream=side)
+    assert all(s is side for s in made)
+    assert [s for _, s in calls] == [side, side]
+    made.clear()
+    Holder([first]).clip_grads(1.0)
+    assert made and all(s is None for s in made)
+
+
+def test_a_handle_of_a_stream_serves_too(monkeypatch, calls):
+    seen = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        seen.append(s)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    Holder([torch.randn(64)]).clip_grads(1.0, stream=1234)
+    assert seen == [("external", 1234)] and calls[0][1] == 1234
+
+
+def test_buffers_stay_when_gradients_are_replaced(calls):
+    """A graph that was captured before, or a stream that still runs, goes on writing where it did."""
+    h = Holder([torch.randn(64), torch.randn(8)])
+    norm = h.clip_grads(1.0)
+    ws = h._clip.ws
+    h.tensors[0] = torch.randn(64)
+    assert h.clip_grads(1.0).data_ptr() == norm.data_ptr() and h._clip.ws.data_ptr() == ws.data_ptr()
+    kept = weakref.ref(ws)
+    del ws
+    h.tensors = [torch.randn(8) for _ in range(1100)]
+    assert h.clip_grads(1.0).data_ptr() == norm.data_ptr()
+    calls.clear()
+    assert kept() is not None and h._clip.ws.numel() > kept().numel()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_the_first_clip_on_a_side_stream_beside_a_busy_one(handle):
+    """The current stream is busy for some 20 ms when the first clip runs on another stream, and when a replaced
+    gradient makes it look its list up again.  More than 512 partial sums: three launches, which leave the scale in
+    memory between the last two."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    grads = [torch.randn(n, generator=gen, device="cuda") for n in (2100 * 8192, 77)]
+    h, side = Holder(grads), torch.cuda.Stream()
+    a = torch.randn(8192, 8192, generator=gen, device="cuda").bfloat16()
+    b = torch.empty_like(a)
+    for again in (False, True):
+        if again:
+            h.tensors[1] = torch.randn(99, generator=gen, device="cuda")
+        keep = [g.clone() for g in h.tensors]
+        norm = float(torch.stack([g.double().square().sum() for g in keep]).sum().sqrt())
+        torch.cuda.synchronize()
+        for _ in range(30):
+            torch.matmul(a, a, out=b)
+        got = h.clip_grads(1.0, side.cuda_stream if handle else side)
+        for wait in (side.synchronize, torch.cuda.synchronize):  # before and after the busy stream has ended
+            wait()
+            with torch.cuda.stream(side):
+                # 34 roundings in the norm, 38 in the scale, one in the product (as for the kernels' own tests)
+                assert abs(float(got) - norm) <= 34 * 2.0 ** -24 * norm
+                assert abs(float(h._clip.scale) * (norm + 1e-6) - 1.0) <= 38 * 2.0 ** -24
+                for g, k in zip(h.tensors, keep):
+                    want = k.double() / (norm + 1e-6)
+                    assert ((g.double() - want).abs() <= 41 * 2.0 ** -24 * want.abs() + 1e-40).all()
