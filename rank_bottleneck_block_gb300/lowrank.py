@@ -227,16 +227,18 @@ def pair_grad(dA, dB) -> lr_pair_grad:
 
 class Prepared:
     """An entry point with every argument but the stream converted once, for callers that repeat a call on the
-    same buffers: call(stream).  It keeps its arguments, so the tensors whose pointers it holds stay alive.  The
+    same buffers: call(stream).  It keeps its arguments and the memory that its tensors have at that time.  The
     tensors must be on one GPU, and that GPU must be the current one when the call is made."""
 
     def __init__(self, name: str, *args):
-        self._fn, self._keep = getattr(lib(), name), args
+        tensors = [a for a in args if hasattr(a, "data_ptr")]
+        # aliases: a tensor may be given other memory later
+        self._fn, self._keep = getattr(lib(), name), (args, [t.detach() for t in tensors])
         types = _SIGS[name][1][:-1]
         if len(types) != len(args):
             raise TypeError(f"{name}: {len(args)} arguments, {len(types)} needed before the stream")
         self._args = tuple(_typed(t, a) for t, a in zip(types, args))
-        devices = {a.device for a in args if hasattr(a, "data_ptr")}
+        devices = {t.device for t in tensors}
         if len(devices) != 1:
             raise ValueError(f"{name}: tensors on one device needed, not on {sorted(map(str, devices))}")
         self._device = devices.pop()

@@ -39,6 +39,24 @@ def _current(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+_READ = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous, operator.attrgetter("dtype"))
+
+
+def _facts(tensors):
+    """What a converted list of tensors rests on."""
+    return [list(map(f, tensors)) for f in _READ]
+
+
+class _FixedList(list):
+    """A list whose elements a prepared call has converted: changing it would change nothing."""
+
+    def _refuse(self, *args, **kw):
+        raise TypeError("the list is fixed")
+
+    __setitem__ = __delitem__ = __iadd__ = __imul__ = _refuse
+    append = extend = insert = pop = remove = clear = sort = reverse = _refuse
+
+
 class GradClip:
     """The norm over a list of gradient tensors, and the tensors scaled to at most max_norm.
 
@@ -48,19 +66,29 @@ class GradClip:
     and the scaled gradients in outs (all of them unset before).  Device tensors: nothing waits for the
     GPU.  stream: the one for which the results' and the workspace's memory is made (None: the current one);
     calls on others are to be ordered after it, and the object kept until they have ended.
+
+    The lists are fixed.  Calls work on the memory that the tensors have when the object is made, and keep it
+    alive: new gradients are written into it, and tensors that have been given other memory need an object of
+    their own (the runners' clip_grads sees to that).  ws may be replaced, by one that several objects share.
     """
 
     def __init__(self, grads: Sequence[torch.Tensor], max_norm: float = 1.0,
                  outs: Optional[Sequence[torch.Tensor]] = None, stream=None):
         self.max_norm = float(max_norm)
-        self.stat = self.ws = None
+        self._stat = self.ws = None
         self._retired = []  # buffers that graphs captured before may still write to
         self._bind(grads, outs, stream)
 
+    grads = property(lambda self: self._grads)
+    outs = property(lambda self: self._outs)
+    stat = property(lambda self: self._stat)  # norm and scale
+    norm = property(lambda self: self._norm)
+    scale = property(lambda self: self._scale)
+
     def _bind(self, grads, outs=None, stream=None):
         """Takes a list of tensors; the results and, where it is long enough, the workspace stay where they are."""
-        grads = list(grads)
-        to_tensors = grads if outs is None else list(outs)
+        grads = _FixedList(grads)
+        to_tensors = grads if outs is None else _FixedList(outs)
         if not grads:
             raise ValueError("no gradients")
         if len(to_tensors) != len(grads):
@@ -84,35 +112,38 @@ class GradClip:
             if lo < (end if w else written):
                 raise ValueError("an output overlaps another output or another gradient")
             end, written = max(end, hi), max(written, hi if w else 0)
-        size, stat, ws = L.lr_grad_workspace_bytes(len(grads)), self.stat, self.ws
+        size, stat, ws = L.lr_grad_workspace_bytes(len(grads)), self._stat, self.ws
         with _current(stream):
             if stat is None or stat.device != first.device:
                 stat = torch.empty(2, dtype=torch.float32, device=first.device)
             if ws is None or ws.device != first.device or ws.numel() < size:
                 ws = _buf(size, first.device)
-        self._retired += [b for b, now in ((self.stat, stat), (self.ws, ws)) if b is not None and b is not now]
-        self.grads, self.outs, self.dt = grads, to_tensors, dt
+        self._retired += [b for b, now in ((self._stat, stat), (self.ws, ws)) if b is not None and b is not now]
+        self._grads, self._outs, self.dt = grads, to_tensors, dt
+        # aliases keep the memory alive when a tensor is given other memory
+        self._held = [t.detach() for t in (grads if outs is None else grads + to_tensors)]
+        self._facts = _facts(grads)
         self._g, self._n = L.tensor_list(at, n)
         self._o = self._g if outs is None else L.tensor_list(to, n)[0]
-        self.stat, self.ws = stat, ws
-        self.norm, self.scale = stat[:1], stat[1:]
+        self._stat, self.ws = stat, ws
+        self._norm, self._scale = stat[:1], stat[1:]
         self._measure = self._clip = None  # the last calls' arguments, converted
 
     def measure(self, stream=None) -> torch.Tensor:
         if self._measure is None or self._measure[0] is not self.ws:
-            self._measure = (self.ws, L.Prepared("lr_grad_norm", self.dt, len(self.grads), self._g, self._n, self.stat,
+            self._measure = (self.ws, L.Prepared("lr_grad_norm", self.dt, len(self._grads), self._g, self._n, self._stat,
                                                  self.ws, L._nbytes(self.ws)))
         self._measure[1](stream)
-        return self.norm
+        return self._norm
 
     def clip(self, stream=None) -> torch.Tensor:
         made = self._clip
         if made is None or made[0] is not self.ws or made[1] != self.max_norm:
             made = self._clip = (self.ws, self.max_norm, L.Prepared(
-                "lr_grad_clip", self.dt, len(self.grads), self._g, self._n, self.max_norm, self._o, self.stat, self.ws,
+                "lr_grad_clip", self.dt, len(self._grads), self._g, self._n, self.max_norm, self._o, self._stat, self.ws,
                 L._nbytes(self.ws)))
         made[2](stream)
-        return self.norm
+        return self._norm
 
 
 class _Clipped:
@@ -125,7 +156,7 @@ class _Clipped:
         grads = self.grad_tensors()
         if self._clip is None:
             self._clip = GradClip(grads, stream=stream)
-        elif not all(map(operator.is_, self._clip.grads, grads)):
+        elif _facts(grads) != self._clip._facts:  # the held memory makes equal addresses the same memory
             self._clip._bind(grads, stream=stream)
         self._clip.max_norm = float(max_norm)
         return self._clip.clip(stream)

@@ -1,7 +1,9 @@
 """clip_grads of the runners: the buffers it makes inside a call, on whatever stream the call names."""
 import contextlib
+import gc
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -136,3 +138,111 @@ def test_the_first_clip_on_a_side_stream_beside_a_busy_one(handle):
                 for g, k in zip(h.tensors, keep):
                     want = k.double() / (norm + 1e-6)
                     assert ((g.double() - want).abs() <= 41 * 2.0 ** -24 * want.abs() + 1e-40).all()
+
+
+def _last(calls):
+    """(pointers of the gradients, of the outputs, element counts) of the newest prepared clip."""
+    name, _, n, grads, counts, _, outs = calls[-1][0][:7]
+    assert name == "lr_grad_clip" and len(grads) == len(outs) == len(counts) == n
+    return list(grads), list(outs), list(counts)
+
+
+def _as_list(tensors):
+    return [t.data_ptr() for t in tensors], [t.data_ptr() for t in tensors], [t.numel() for t in tensors]
+
+
+def _like(ts, n):
+    return torch.randn(n, device=ts[0].device)
+
+
+CHANGES = {
+    "added": lambda ts: ts.append(_like(ts, 24)),
+    "lost": lambda ts: ts.pop(),
+    "inserted": lambda ts: ts.insert(0, _like(ts, 4)),
+    "replaced": lambda ts: ts.__setitem__(1, _like(ts, 40)),
+    "reordered": lambda ts: ts.reverse(),
+    "new memory": lambda ts: setattr(ts[0], "data", _like(ts, 64)),
+    "other size": lambda ts: setattr(ts[0], "data", _like(ts, 48)),
+    "shorter, same memory": lambda ts: setattr(ts[0], "data", ts[0].data[:32]),
+    "set": lambda ts: ts[2].set_(_like(ts, 16)),
+}
+
+
+@pytest.mark.parametrize("change", CHANGES)
+def test_clipping_takes_the_gradients_of_the_moment(calls, change):
+    h = Holder([torch.randn(n) for n in (64, 40, 16)])
+    h.clip_grads(1.0)
+    assert _last(calls) == _as_list(h.tensors)
+    CHANGES[change](h.tensors)
+    h.clip_grads(1.0)
+    assert _last(calls) == _as_list(h.tensors)
+
+
+@pytest.mark.parametrize("bad", [torch.randn(64).bfloat16(), torch.randn(8, 8).T, torch.randn(128)[::2]])
+def test_a_gradient_that_cannot_be_clipped_any_more_is_refused(calls, bad):
+    h = Holder([torch.randn(64), torch.randn(8)])
+    h.clip_grads(1.0)
+    h.tensors[0].data = bad
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            h.clip_grads(1.0)
+    h.tensors[0].data = torch.randn(64)
+    h.clip_grads(1.0)
+    assert _last(calls) == _as_list(h.tensors)
+
+
+def test_a_list_is_fixed_and_its_memory_stays(calls):
+    """A GradClip of the caller's own works on the memory that it was given, which lives as long as it does."""
+    memory = np.zeros(64, dtype=np.float32)
+    kept = weakref.ref(memory)
+    grads = [torch.from_numpy(memory), torch.randn(8)]
+    del memory
+    clip = R.GradClip(grads, outs=[torch.empty(64), torch.empty(8)])
+    before = clip.grads[0].data_ptr()
+    grads[0].data = torch.randn(64)
+    grads.append(torch.randn(4))
+    gc.collect()
+    assert kept() is not None and len(clip.grads) == 2
+    clip.clip()
+    assert _last(calls)[0][0] == before
+    for name in ("grads", "outs", "stat", "norm", "scale"):
+        with pytest.raises(AttributeError):
+            setattr(clip, name, getattr(clip, name))
+    for change in (lambda ts: ts.__setitem__(0, grads[0]), lambda ts: ts.append(grads[0]), lambda ts: ts.pop(),
+                   lambda ts: ts.clear(), lambda ts: ts.__delitem__(0), lambda ts: ts.reverse()):
+        for ts in (clip.grads, clip.outs):
+            with pytest.raises(TypeError):
+                change(ts)
+    del clip, calls[:]
+    gc.collect()
+    assert kept() is None
+
+
+def test_buffers_of_a_prepared_call_stay(monkeypatch):
+    """A call that has been prepared keeps the memory whose addresses it holds."""
+    memory = np.zeros(64, dtype=np.float32)
+    kept = weakref.ref(memory)
+    ws = torch.from_numpy(memory)
+    del memory
+    call = R.L.Prepared("lr_grad_norm", R.L.LR_F32, 0, None, None, torch.zeros(4), ws, 256)
+    ws.data = torch.zeros(64)
+    gc.collect()
+    assert kept() is not None
+    del call
+    gc.collect()
+    assert kept() is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("change", CHANGES)
+def test_what_changed_is_clipped_on_the_gpu(change):
+    h = Holder([torch.randn(n).cuda() for n in (64, 40, 16)])
+    h.clip_grads(1.0)
+    CHANGES[change](h.tensors)
+    for i, t in enumerate(h.tensors):
+        t.copy_(torch.arange(t.numel()) + i)
+    keep = [t.double() for t in h.tensors]
+    norm = float(torch.cat(keep).square().sum().sqrt())
+    assert abs(float(h.clip_grads(1.0)) - norm) <= 34 * 2.0 ** -24 * norm
+    for t, k in zip(h.tensors, keep):
+        assert ((t.double() - k / (norm + 1e-6)).abs() <= 41 * 2.0 ** -24 * k / norm + 1e-40).all()
