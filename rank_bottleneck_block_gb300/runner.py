@@ -472,31 +472,31 @@ class QkRotary:
     heads), gq, gk [dh] (None: no norm), pos int32 [axes, T] (None: position t mod shape.seq), freq (the
     rot / 2 frequencies in radians per position) and, for backward(), dqo, dko.  forward() writes qo, ko;
     backward() writes dq, dk and, with the norm, dgq, dgk [dh] fp32.
+
+    The tensors are attributes, and may be replaced by others of their size and type on the same device, 16-byte
+    aligned (run.q = ..., run.qo = run.q for a forward in place).  The calls' arguments are converted once for
+    each assignment: a tensor that is given other memory by other means is to be assigned again.  The shape is fixed.
     """
 
+    _FORWARD = ("turns", "pos", "gq", "gk", "q", "k", "qo", "ko")
+    _BACKWARD = ("turns", "pos", "gq", "gk", "q", "k", "dqo", "dko", "dq", "dk", "dgq", "dgk", "ws")
+    _TENSORS = frozenset(_FORWARD + _BACKWARD)
+
     def __init__(self, shape: QkShape, case: Dict[str, object], device="cuda"):
-        s, self.s, self.dt = shape, shape, _dt(shape.dtype)
-        self.sh = _qk_shape(s)
-        td = _tdt(s.dtype)
-
-        def on_device(name, size, dtype=td):
-            t = case.get(name)
-            if t is None:
-                return None
-            if tuple(t.shape) != size or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
-                raise ValueError(f"{name}: {list(size)} {dtype} with contiguous rows needed, not {list(t.shape)} "
-                                 f"{t.dtype} with strides {t.stride()}")
-            return t.to(device)
-
+        self.s, self.dt, self.sh = shape, _dt(shape.dtype), _qk_shape(shape)
+        s, td, f32 = shape, _tdt(shape.dtype), torch.float32
+        q, k, g = (s.T, s.Hq * s.dh), (s.T, s.Hk * s.dh), (s.dh,)
+        self._fits = {"turns": ((s.rot // 2,), torch.int64), "pos": ((len(s.sec), s.T), torch.int32), "gq": (g, td),
+                      "gk": (g, td), "dgq": (g, f32), "dgk": (g, f32), "ws": (None, _U8),
+                      **{n: (q, td) for n in ("q", "qo", "dqo", "dq")}, **{n: (k, td) for n in ("k", "ko", "dko", "dk")}}
         if len(case["freq"]) != s.rot // 2:
             raise ValueError(f"{len(case['freq'])} frequencies for {s.rot // 2} pairs")
-        self.turns = L.turns_tensor(case["freq"], device)
-        self.pos = on_device("pos", (len(s.sec), s.T), torch.int32)
-        if self.pos is not None and not self.pos.is_contiguous():
-            raise ValueError("pos must be contiguous")
-        self.q, self.k = on_device("q", (s.T, s.Hq * s.dh)), on_device("k", (s.T, s.Hk * s.dh))
-        self.gq, self.gk = on_device("gq", (s.dh,)), on_device("gk", (s.dh,))
-        self.dqo, self.dko = on_device("dqo", (s.T, s.Hq * s.dh)), on_device("dko", (s.T, s.Hk * s.dh))
+        turns = L.turns_tensor(case["freq"], device)
+        self._device = turns.device
+        self.turns = turns
+        for n in ("pos", "q", "k", "gq", "gk", "dqo", "dko"):
+            t = case.get(n)
+            setattr(self, n, None if t is None else self._fit(n, t).to(device))
 
         def fresh(H, wanted=True):
             return torch.empty(s.T, H * s.dh, dtype=td, device=device) if H and wanted else None
@@ -504,30 +504,59 @@ class QkRotary:
         self.qo, self.ko = fresh(s.Hq), fresh(s.Hk)
         back = self.dqo is not None or self.dko is not None
         self.dq, self.dk = fresh(s.Hq, back), fresh(s.Hk, back)
-        f32 = dict(dtype=torch.float32, device=device)
-        self.dgq = torch.empty(s.dh, **f32) if back and s.Hq and self.gq is not None else None
-        self.dgk = torch.empty(s.dh, **f32) if back and s.Hk and self.gk is not None else None
+        self.dgq = torch.empty(s.dh, dtype=f32, device=device) if back and s.Hq and self.gq is not None else None
+        self.dgk = torch.empty(s.dh, dtype=f32, device=device) if back and s.Hk and self.gk is not None else None
         self.ws = _buf(L.lr_qk_bwd_workspace_bytes(self.dt, s.T, self.sh), device) if back else None
-
-        def rows(t):
-            return (t, 0 if t is None else t.stride(0) if s.T > 1 else t.shape[1])
-
-        common = (self.dt, s.T, L.ctypes.pointer(self.sh), s.eps, self.turns, self.pos, self.gq, self.gk,
-                  *rows(self.q), *rows(self.k))
-        self._fwd = L.Prepared("lr_qk_fwd", *common, *rows(self.qo), *rows(self.ko))
-        self._bwd = None
+        self._prepare_forward()
         if back:
-            self._bwd = L.Prepared("lr_qk_bwd", *common, *rows(self.dqo), *rows(self.dko), *rows(self.dq),
-                                   *rows(self.dk), self.dgq, self.dgk, self.ws, L._nbytes(self.ws))
+            self._prepare_backward()
+
+    def __setattr__(self, name, value):
+        if name in self._TENSORS:
+            if value is not None and self._fit(name, value).device != self._device:
+                raise ValueError(f"{name}: a tensor on {self._device} needed, not on {value.device}")
+            self.__dict__.update(_fwd=None, _bwd=None)
+        elif name in ("s", "dt", "sh") and name in self.__dict__:
+            raise AttributeError(f"{name} is fixed")
+        object.__setattr__(self, name, value)
+
+    def _fit(self, name, t):
+        size, dtype = self._fits[name]
+        if (size is not None and tuple(t.shape) != size) or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
+            raise ValueError(f"{name}: {'' if size is None else list(size)} {dtype} with contiguous rows needed, not "
+                             f"{list(t.shape)} {t.dtype} with strides {t.stride()}")
+        if name in ("pos", "ws") and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    def _rows(self, *names):
+        """Each tensor and its row distance."""
+        for n in names:
+            t = getattr(self, n)
+            yield t
+            yield 0 if t is None else t.stride(0) if self.s.T > 1 else t.shape[1]
+
+    def _common(self):
+        return (self.dt, self.s.T, L.ctypes.pointer(self.sh), self.s.eps, self.turns, self.pos, self.gq, self.gk,
+                *self._rows("q", "k"))
+
+    def _prepare_forward(self):
+        self._fwd = L.Prepared("lr_qk_fwd", *self._common(), *self._rows("qo", "ko"))
+        return self._fwd
+
+    def _prepare_backward(self):
+        if self.ws is None or (self.dqo is None and self.dko is None):
+            raise ValueError("no upstream gradients dqo, dko were given")
+        self._bwd = L.Prepared("lr_qk_bwd", *self._common(), *self._rows("dqo", "dko", "dq", "dk"), self.dgq, self.dgk,
+                               self.ws, L._nbytes(self.ws))
+        return self._bwd
 
     def forward(self, stream=None):
-        self._fwd(stream)
+        (self._fwd or self._prepare_forward())(stream)
         return self.qo, self.ko
 
     def backward(self, stream=None):
-        if self._bwd is None:
-            raise ValueError("no upstream gradients dqo, dko were given")
-        self._bwd(stream)
+        (self._bwd or self._prepare_backward())(stream)
         return self.dq, self.dk
 
     def step(self, stream=None):
