@@ -564,65 +564,108 @@ class QkRotary:
         self.backward(stream)
 
 
+_BLOCK_PAIRS = tuple(f"{m}_{n}" for n in ("q", "k", "v", "o", "gate", "up", "down") for m in "AB")
+
+
+def _block_struct(kind, pair, g_attn, g_mlp, at):
+    """lr_block_weights or lr_block_grads of the pointers of _BLOCK_PAIRS."""
+    pairs = [pair(*at[i:i + 2]) for i in range(0, len(at), 2)]
+    return kind(g_attn, *pairs[:4], g_mlp, *pairs[4:])
+
+
 class TransformerBlock(_Clipped):
     """One low-rank transformer block (q/k/v group, causal attention, o-projection with its
     residual, MLP block in checkpoint mode) resident on the device, bf16.
 
     qk: the heads' position rotation (its T, Hq, Hk, dh those of the block), with case["freq"], case["pos"]
     (int32 [axes, b*s]; None or missing: positions within each sequence) and the gains case["gq"], case["gk"]
-    [dh] of the queries' and keys' norms (None or missing: no norm).  The block's eps serves these norms too."""
+    [dh] of the queries' and keys' norms (None or missing: no norm).  The block's eps serves these norms too.
+
+    Inputs and weights are the entries of self.t and gradients those of self.grads, dg_attn, dg_mlp, dgq and dgk, as
+    they are when a call is made: each may be replaced by a tensor of its size and type."""
 
     def __init__(self, shape, case: Dict[str, object], device="cuda", qk: Optional[QkShape] = None):
         self.sh = shape
         self.t = {k: v.to(device).contiguous() for k, v in case.items() if isinstance(v, torch.Tensor)}
-        t = self.t
-        self.qk = self.dgq = self.dgk = None
+        t, bf16, f32 = self.t, torch.bfloat16, torch.float32
+        self._rotation = self.dgq = self.dgk = None
+        self._made, self._fits = {}, {n: (tuple(t[n].shape), bf16) for n in ("g_attn", "g_mlp", *_BLOCK_PAIRS)}
         if qk is not None:
             if (qk.T, qk.Hq, qk.Hk, qk.dh, qk.dtype) != (shape.T, shape.H, shape.H, shape.dh, "bf16"):
                 raise ValueError("the rotation's tokens, heads or type are not those of the block")
             if len(case["freq"]) != qk.rot // 2:
                 raise ValueError(f"{len(case['freq'])} frequencies for {qk.rot // 2} pairs")
-            for n, size, dtype in (("pos", (len(qk.sec), qk.T), torch.int32), ("gq", (qk.dh,), torch.bfloat16),
-                                   ("gk", (qk.dh,), torch.bfloat16)):
-                if n in t and (tuple(t[n].shape) != size or t[n].dtype != dtype):
-                    raise ValueError(f"{n}: {list(size)} {dtype} needed, not {list(t[n].shape)} {t[n].dtype}")
+            self._fits.update(turns=((qk.rot // 2,), torch.int64), pos=((len(qk.sec), qk.T), torch.int32),
+                              gq=((qk.dh,), bf16), gk=((qk.dh,), bf16), dgq=((qk.dh,), f32), dgk=((qk.dh,), f32))
+            self._rotation = _qk_shape(qk)
             self.turns = L.turns_tensor(case["freq"], device)
-            self.qk = L.lr_block_qk(_qk_shape(qk), L._p(self.turns), *(L._p(t.get(n)) for n in ("pos", "gq", "gk")))
-            self.dgq, self.dgk = (torch.empty(qk.dh, dtype=torch.float32, device=device) if n in t else None
+            self.dgq, self.dgk = (torch.empty(qk.dh, dtype=f32, device=device) if n in t else None
                                   for n in ("gq", "gk"))
-        self.w = L.lr_block_weights(
-            L._p(t["g_attn"]), *(L.pair(t[f"A_{n}"], t[f"B_{n}"]) for n in "qkvo"), L._p(t["g_mlp"]),
-            *(L.pair(t[f"A_{n}"], t[f"B_{n}"]) for n in ("gate", "up", "down")))
         self.grads = {}
-        for n in ("q", "k", "v", "o", "gate", "up", "down"):
-            self.grads[f"dA_{n}"] = torch.empty(t[f"A_{n}"].shape, dtype=torch.float32, device=device)
-            self.grads[f"dB_{n}"] = torch.empty(t[f"B_{n}"].shape, dtype=torch.float32, device=device)
-        self.dg_attn = torch.empty(shape.d, dtype=torch.float32, device=device)
-        self.dg_mlp = torch.empty(shape.d, dtype=torch.float32, device=device)
-        gr = self.grads
-        self.g = L.lr_block_grads(
-            L._p(self.dg_attn), *(L.pair_grad(gr[f"dA_{n}"], gr[f"dB_{n}"]) for n in "qkvo"), L._p(self.dg_mlp),
-            *(L.pair_grad(gr[f"dA_{n}"], gr[f"dB_{n}"]) for n in ("gate", "up", "down")))
+        for n in _BLOCK_PAIRS:
+            self.grads["d" + n] = torch.empty(t[n].shape, dtype=f32, device=device)
+        self.dg_attn = torch.empty(shape.d, dtype=f32, device=device)
+        self.dg_mlp = torch.empty(shape.d, dtype=f32, device=device)
+        self._fits.update({"d" + n: (self._fits[n][0], f32) for n in _BLOCK_PAIRS}, dg_attn=((shape.d,), f32),
+                          dg_mlp=((shape.d,), f32))
         dims = (shape.b, shape.s, shape.H, shape.dh, shape.f, shape.ra, shape.rm)
         self.dims = dims
         self.out = torch.empty_like(t["x"])
         self.dx = torch.empty_like(t["x"])
-        rotated = self.qk is not None
+        rotated = self._rotation is not None
         self.saved = _buf((L.lr_block_qk_saved_bytes if rotated else L.lr_block_saved_bytes)(*dims), device)
         self.ws = _buf((L.lr_block_qk_workspace_bytes if rotated else L.lr_block_workspace_bytes)(*dims), device)
+        self.w, self.g, self.qk  # refuse what does not fit
+
+    def _struct(self, kind, tensors, make):
+        """What `make` builds of the tensors' pointers, kept with their memory until one of them changes."""
+        given = [t for t in tensors.values() if t is not None]
+        now = ([t is None for t in tensors.values()], _facts(given))
+        made = self._made.get(kind)
+        if made is None or made[0] != now:
+            for n, t in tensors.items():
+                size, dtype = self._fits[n]
+                if t is not None and (tuple(t.shape) != size or t.dtype != dtype or not t.is_contiguous()
+                                      or t.device != self.out.device):
+                    raise ValueError(f"{n}: {list(size)} {dtype} on {self.out.device} needed, contiguous, not "
+                                     f"{list(t.shape)} {t.dtype} on {t.device} with strides {t.stride()}")
+            made = self._made[kind] = (now, make(*map(L._p, tensors.values())), [t.detach() for t in given])
+        return made[1]
+
+    @property
+    def w(self) -> L.lr_block_weights:
+        t = self.t
+        return self._struct("w", {n: t[n] for n in ("g_attn", "g_mlp", *_BLOCK_PAIRS)},
+                            lambda ga, gm, *p: _block_struct(L.lr_block_weights, L.pair, ga, gm, p))
+
+    @property
+    def g(self) -> L.lr_block_grads:
+        gr = self.grads
+        return self._struct("g", {"dg_attn": self.dg_attn, "dg_mlp": self.dg_mlp,
+                                  **{"d" + n: gr["d" + n] for n in _BLOCK_PAIRS}},
+                            lambda ga, gm, *p: _block_struct(L.lr_block_grads, L.pair_grad, ga, gm, p))
+
+    @property
+    def qk(self) -> Optional[L.lr_block_qk]:
+        if self._rotation is None:
+            return None
+        t = self.t
+        return self._struct("qk", {"turns": self.turns, "pos": t.get("pos"), "gq": t.get("gq"), "gk": t.get("gk")},
+                            lambda *at: L.lr_block_qk(self._rotation, *at))
 
     def forward(self, stream=None):
         common = (L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w)
-        if self.qk is None:
+        if self._rotation is None:
             L.lr_block_fwd(*common, self.out, self.saved, self.ws, stream)
         else:
             L.lr_block_qk_fwd(*common, self.qk, self.out, self.saved, self.ws, stream)
 
     def backward(self, stream=None):
         common = (L.LR_BF16, *self.dims, self.sh.eps, self.t["x"], self.w)
-        if self.qk is None:
+        if self._rotation is None:
             L.lr_block_bwd(*common, self.saved, self.t["G"], self.dx, self.g, self.ws, stream)
         else:
+            self._struct("dg", {"dgq": self.dgq, "dgk": self.dgk}, lambda *at: None)
             L.lr_block_qk_bwd(*common, self.qk, self.saved, self.t["G"], self.dx, self.g, self.dgq, self.dgk, self.ws,
                               stream)
 

@@ -143,3 +143,106 @@ def test_in_place_by_assignment():
     run.qo, run.ko = run.q, run.k
     run.forward()
     assert all(torch.equal(getattr(run, n), getattr(want, n)) for n in OUTPUTS)
+
+
+BLOCK = I.BlockShape(1, 256, 2, 128, 344, 32, 48)
+BLOCK_QK = I.QkShape(T=256, Hq=2, Hk=2, dh=128, rot=128, sec=(40, 24))
+PAIRS = [f"{m}_{n}" for n in ("q", "k", "v", "o", "gate", "up", "down") for m in "AB"]
+
+
+def _block_case(seed=0):
+    case, qk = I.make_block_case(BLOCK, seed), I.make_qk_case(BLOCK_QK, seed, with_grad=False)
+    return dict(case, **{n: qk[n] for n in ("gq", "gk", "pos", "freq")})
+
+
+def _pointers(struct):
+    """The pointers of a struct of pairs, in order."""
+    out = []
+    for name, _ in struct._fields_:
+        v = getattr(struct, name)
+        out += _pointers(v) if hasattr(v, "_fields_") else [v]
+    return out
+
+
+@pytest.fixture
+def block_calls(monkeypatch):
+    made = {}
+    for name in ("lr_block_qk_fwd", "lr_block_qk_bwd"):
+        monkeypatch.setattr(R.L, name, lambda *args, _name=name: made.__setitem__(_name, args))
+    return made
+
+
+@pytest.mark.parametrize("name", ["x", "pos", "gq", "gk", "g_attn", "g_mlp", "A_q", "B_o", "A_gate", "B_down"])
+def test_the_block_reads_the_tensors_of_the_moment(block_calls, name):
+    blk = R.TransformerBlock(BLOCK, _block_case(), device="cpu", qk=BLOCK_QK)
+    blk.step()
+    t = blk.t[name] = blk.t[name].clone()
+    for renew in (False, True):
+        if renew:
+            t.data = t.data.clone()
+        block_calls.clear()
+        blk.step()
+        for args in block_calls.values():
+            x, w, qk = args[9], args[10], args[11]
+            assert x is blk.t["x"]
+            assert (qk.turns, qk.pos, qk.gq, qk.gk) == (blk.turns.data_ptr(), *(blk.t[n].data_ptr() for n in
+                                                                               ("pos", "gq", "gk")))
+            order = ["g_attn", *PAIRS[:8], "g_mlp", *PAIRS[8:]]
+            assert _pointers(w) == [blk.t[n].data_ptr() for n in order]
+
+
+def test_the_block_writes_the_gradients_of_the_moment(block_calls):
+    blk = R.TransformerBlock(BLOCK, _block_case(), device="cpu", qk=BLOCK_QK)
+    blk.step()
+    for n in list(blk.grads):
+        blk.grads[n] = torch.empty_like(blk.grads[n])
+    blk.dg_attn, blk.dgq = torch.empty_like(blk.dg_attn), torch.empty_like(blk.dgq)
+    blk.grads["dA_v"].data = torch.empty_like(blk.grads["dA_v"])
+    blk.step()
+    g, dgq = block_calls["lr_block_qk_bwd"][15], block_calls["lr_block_qk_bwd"][16]
+    order = [blk.dg_attn, *(blk.grads["d" + n] for n in PAIRS[:8]), blk.dg_mlp, *(blk.grads["d" + n] for n in PAIRS[8:])]
+    assert _pointers(g) == [t.data_ptr() for t in order] and dgq is blk.dgq
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("pos", lambda t: t.long()), ("pos", lambda t: t[:1]), ("gq", lambda t: t[:64]), ("gk", lambda t: t.float()),
+    ("A_q", lambda t: t[:8]), ("B_up", lambda t: t.float()), ("A_o", lambda t: t.repeat(1, 2)[:, ::2]),
+    ("g_mlp", lambda t: t.to("meta")),
+])
+def test_the_block_refuses_what_does_not_fit(block_calls, name, bad):
+    blk = R.TransformerBlock(BLOCK, _block_case(), device="cpu", qk=BLOCK_QK)
+    old = blk.t[name]
+    blk.step()
+    block_calls.clear()
+    blk.t[name] = bad(old)
+    for call in (blk.forward, blk.backward):
+        with pytest.raises(ValueError, match=name):
+            call()
+    assert not block_calls
+    blk.t[name] = old
+    blk.step()
+    blk.grads["dA_k"] = blk.grads["dA_k"].bfloat16()
+    with pytest.raises(ValueError, match="dA_k"):
+        blk.backward()
+    blk.grads["dA_k"] = blk.grads["dA_k"].float()
+    blk.dgk = blk.dgk[:64]
+    with pytest.raises(ValueError, match="dgk"):
+        blk.backward()
+
+
+@pytest.mark.gpu
+def test_the_block_follows_new_positions_gains_weights_and_gradients():
+    first, second = _block_case(1), _block_case(2)
+    blk = R.TransformerBlock(BLOCK, first, qk=BLOCK_QK)
+    blk.step()
+    for n, v in second.items():
+        if isinstance(v, torch.Tensor):
+            blk.t[n] = v.cuda()
+    blk.grads = {n: torch.zeros_like(g) for n, g in blk.grads.items()}
+    blk.step()
+    fresh = R.TransformerBlock(BLOCK, second, qk=BLOCK_QK)
+    fresh.step()
+    assert torch.equal(blk.out, fresh.out) and torch.equal(blk.dx, fresh.dx)
+    assert all(torch.equal(a, b) for a, b in zip(blk.grad_tensors(), fresh.grad_tensors()))
+    assert torch.equal(blk.clip_grads(0.5), fresh.clip_grads(0.5))
+    assert all(torch.equal(a, b) for a, b in zip(blk.grad_tensors(), fresh.grad_tensors()))
