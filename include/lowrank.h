@@ -260,8 +260,12 @@ lr_status lr_attn_bwd(lr_dtype dt, int b, int s, int H, int dh, float scale, con
  * (the same pointer and row distance: qo = q, dq = dqo, ...); outputs must not overlap
  * anything else.  Elements between rows' ends are not touched.
  * dh and rot multiples of 8, 8 <= dh <= 256 (or dh <= 512 with dh and rot multiples of 16),
- * 0 <= rot <= dh, axes 1..4, H*dh <= 2^24 and T*H <= 2^30 for each tensor.  Sums over channels and the dg sums are fp32; y, dx are rounded
- * once.  |x| must stay below 1e18 (the square sums are fp32).
+ * 0 <= rot <= dh, axes 1..4, H*dh <= 2^24 and T*H <= 2^30 for each tensor.
+ * Sums over channels and the dg sums are fp32; y, dx are rounded once.  With a gain, the
+ * Euclidean norm of every head vector of x must stay below 1.8e19, so that its square is an
+ * fp32 number (|x| <= 7.9e17 in every channel keeps it there at any dh), and in the backward
+ * so must its sum of |dn g x|.  With eps below 1e-35 (0 among them) that norm must be at
+ * least 4e-18: squares of less are lost, and a vector of zeros has no direction to scale.
  */
 typedef enum { LR_PAIR_HALF = 0, LR_PAIR_ADJACENT = 1 } lr_pair_layout;
 
