@@ -465,6 +465,26 @@ def _qk_shape(s: QkShape) -> L.lr_qk_shape:
     return L.qk_shape(s.Hq, s.Hk, s.dh, s.rot, s.sec, layouts[s.layout], s.seq)
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors with contiguous rows share an element."""
+
+    def span(t):  # address, bytes of a row, bytes from row to row, bytes in all
+        row = t.shape[-1] * t.element_size()
+        if t.dim() < 2 or t.shape[0] < 2:
+            return t.data_ptr(), row, 0, row
+        step = t.stride(0) * t.element_size()
+        return t.data_ptr(), row, step, (t.shape[0] - 1) * step + row
+
+    if not a.numel() or not b.numel():
+        return False
+    (pa, ra, sa, na), (pb, rb, sb, nb) = span(a), span(b)
+    if pa + na <= pb or pb + nb <= pa:
+        return False
+    if sa != sb or sa == 0:
+        return True
+    return (pb - pa) % sa < ra or (pa - pb) % sa < rb  # columns of one matrix
+
+
 class QkRotary:
     """Norm and position rotation of queries and keys between their projections and attention.
 
@@ -475,7 +495,9 @@ class QkRotary:
 
     The tensors are attributes, and may be replaced by others of their size and type on the same device, 16-byte
     aligned (run.q = ..., run.qo = run.q for a forward in place).  The calls' arguments are converted once for
-    each assignment: a tensor that is given other memory by other means is to be assigned again.  The shape is fixed.
+    each assignment: a tensor that is given other memory by other means is to be assigned again.  An output may take
+    the place of its own input (qo of q, ko of k, dq of dqo, dk of dko) and overlaps no other tensor of its call.  The
+    shape is fixed.
     """
 
     _FORWARD = ("turns", "pos", "gq", "gk", "q", "k", "qo", "ko")
@@ -507,9 +529,9 @@ class QkRotary:
         self.dgq = torch.empty(s.dh, dtype=f32, device=device) if back and s.Hq and self.gq is not None else None
         self.dgk = torch.empty(s.dh, dtype=f32, device=device) if back and s.Hk and self.gk is not None else None
         self.ws = _buf(L.lr_qk_bwd_workspace_bytes(self.dt, s.T, self.sh), device) if back else None
-        self._prepare_forward()
+        self._convert_forward()
         if back:
-            self._prepare_backward()
+            self._convert_backward()
 
     def __setattr__(self, name, value):
         if name in self._TENSORS:
@@ -540,13 +562,34 @@ class QkRotary:
         return (self.dt, self.s.T, L.ctypes.pointer(self.sh), self.s.eps, self.turns, self.pos, self.gq, self.gk,
                 *self._rows("q", "k"))
 
+    def _apart(self, names, outputs):
+        """Refuses outputs that overlap one another or an input of their call."""
+        tensors = {n: t for n in names if (t := getattr(self, n)) is not None}
+        own = {"qo": "q", "ko": "k", "dq": "dqo", "dk": "dko"}
+        for o, out in ((o, tensors[o]) for o in outputs if o in tensors):
+            for n, t in tensors.items():
+                if n == o or not _overlap(out, t):
+                    continue
+                if n == own.get(o) and out.data_ptr() == t.data_ptr() and (self.s.T == 1 or out.stride(0) == t.stride(0)):
+                    continue
+                raise ValueError(f"{o} overlaps {n}")
+
     def _prepare_forward(self):
-        self._fwd = L.Prepared("lr_qk_fwd", *self._common(), *self._rows("qo", "ko"))
-        return self._fwd
+        self._apart(self._FORWARD, ("qo", "ko"))
+        return self._convert_forward()
 
     def _prepare_backward(self):
         if self.ws is None or (self.dqo is None and self.dko is None):
             raise ValueError("no upstream gradients dqo, dko were given")
+        unused = {n for g, names in ((self.gq, ("q", "dgq")), (self.gk, ("k", "dgk"))) if g is None for n in names}
+        self._apart([n for n in self._BACKWARD if n not in unused], ("dq", "dk", "dgq", "dgk", "ws"))
+        return self._convert_backward()
+
+    def _convert_forward(self):
+        self._fwd = L.Prepared("lr_qk_fwd", *self._common(), *self._rows("qo", "ko"))
+        return self._fwd
+
+    def _convert_backward(self):
         self._bwd = L.Prepared("lr_qk_bwd", *self._common(), *self._rows("dqo", "dko", "dq", "dk"), self.dgq, self.dgk,
                                self.ws, L._nbytes(self.ws))
         return self._bwd

@@ -246,3 +246,48 @@ def test_the_block_follows_new_positions_gains_weights_and_gradients():
     assert all(torch.equal(a, b) for a, b in zip(blk.grad_tensors(), fresh.grad_tensors()))
     assert torch.equal(blk.clip_grads(0.5), fresh.clip_grads(0.5))
     assert all(torch.equal(a, b) for a, b in zip(blk.grad_tensors(), fresh.grad_tensors()))
+
+
+def _packed(T, width, dtype=torch.bfloat16):
+    m = torch.zeros(T, width, dtype=dtype)
+    return lambda a, b: m[:, a:b]
+
+
+@pytest.mark.parametrize("change", [
+    lambda r: setattr(r, "qo", r.k.new_zeros(6, 96)) or setattr(r, "ko", r.qo[:, :64]),        # two outputs
+    lambda r: setattr(r, "qo", r.dqo) or setattr(r, "dq", r.dqo) or setattr(r, "q", r.dqo),     # dq in q's place
+    lambda r: setattr(r, "dgk", r.dgq),
+    lambda r: setattr(r, "q", r.q[:1].expand(6, 96).clone()) or setattr(r, "ko", r.q[:, 8:72]),  # k's output in q
+    lambda r: setattr(r, "ws", r.dq.view(torch.uint8).view(-1)),
+    lambda r: setattr(r, "qo", torch.zeros(9, 96, dtype=torch.bfloat16)[3:]) or setattr(r, "q", r.qo._base[:6]),
+    lambda r: (lambda at: setattr(r, "qo", at(0, 96)) or setattr(r, "ko", at(88, 152)))(_packed(6, 200)),
+])
+def test_outputs_that_overlap_are_refused(calls, change):
+    run = R.QkRotary(SHAPE, I.make_qk_case(SHAPE), device="cpu")
+    change(run)
+    with pytest.raises(ValueError, match="overlap"):
+        run.step()
+    assert "lr_qk_bwd" not in calls
+
+
+def test_outputs_beside_one_another_and_in_place_are_not(calls):
+    run = R.QkRotary(SHAPE, I.make_qk_case(SHAPE), device="cpu")
+    at, back = _packed(6, 200), _packed(6, 160)
+    run.q, run.k, run.qo, run.ko = at(0, 96), at(96, 160), at(0, 96), at(96, 160)  # columns of one matrix, in place
+    run.dqo, run.dko = back(64, 160), back(0, 64)
+    run.dq, run.dk = run.dqo, run.dko
+    run.step()
+    run.k = run.q[:, :64]  # inputs may share memory ...
+    run.ko = torch.zeros(6, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="overlap"):
+        run.step()  # ... but not with an output
+    run.qo = torch.zeros(6, 96, dtype=torch.bfloat16)
+    run.step()
+    run.gq = None
+    run.dq = run.q  # not read by a backward without the norm
+    run.backward()
+    one = dataclasses.replace(SHAPE, T=1)
+    run = R.QkRotary(one, I.make_qk_case(one), device="cpu")
+    row = torch.zeros(1, 160, dtype=torch.bfloat16)
+    run.q, run.qo, run.ko = row[:, :96], row[:, :96], row[:, 96:]
+    run.step()
