@@ -283,6 +283,7 @@ def test_outputs_beside_one_another_and_in_place_are_not(calls):
         run.step()  # ... but not with an output
     run.qo = torch.zeros(6, 96, dtype=torch.bfloat16)
     run.step()
+    run.k = torch.zeros(6, 64, dtype=torch.bfloat16)  # apart from q again
     run.gq = None
     run.dq = run.q  # not read by a backward without the norm
     run.backward()
