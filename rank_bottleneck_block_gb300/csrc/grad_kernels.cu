@@ -1,11 +1,14 @@
 // Both passes are bound by memory: a thread has 128 bytes in flight (16-byte loads), a block takes consecutive chunks of
 // the tensors' concatenation, and there are several times as many blocks as run at once, since SMs do not get the same
-// share of the bandwidth.  The scaling pass goes through the chunks backwards, so that it finds in L2 what the sum
-// read last: all but the last 64 MB of the sum's reads and all of the outputs are marked to leave L2 first.
-// Measured, fp32, clipped into other tensors: 283 million elements (168 tensors) 478 us, of which the sum 154 us
-// (1.13 GB at 7.3 TB/s); 80 million (16 tensors) 135 us; what both passes move at the copy rate is 509 and 144 us
-// less the part found in L2, and reading and writing once would be 339 and 96 us.  20 million bf16 elements in 613
-// tensors of uneven sizes 21 us; 181,000 fp32 elements in one launch 5 us.
+// share of the bandwidth.  A launch that scales goes through its chunks backwards, so that one that takes the whole list
+// finds in L2 what the sum read last: all but the last 64 MB of a launch's reads and all of the outputs are marked to
+// leave L2 first.  Lists of more than kGradTable tensors are scaled launch by launch in the order of their sums,
+// which loses that unless L2 holds the whole list.
+// Measured, fp32, clipped into other tensors, three sets of buffers in turn (in brackets the same ones each time, of
+// which L2 still holds some): 283 million elements (168 tensors) 484 us (478), of which the sum 154 us; 80 million (16
+// tensors) 141 us (135); what both passes move at the copy rate is 509 and 144 us less the part found in L2, and reading
+// and writing once would be 339 and 96 us.  20 million bf16 elements in 613 tensors of uneven sizes 24 us; 181,000 fp32
+// elements in one launch 5 us.
 #include "grad_kernels.cuh"
 
 #include <cooperative_groups.h>
@@ -297,7 +300,8 @@ cudaError_t launch_grad_stat(const GradStat& gs, cudaStream_t st) {
 template <typename ST, int N>
 cudaError_t launch_grad_scale(const GradTable<N>& tab, const GradStat& gs, bool in_place, cudaStream_t st) {
   // Chunks of a block.  In place the launch often finds a scale of 1, and then only starts and ends its blocks: of 283
-  // million fp32 elements, two chunks to a block take 169 us with the sum (484 where they are scaled), four 161 (488).
+  // million fp32 elements, two chunks to a block take 169 us with the sum (484 where they are scaled), four 162 (487),
+  // the same buffers each time.
   constexpr int kInPlaceEach = 4;
   const int chunks = tab.first[tab.n], each = in_place ? std::min(kInPlaceEach, std::max(2, chunks / 2432)) : 2;
   return launch_pdl(grad_scale_kernel<ST, N>, dim3(grad_blocks(chunks, each)), dim3(kThreads), 0, st, tab, gs, each,

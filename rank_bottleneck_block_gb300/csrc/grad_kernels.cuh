@@ -13,7 +13,7 @@ constexpr int kGradOwners = 256;        // entries that say where to look for a 
 constexpr int kGradChunkBytes = 32768;  // what 256 threads take at a time (8 16-byte words each)
 constexpr int kGradParts = 3040;        // most blocks of one launch that sums, each writing one partial sum
 constexpr int kGradFew = 512;           // partial sums that the scaling blocks add up themselves
-constexpr int kGradKeepBytes = 64 << 20;  // the last of the sum's reads, which the scaling finds in L2
+constexpr int kGradKeepBytes = 64 << 20;  // the last of a launch's reads, which a scaling right behind it finds in L2
 constexpr int kGradSmall = 32;          // chunks that one cluster sums and scales in one launch
 
 // The tensors of one launch, passed by value with it (no host-to-device copy, so a call can be captured).

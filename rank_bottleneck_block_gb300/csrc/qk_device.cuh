@@ -356,7 +356,8 @@ struct QkVariant {
 inline QkVariant variant(const QkArgs& a, size_t es, bool wide = true) {
   wide = a.dh > 256 || (wide && es == 2 && a.dh % 16 == 0 && a.rot % 16 == 0);
   const int u = wide ? 8 : 4, slots = a.dh / (2 * u);
-  // 6 and 3 vectors a warp, not 4 and 2: 16 + 2 heads of 72 in bf16, 40003 tokens: 46 us against 61
+  // 6 and 3 vectors a warp, not 4 and 2: 16 + 2 heads of 72 in bf16, 40003 tokens: 46 us against 61 (floor 31).  The
+  // same count would serve 3 and 6 slots (24 of 32 lanes now); it has not been built or measured for them.
   if (slots == 5 || slots == 9 || slots == 10) return {u, slots == 5 ? 5 : 10};
   return {u, slots <= 4 && es == 2 ? 4 : slots <= 8 ? 8 : slots <= 16 ? 16 : 32};
 }
