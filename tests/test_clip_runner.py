@@ -79,7 +79,9 @@ def test_buffers_are_made_on_the_stream_of_the_call(monkeypatch, calls):
     assert made and all(s is None for s in made)
 
 
-def test_a_handle_of_a_stream_serves_too(monkeypatch, calls):
+@pytest.mark.parametrize("handle,want", [(1234, ("external", 1234)), (0, "default")])
+def test_a_handle_of_a_stream_serves_too(monkeypatch, calls, handle, want):
+    """0 is the default stream: torch would make a new stream of it."""
     seen = []
 
     @contextlib.contextmanager
@@ -89,8 +91,9 @@ def test_a_handle_of_a_stream_serves_too(monkeypatch, calls):
 
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
-    Holder([torch.randn(64)]).clip_grads(1.0, stream=1234)
-    assert seen == [("external", 1234)] and calls[0][1] == 1234
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    Holder([torch.randn(64)]).clip_grads(1.0, stream=handle)
+    assert seen == [want] and calls[0][1] == handle
 
 
 def test_buffers_stay_when_gradients_are_replaced(calls):
@@ -246,3 +249,19 @@ def test_what_changed_is_clipped_on_the_gpu(change):
     assert abs(float(h.clip_grads(1.0)) - norm) <= 34 * 2.0 ** -24 * norm
     for t, k in zip(h.tensors, keep):
         assert ((t.double() - k / (norm + 1e-6)).abs() <= 41 * 2.0 ** -24 * k / norm + 1e-40).all()
+
+
+@pytest.mark.gpu
+def test_the_default_streams_handle():
+    h, side = Holder([torch.arange(64.0).cuda()]), torch.cuda.Stream()
+    norm = float(h.tensors[0].norm())
+    torch.cuda.synchronize()
+    seen = []
+    with torch.cuda.stream(side):
+        with R._current(0):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+        with R._current(side.cuda_stream):
+            seen.append(torch.cuda.current_stream().cuda_stream)
+        got = h.clip_grads(1.0, stream=0)
+    torch.cuda.synchronize()
+    assert seen == [0, side.cuda_stream] and float(got) == pytest.approx(norm, rel=1e-6)
