@@ -296,6 +296,78 @@ lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const 
                     long long lddq, void* dk, long long lddk, float* dgq, float* dgk, void* ws, size_t ws_bytes,
                     void* stream);
 
+/* ------------------------------------------- packed causal attention
+ * Causal self-attention over nseq sequences of different lengths that lie one behind the
+ * other in T rows, with query heads that share key heads (lr_attn_* takes sequences of one
+ * length and a key head for each query head).  Sequence i is rows offs[i] .. offs[i+1] - 1;
+ * offs: device int32 [nseq + 1], 0 <= offs[0] <= offs[1] <= ... <= offs[nseq] <= T, so a
+ * sequence may be empty.  G = Hq / Hk; query head h reads key head h / G.  Row t of a
+ * sequence, j over the rows of that sequence up to t:
+ *     S_tj = scale q_t.k_j,  lse_t = log sum_j exp(S_tj),  o_t = sum_j exp(S_tj - lse_t) v_j,
+ * and the backward of sum(o * dout):
+ *     D_t = dout_t.o_t,  P = exp(S - lse),  dS = scale P (dout_t.v_j - D_t),
+ *     dq_t = sum_j dS_tj k_j,  dk_j = sum dS_tj q_t,  dv_j = sum P_tj dout_t
+ * (the last two over the rows t >= j and the G query heads of the key head).
+ * q, o, dout, dq: [T, Hq*dh], k, v, dk, dv: [T, Hk*dh], rows ldq, ldk, ... elements apart: a
+ * multiple of 8, at least the row's own width, so q, k and v may be columns of one packed
+ * matrix.  lse: [T, Hq] fp32, contiguous, natural logarithm; the backward reads o and lse of
+ * the forward.  Outputs must not overlap anything else.
+ * Rows of no sequence (before offs[0], from offs[nseq] on) are not written and do not reach
+ * any result, whatever they hold.  A value that is not finite reaches results of its own
+ * sequence only, there also those of rows before it.
+ * bf16 only (LR_F32: LR_ERR_UNSUPPORTED).  Hq a multiple of Hk, G <= 128, dh a multiple of 8
+ * up to 128, H*dh <= 2^24, T*Hq <= 2^30, nseq <= 2^24; scale finite and positive.
+ * Products are of bf16 operands summed in fp32; P and dS are rounded to bf16 for theirs, the
+ * softmax statistics, O, dQ, dK and dV are fp32 until they are rounded once.
+ * Offsets live on the device and are read there: if they are not in order or leave the
+ * rows, the call writes no result and lr_check_device_error reports LR_ERR_SHAPE.
+ * Launched without programmatic dependent launch, as lr_attn_*.
+ */
+typedef struct {
+  int T, nseq;
+  int Hq, Hk, dh;
+} lr_packed_shape;
+
+size_t lr_packed_attn_fwd_workspace_bytes(const lr_packed_shape* sh);
+size_t lr_packed_attn_bwd_workspace_bytes(const lr_packed_shape* sh);
+lr_status lr_packed_attn_fwd(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
+                             long long ldq, const void* k, long long ldk, const void* v, long long ldv, void* o,
+                             long long ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
+lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
+                             long long ldq, const void* k, long long ldk, const void* v, long long ldv, const void* o,
+                             long long ldo, const float* lse, const void* dout, long long lddout, void* dq,
+                             long long lddq, void* dk, long long lddk, void* dv, long long lddv, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* --------------------------------------- log probabilities of tokens
+ * What a language model's last layer is trained on and answers with.  logits [T, V], rows
+ * ld elements apart (any ld >= V, V odd too); per row, z_j = scale * logits_j (scale: one
+ * over the temperature):
+ *     lse = log sum_j exp(z_j),  p_j = exp(z_j - lse),
+ *     logp = z_target - lse,     entropy = -sum_j p_j log p_j.
+ * target: device int32 [T]; a row whose target lies outside 0 .. V-1 has none: its logp is 0
+ * and passes no gradient.  top: the `top` largest logits of each row (0 .. 32, at most V), as
+ * top_ids int32 [T, top] and their log probabilities top_logp fp32 [T, top], the largest
+ * first, equal logits by their index, a NaN before any number; top = 0: both unused and may
+ * be NULL.  logp, entropy, lse: fp32 [T].
+ * A logit of -inf has p = 0.  A row of nothing else has lse = -inf, entropy 0, and no
+ * gradient.  A row that holds a NaN or +inf has NaN for all three.
+ * Backward of sum(dlogp * logp + dentropy * entropy):
+ *     dlogits_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + entropy)).
+ * dlogp: fp32 [T]; dentropy: fp32 [T] or NULL (entropy is then unused and may be NULL);
+ * lse, entropy: the forward's.  dlogits may be logits (the same pointer and row distance).
+ * Rows without a gradient (no target or dlogp 0, and dentropy 0) are set to 0 unread.
+ * scale finite and positive; V <= 2^20, T <= 2^24; every pointer 16-byte aligned (rows need not be).
+ * Sums are fp32; the gradient is rounded once.
+ */
+size_t lr_logprob_workspace_bytes(lr_dtype dt, int T, int V, int top);
+lr_status lr_logprob_fwd(lr_dtype dt, int T, int V, float scale, int top, const void* logits, long long ld,
+                         const int* target, float* logp, float* entropy, float* lse, int* top_ids, float* top_logp,
+                         void* ws, size_t ws_bytes, void* stream);
+lr_status lr_logprob_bwd(lr_dtype dt, int T, int V, float scale, const void* logits, long long ld, const int* target,
+                         const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                         void* dlogits, long long lddlogits, void* stream);
+
 /* ------------------------------------------------- low-rank transformer block
  * One pre-norm LLaMA-style block whose linear maps are all low-rank pairs (d = H*dh,
  * T = b*s tokens, attention rank ra, MLP rank rm, MLP width f):
@@ -433,8 +505,9 @@ lr_status lr_proj_fwd_noalloc(lr_dtype dt, int T, int d_in, int d_out, int r, in
 /* ------------------------------------------------------------------ status
  * lr_last_error: message of the last failing call on this thread ("" if none).
  * lr_check_device_error: synchronises `stream`, reads and clears the current
- * device's error word; LR_ERR_TIMEOUT if a bounded wait ran out, LR_ERR_CUDA
- * if the stream reports an error, else LR_OK.
+ * device's error word; LR_ERR_TIMEOUT if a bounded wait ran out, LR_ERR_SHAPE if
+ * the offsets of a packed call were not in order, LR_ERR_CUDA if the stream
+ * reports an error, else LR_OK.
  * lr_selftest_wait_timeout: launches one kernel that waits on a barrier nothing
  * completes, for limit_ns nanoseconds, then sets the timeout bit and returns
  * (exercises the timeout path without any fault). */

@@ -149,6 +149,7 @@ enum DeviceError : unsigned {
   DEV_ERR_TIMEOUT_EPILOGUE = 4u,
   DEV_ERR_TIMEOUT_SELFTEST = 8u,
   DEV_ERR_TMEM = 16u,
+  DEV_ERR_OFFSETS = 32u,  // sequence offsets that are not in order (nothing was computed)
 };
 
 __device__ __forceinline__ uint64_t global_timer_ns() {

@@ -18,6 +18,8 @@
 #include "gemm.h"
 #include "attn_kernels.cuh"
 #include "grad_kernels.cuh"
+#include "logprob_kernels.cuh"
+#include "packed_attn.cuh"
 #include "qk_kernels.cuh"
 #include "small_kernels.cuh"
 
@@ -2604,6 +2606,226 @@ lr_status lr_proj_fwd_noalloc(lr_dtype dt, int T, int d_in, int d_out, int r, in
   return proj_fwd_impl(c, T, d_in, d_out, r, group, pairs, g, eps, x, outs, saved, scratch);
 }
 
+// ------------------------------------------------- packed attention
+static lr_status check_packed(lr_dtype dt, const lr_packed_shape* sh) {
+  LR_TRY(check_dtype(dt));
+  if (dt != LR_BF16) return fail(LR_ERR_UNSUPPORTED, "packed attention is bf16 only");
+  if (!sh) return fail(LR_ERR_NULL, "shape is NULL");
+  if (sh->T < 1) return fail(LR_ERR_SHAPE, "T = %d must be positive", sh->T);
+  if (sh->nseq < 1 || sh->nseq > (1 << 24)) return fail(LR_ERR_SHAPE, "nseq = %d must be 1..2^24", sh->nseq);
+  if (sh->Hk < 1 || sh->Hq < 1 || sh->Hq % sh->Hk || sh->Hq / sh->Hk > 128)
+    return fail(LR_ERR_SHAPE, "Hq = %d must be a multiple (1 to 128) of Hk = %d", sh->Hq, sh->Hk);
+  if (sh->dh < 8 || sh->dh > 128 || sh->dh % 8)
+    return fail(LR_ERR_SHAPE, "dh = %d must be a multiple of 8, 8..128", sh->dh);
+  if (1LL * sh->Hq * sh->dh > (1 << 24) || 1LL * sh->T * sh->Hq > (1LL << 30))
+    return fail(LR_ERR_SHAPE, "Hq*dh = %lld exceeds 2^24 or T*Hq = %lld exceeds 2^30", 1LL * sh->Hq * sh->dh,
+                1LL * sh->T * sh->Hq);
+  return LR_OK;
+}
+
+static lr_status check_scale(float scale) {
+  if (!(scale > 0.f) || scale > 3.4e38f) return fail(LR_ERR_SHAPE, "scale must be finite and positive");
+  return LR_OK;
+}
+
+// What the forward and the backward have in common.
+static lr_status check_packed_call(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
+                                   long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                                   const void* o, long long ldo, const float* lse, void* ws) {
+  LR_TRY(check_packed(dt, sh));
+  LR_TRY(check_scale(scale));
+  LR_TRY(check_ptr(offs, "offs"));
+  LR_TRY(check_rows(q, ldq, sh->Hq, sh->dh, "q"));
+  LR_TRY(check_rows(k, ldk, sh->Hk, sh->dh, "k"));
+  LR_TRY(check_rows(v, ldv, sh->Hk, sh->dh, "v"));
+  LR_TRY(check_rows(o, ldo, sh->Hq, sh->dh, "o"));
+  LR_TRY(check_ptr(lse, "lse"));
+  return check_ptr(ws, "ws");
+}
+
+static PackedRows packed_rows(const void* p, long long ld) {
+  return PackedRows{static_cast<bf16*>(const_cast<void*>(p)), ld};
+}
+
+static PackedArgs packed_args(const lr_packed_shape& sh, float scale, const int* offs, const void* q, long long ldq,
+                              const void* k, long long ldk, const void* v, long long ldv, const void* o, long long ldo,
+                              const float* lse) {
+  PackedArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = sh.T;
+  a.nseq = sh.nseq;
+  a.Hq = sh.Hq;
+  a.Hk = sh.Hk;
+  a.dh = sh.dh;
+  a.scale = scale;
+  a.offs = offs;
+  a.q = packed_rows(q, ldq);
+  a.k = packed_rows(k, ldk);
+  a.v = packed_rows(v, ldv);
+  a.o = packed_rows(o, ldo);
+  a.lse = const_cast<float*>(lse);
+  return a;
+}
+
+size_t lr_packed_attn_fwd_workspace_bytes(const lr_packed_shape* sh) {
+  t_last_error.clear();
+  if (check_packed(LR_BF16, sh)) return 0;
+  return packed_attn_fwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk);
+}
+
+size_t lr_packed_attn_bwd_workspace_bytes(const lr_packed_shape* sh) {
+  t_last_error.clear();
+  if (check_packed(LR_BF16, sh)) return 0;
+  return packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk);
+}
+
+lr_status lr_packed_attn_fwd(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
+                             long long ldq, const void* k, long long ldk, const void* v, long long ldv, void* o,
+                             long long ldo, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_packed_call(dt, sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse, ws));
+  LR_TRY(check_size(ws_bytes, packed_attn_fwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk), "ws"));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  const PackedArgs a = packed_args(*sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse);
+  const double rows = 2.0 * sh->T * sh->dh;
+  LaunchScope scope("packed_attn_fwd", c.st, 0, rows * (2.0 * sh->Hq + 2.0 * sh->Hk));
+  cudaError_t e = launch_packed_attn_fwd(a, ws, c.err, c.st);
+  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "packed attention: %s", cudaGetErrorString(e));
+  return LR_OK;
+}
+
+lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
+                             long long ldq, const void* k, long long ldk, const void* v, long long ldv, const void* o,
+                             long long ldo, const float* lse, const void* dout, long long lddout, void* dq,
+                             long long lddq, void* dk, long long lddk, void* dv, long long lddv, void* ws,
+                             size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_packed_call(dt, sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse, ws));
+  LR_TRY(check_rows(dout, lddout, sh->Hq, sh->dh, "dout"));
+  LR_TRY(check_rows(dq, lddq, sh->Hq, sh->dh, "dq"));
+  LR_TRY(check_rows(dk, lddk, sh->Hk, sh->dh, "dk"));
+  LR_TRY(check_rows(dv, lddv, sh->Hk, sh->dh, "dv"));
+  LR_TRY(check_size(ws_bytes, packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk), "ws"));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  PackedArgs a = packed_args(*sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse);
+  a.dout = packed_rows(dout, lddout);
+  a.dq = packed_rows(dq, lddq);
+  a.dk = packed_rows(dk, lddk);
+  a.dv = packed_rows(dv, lddv);
+  const double rows = 2.0 * sh->T * sh->dh;
+  LaunchScope scope("packed_attn_bwd", c.st, 0, rows * (4.0 * sh->Hq + 4.0 * sh->Hk));
+  cudaError_t e = launch_packed_attn_bwd(a, ws, c.err, c.st);
+  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "packed attention backward: %s", cudaGetErrorString(e));
+  return LR_OK;
+}
+
+// --------------------------------------- log probabilities of tokens
+static lr_status check_logprob(lr_dtype dt, int T, int V, int top) {
+  LR_TRY(check_dtype(dt));
+  LR_TRY(check_dim(T, "T", false));
+  if (V < 1 || V > kLogprobMaxV) return fail(LR_ERR_SHAPE, "V = %d must be 1..%d", V, kLogprobMaxV);
+  if (top < 0 || top > kLogprobMaxTop || top > V)
+    return fail(LR_ERR_SHAPE, "top = %d must be 0..%d and at most V = %d", top, kLogprobMaxTop, V);
+  return LR_OK;
+}
+
+static lr_status check_logit_rows(const void* p, long long ld, int V, const char* name) {
+  LR_TRY(check_ptr(p, name));
+  if (ld < V || ld > (1LL << 31))
+    return fail(LR_ERR_SHAPE, "%s: row distance %lld must be at least V = %d and at most 2^31", name, ld, V);
+  return LR_OK;
+}
+
+// Room for the plan of any GPU: more SMs cut rows into more parts.
+static size_t logprob_ws_layout(lr_dtype dt, int T, int V, int top, void* base, float4** part, float** segmax) {
+  const LogprobPlan p = logprob_plan(T, V, static_cast<int>(esize(dt)), 1 << 16);
+  Arena ar(base);
+  float4* at = static_cast<float4*>(ar.take(sizeof(float4) * T * p.splits));
+  float* sm = static_cast<float*>(ar.take(top > 0 ? sizeof(float) * T * p.nseg : 0));
+  if (part) *part = at;
+  if (segmax) *segmax = sm;
+  return ar.size();
+}
+
+size_t lr_logprob_workspace_bytes(lr_dtype dt, int T, int V, int top) {
+  t_last_error.clear();
+  if (check_logprob(dt, T, V, top)) return 0;
+  return logprob_ws_layout(dt, T, V, top, nullptr, nullptr, nullptr);
+}
+
+lr_status lr_logprob_fwd(lr_dtype dt, int T, int V, float scale, int top, const void* logits, long long ld,
+                         const int* target, float* logp, float* entropy, float* lse, int* top_ids, float* top_logp,
+                         void* ws, size_t ws_bytes, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_logprob(dt, T, V, top));
+  LR_TRY(check_scale(scale));
+  LR_TRY(check_logit_rows(logits, ld, V, "logits"));
+  LR_TRY(check_ptr(target, "target"));
+  LR_TRY(check_ptr(logp, "logp"));
+  LR_TRY(check_ptr(entropy, "entropy"));
+  LR_TRY(check_ptr(lse, "lse"));
+  if (top > 0) {
+    LR_TRY(check_ptr(top_ids, "top_ids"));
+    LR_TRY(check_ptr(top_logp, "top_logp"));
+  }
+  LR_TRY(check_ptr(ws, "ws"));
+  LogprobFwd a;
+  memset(&a, 0, sizeof(a));
+  LR_TRY(check_size(ws_bytes, logprob_ws_layout(dt, T, V, top, ws, &a.part, &a.segmax), "ws"));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  a.logits = logits;
+  a.ld = ld;
+  a.target = target;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.T = T;
+  a.V = V;
+  a.top = top;
+  a.scale = scale;
+  const LogprobPlan plan = logprob_plan(T, V, static_cast<int>(c.es), c.sms);
+  {
+    LaunchScope scope("logprob_fwd", c.st, 0, 1.0 * c.es * T * V);
+    cudaError_t e = dt == LR_BF16 ? launch_logprob_fwd<bf16>(a, plan, c.st) : launch_logprob_fwd<float>(a, plan, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities: %s", cudaGetErrorString(e));
+  }
+  if (logprob_joins(plan, top)) {
+    LaunchScope scope("logprob_join", c.st, 0, 1.0 * c.es * T * top * plan.seg);
+    cudaError_t e = dt == LR_BF16 ? launch_logprob_join<bf16>(a, plan, c.st) : launch_logprob_join<float>(a, plan, c.st);
+    if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities (join): %s", cudaGetErrorString(e));
+  }
+  return LR_OK;
+}
+
+lr_status lr_logprob_bwd(lr_dtype dt, int T, int V, float scale, const void* logits, long long ld, const int* target,
+                         const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                         void* dlogits, long long lddlogits, void* stream) {
+  t_last_error.clear();
+  LR_TRY(check_logprob(dt, T, V, 0));
+  LR_TRY(check_scale(scale));
+  LR_TRY(check_logit_rows(logits, ld, V, "logits"));
+  LR_TRY(check_ptr(target, "target"));
+  LR_TRY(check_ptr(lse, "lse"));
+  LR_TRY(check_ptr(dlogp, "dlogp"));
+  if (dentropy) {
+    LR_TRY(check_ptr(dentropy, "dentropy"));
+    LR_TRY(check_ptr(entropy, "entropy"));
+  }
+  LR_TRY(check_logit_rows(dlogits, lddlogits, V, "dlogits"));
+  Ctx c;
+  LR_TRY(make_ctx(dt, stream, &c));
+  LogprobBwd a{logits, ld, target, lse, entropy, dlogp, dentropy, dlogits, lddlogits, T, V, scale};
+  LaunchScope scope("logprob_bwd", c.st, 0, 2.0 * c.es * T * V);
+  cudaError_t e = dt == LR_BF16 ? launch_logprob_bwd<bf16>(a, c.st) : launch_logprob_bwd<float>(a, c.st);
+  if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities backward: %s", cudaGetErrorString(e));
+  return LR_OK;
+}
+
 lr_status lr_check_device_error(void* stream) {
   unsigned* p = nullptr;
   LR_TRY(device_error_word(&p));
@@ -2615,7 +2837,9 @@ lr_status lr_check_device_error(void* stream) {
   if (word) {
     const unsigned zero = 0;
     cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    return fail(LR_ERR_TIMEOUT, "device error word 0x%x (1 producer, 2 mma, 4 epilogue, 8 self-test timeout)", word);
+    if (word == DEV_ERR_OFFSETS)
+      return fail(LR_ERR_SHAPE, "the offsets of a packed call are not in order or leave its rows: it wrote no result");
+    return fail(LR_ERR_TIMEOUT, "device error word 0x%x (1 producer, 2 mma, 4 epilogue, 8 self-test timeout, 32 offsets)", word);
   }
   return LR_OK;
 }

@@ -22,7 +22,7 @@ shapes stand in for them):
 from __future__ import annotations
 
 import dataclasses
-from typing import Dict, List, Optional, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
@@ -35,6 +35,10 @@ __all__ = [
     "QkShape",
     "rotary_freq",
     "make_qk_case",
+    "PackedShape",
+    "make_packed_case",
+    "LogProbShape",
+    "make_logprob_case",
     "MLP_TINY_F32",
     "MLP_BLOCK_BF16",
     "ATTN_PROJ_BF16",
@@ -221,6 +225,72 @@ def make_qk_case(shape: QkShape, seed: int = 0, norm: bool = True, with_grad: bo
     c["freq"] = rotary_freq(shape.rot)
     if with_grad:
         c["dqo"], c["dko"] = rows()
+    return c
+
+
+@dataclasses.dataclass(frozen=True)
+class PackedShape:
+    """Causal attention over nseq sequences packed in T rows: Hq query heads, which share Hk key heads, of dh channels;
+    scale: dh^-0.5 unless given."""
+
+    T: int
+    nseq: int
+    Hq: int
+    Hk: int
+    dh: int
+    scale: Optional[float] = None
+    dtype: str = "bf16"
+
+
+def make_packed_case(shape: PackedShape, lengths: Sequence[int], seed: int = 0, first: int = 0, with_grad: bool = True,
+                     packed: bool = False, device: str = "cpu") -> Dict[str, object]:
+    """q [T, Hq*dh], k, v [T, Hk*dh] (packed: columns of one [T, (Hq + 2 Hk)*dh] matrix) and the upstream grad dout,
+    ~N(0, 1); offs int32 [nseq + 1]: sequences of these lengths from row `first` on."""
+    if len(lengths) != shape.nseq:
+        raise ValueError(f"{len(lengths)} lengths for {shape.nseq} sequences")
+    dt = _torch_dtype(shape.dtype)
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    nq, nk = shape.Hq * shape.dh, shape.Hk * shape.dh
+    m = _normal(gen, (shape.T, nq + 2 * nk), 1.0).to(dt)
+    c: Dict[str, object] = dict(zip("qkv", m.split([nq, nk, nk], dim=1)))
+    if not packed:
+        c = {n: t.contiguous() for n, t in c.items()}
+    offs = [first]
+    for n in lengths:
+        offs.append(offs[-1] + n)
+    c["offs"] = torch.tensor(offs, dtype=torch.int32, device=device)
+    if with_grad:
+        c["dout"] = _normal(gen, (shape.T, nq), 1.0).to(dt)
+    return c
+
+
+@dataclasses.dataclass(frozen=True)
+class LogProbShape:
+    """Log probabilities of T tokens under logits over a vocabulary of V, times scale (one over the temperature), with
+    each row's `top` largest logits."""
+
+    T: int
+    V: int
+    top: int = 0
+    scale: float = 1.0
+    dtype: str = "bf16"
+
+
+def make_logprob_case(shape: LogProbShape, seed: int = 0, with_grad: bool = True, entropy: bool = True,
+                      device: str = "cpu") -> Dict[str, object]:
+    """logits [T, V] ~ 3 N(0, 1), target int32 [T] (one in eight rows has none: -1) and the upstream grads dlogp and
+    dentropy [T] fp32 (None without `entropy`) ~ N(0, 1)."""
+    dt = _torch_dtype(shape.dtype)
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    c: Dict[str, object] = {"logits": _normal(gen, (shape.T, shape.V), 3.0).to(dt)}
+    target = torch.randint(0, shape.V, (shape.T,), generator=gen, device=device)
+    none = torch.randint(0, 8, (shape.T,), generator=gen, device=device) == 0
+    c["target"] = target.masked_fill(none, -1).int()
+    if with_grad:
+        c["dlogp"] = _normal(gen, (shape.T,), 1.0)
+        c["dentropy"] = _normal(gen, (shape.T,), 1.0) if entropy else None
     return c
 
 

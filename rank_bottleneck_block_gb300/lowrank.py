@@ -36,6 +36,8 @@ EXPORTED = [
     "lr_block_saved_bytes", "lr_block_workspace_bytes", "lr_block_fwd", "lr_block_bwd", "lr_rot_turns", "lr_qk_fwd",
     "lr_qk_bwd_workspace_bytes", "lr_qk_bwd", "lr_grad_workspace_bytes", "lr_grad_norm", "lr_grad_clip",
     "lr_block_qk_saved_bytes", "lr_block_qk_workspace_bytes", "lr_block_qk_fwd", "lr_block_qk_bwd",
+    "lr_packed_attn_fwd_workspace_bytes", "lr_packed_attn_bwd_workspace_bytes", "lr_packed_attn_fwd",
+    "lr_packed_attn_bwd", "lr_logprob_workspace_bytes", "lr_logprob_fwd", "lr_logprob_bwd",
 ]
 
 
@@ -69,6 +71,11 @@ class lr_qk_shape(ctypes.Structure):
                 ("layout", ctypes.c_int), ("axes", ctypes.c_int), ("sec", ctypes.c_int * 4), ("seq", ctypes.c_int)]
 
 
+class lr_packed_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("nseq", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("dh", ctypes.c_int)]
+
+
 class lr_block_qk(ctypes.Structure):
     _fields_ = [("shape", lr_qk_shape), ("turns", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("gq", ctypes.c_void_p),
                 ("gk", ctypes.c_void_p)]
@@ -77,7 +84,7 @@ class lr_block_qk(ctypes.Structure):
 _lib = None
 
 _I, _F, _P, _SZ = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
-_LL, _QKS = ctypes.c_longlong, ctypes.POINTER(lr_qk_shape)
+_LL, _QKS, _PKS = ctypes.c_longlong, ctypes.POINTER(lr_qk_shape), ctypes.POINTER(lr_packed_shape)
 _SIGS = {
     "lr_mlp_saved_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "lr_mlp_fwd_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
@@ -130,6 +137,14 @@ _SIGS = {
     "lr_qk_bwd_workspace_bytes": (_SZ, [_I, _I, _QKS]),
     "lr_qk_bwd": (_I, [_I, _I, _QKS, _F, _P, _P, _P, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P,
                        _P, _P, _SZ, _P]),
+    "lr_packed_attn_fwd_workspace_bytes": (_SZ, [_PKS]),
+    "lr_packed_attn_bwd_workspace_bytes": (_SZ, [_PKS]),
+    "lr_packed_attn_fwd": (_I, [_I, _PKS, _F, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _P, _SZ, _P]),
+    "lr_packed_attn_bwd": (_I, [_I, _PKS, _F, _P, _P, _LL, _P, _LL, _P, _LL, _P, _LL, _P, _P, _LL, _P, _LL, _P, _LL, _P,
+                                _LL, _P, _SZ, _P]),
+    "lr_logprob_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "lr_logprob_fwd": (_I, [_I, _I, _I, _F, _I, _P, _LL, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "lr_logprob_bwd": (_I, [_I, _I, _I, _F, _P, _LL, _P, _P, _P, _P, _P, _P, _LL, _P]),
     "lr_grad_workspace_bytes": (_SZ, [_I]),
     "lr_grad_norm": (_I, [_I, _I, ctypes.POINTER(_P), ctypes.POINTER(_LL), _P, _P, _SZ, _P]),
     "lr_grad_clip": (_I, [_I, _I, ctypes.POINTER(_P), ctypes.POINTER(_LL), _F, ctypes.POINTER(_P), _P, _P, _SZ, _P]),
@@ -452,6 +467,40 @@ def lr_qk_bwd(dt, T, sh: lr_qk_shape, eps, turns, pos, gq, gk, q, ldq, k, ldk, d
     _check(lib().lr_qk_bwd(dt, T, ctypes.byref(sh), eps, _p(turns), _p(pos), _p(gq), _p(gk), _p(q), ldq, _p(k), ldk,
                            _p(dqo), lddqo, _p(dko), lddko, _p(dq), lddq, _p(dk), lddk, _p(dgq), _p(dgk), _p(ws),
                            _nbytes(ws), _stream(stream)))
+
+
+def lr_packed_attn_fwd_workspace_bytes(sh: lr_packed_shape) -> int:
+    return lib().lr_packed_attn_fwd_workspace_bytes(ctypes.byref(sh))
+
+
+def lr_packed_attn_bwd_workspace_bytes(sh: lr_packed_shape) -> int:
+    return lib().lr_packed_attn_bwd_workspace_bytes(ctypes.byref(sh))
+
+
+def lr_packed_attn_fwd(dt, sh: lr_packed_shape, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse, ws, stream=None):
+    _check(lib().lr_packed_attn_fwd(dt, ctypes.byref(sh), scale, _p(offs), _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(o), ldo,
+                                    _p(lse), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def lr_packed_attn_bwd(dt, sh: lr_packed_shape, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse, dout, lddout, dq, lddq,
+                       dk, lddk, dv, lddv, ws, stream=None):
+    _check(lib().lr_packed_attn_bwd(dt, ctypes.byref(sh), scale, _p(offs), _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(o), ldo,
+                                    _p(lse), _p(dout), lddout, _p(dq), lddq, _p(dk), lddk, _p(dv), lddv, _p(ws),
+                                    _nbytes(ws), _stream(stream)))
+
+
+def lr_logprob_workspace_bytes(dt, T, V, top) -> int:
+    return lib().lr_logprob_workspace_bytes(dt, T, V, top)
+
+
+def lr_logprob_fwd(dt, T, V, scale, top, logits, ld, target, logp, entropy, lse, top_ids, top_logp, ws, stream=None):
+    _check(lib().lr_logprob_fwd(dt, T, V, scale, top, _p(logits), ld, _p(target), _p(logp), _p(entropy), _p(lse),
+                                _p(top_ids), _p(top_logp), _p(ws), _nbytes(ws), _stream(stream)))
+
+
+def lr_logprob_bwd(dt, T, V, scale, logits, ld, target, lse, entropy, dlogp, dentropy, dlogits, lddlogits, stream=None):
+    _check(lib().lr_logprob_bwd(dt, T, V, scale, _p(logits), ld, _p(target), _p(lse), _p(entropy), _p(dlogp),
+                                _p(dentropy), _p(dlogits), lddlogits, _stream(stream)))
 
 
 def tensor_list(ts, numel=None):

@@ -1,6 +1,7 @@
 """Device-buffer plumbing around the C ABI for one MLP block, one projection
 group, one block stack, attention with the norm and rotation of its queries and
-keys, one transformer block, and the clipping of their gradients.
+keys, attention over packed sequences, one transformer block, log probabilities
+of tokens, and the clipping of gradients.
 
 torch only allocates device memory and supplies the stream; every computation
 is a call into liblowrank.so through the ctypes binding.
@@ -14,7 +15,7 @@ from typing import Dict, List, Optional, Sequence
 import torch
 
 from . import lowrank as L
-from .inputs import MlpShape, ProjShape, QkShape
+from .inputs import LogProbShape, MlpShape, PackedShape, ProjShape, QkShape
 
 _U8 = torch.uint8
 
@@ -487,7 +488,57 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     return (pb - pa) % sa < ra or (pa - pb) % sa < rb  # columns of one matrix
 
 
-class QkRotary:
+class _Assigned:
+    """Calls on tensors that are attributes: each may be replaced by another of its size and type, the shape is fixed.
+
+    _fits: what each tensor must be, (size or None, dtype); _WHOLE: those that must be contiguous; _FIXED: attributes
+    that stay; _OWN: inputs whose place an output may take.  _calls holds the last calls' arguments, converted, until a
+    tensor is replaced."""
+
+    _TENSORS: frozenset
+    _WHOLE: Sequence[str] = ()
+    _FIXED = ("s", "dt", "sh")
+    _OWN: Dict[str, str] = {}
+
+    def __setattr__(self, name, value):
+        if name in self._TENSORS:
+            if value is not None and self._fit(name, value).device != self._device:
+                raise ValueError(f"{name}: a tensor on {self._device} needed, not on {value.device}")
+            self.__dict__["_calls"] = {}
+        elif name in self._FIXED and name in self.__dict__:
+            raise AttributeError(f"{name} is fixed")
+        object.__setattr__(self, name, value)
+
+    def _fit(self, name, t):
+        size, dtype = self._fits[name]
+        if (size is not None and tuple(t.shape) != size) or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
+            raise ValueError(f"{name}: {'' if size is None else list(size)} {dtype} with contiguous rows needed, not "
+                             f"{list(t.shape)} {t.dtype} with strides {t.stride()}")
+        if name in self._WHOLE and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t
+
+    def _rows(self, *names):
+        """Each tensor and its row distance."""
+        for n in names:
+            t = getattr(self, n)
+            yield t
+            yield 0 if t is None else t.stride(0) if self.s.T > 1 else t.shape[1]
+
+    def _apart(self, names, outputs):
+        """Refuses outputs that overlap one another or an input of their call."""
+        tensors = {n: t for n in names if (t := getattr(self, n)) is not None}
+        for o, out in ((o, tensors[o]) for o in outputs if o in tensors):
+            for n, t in tensors.items():
+                if n == o or not _overlap(out, t):
+                    continue
+                if (n == self._OWN.get(o) and out.data_ptr() == t.data_ptr()
+                        and (self.s.T == 1 or out.stride(0) == t.stride(0))):
+                    continue
+                raise ValueError(f"{o} overlaps {n}")
+
+
+class QkRotary(_Assigned):
     """Norm and position rotation of queries and keys between their projections and attention.
 
     case: q [T, Hq*dh], k [T, Hk*dh] (rows may be further apart: columns of a packed matrix; None with 0
@@ -505,6 +556,8 @@ class QkRotary:
     _FORWARD = ("turns", "pos", "gq", "gk", "q", "k", "qo", "ko")
     _BACKWARD = ("turns", "pos", "gq", "gk", "q", "k", "dqo", "dko", "dq", "dk", "dgq", "dgk", "ws")
     _TENSORS = frozenset(_FORWARD + _BACKWARD)
+    _WHOLE = ("pos", "ws")
+    _OWN = {"qo": "q", "ko": "k", "dq": "dqo", "dk": "dko"}
 
     def __init__(self, shape: QkShape, case: Dict[str, object], device="cuda"):
         self.s, self.dt, self.sh = shape, _dt(shape.dtype), _qk_shape(shape)
@@ -535,46 +588,9 @@ class QkRotary:
         if back:
             self._convert_backward()
 
-    def __setattr__(self, name, value):
-        if name in self._TENSORS:
-            if value is not None and self._fit(name, value).device != self._device:
-                raise ValueError(f"{name}: a tensor on {self._device} needed, not on {value.device}")
-            self.__dict__.update(_fwd=None, _bwd=None)
-        elif name in ("s", "dt", "sh") and name in self.__dict__:
-            raise AttributeError(f"{name} is fixed")
-        object.__setattr__(self, name, value)
-
-    def _fit(self, name, t):
-        size, dtype = self._fits[name]
-        if (size is not None and tuple(t.shape) != size) or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
-            raise ValueError(f"{name}: {'' if size is None else list(size)} {dtype} with contiguous rows needed, not "
-                             f"{list(t.shape)} {t.dtype} with strides {t.stride()}")
-        if name in ("pos", "ws") and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t
-
-    def _rows(self, *names):
-        """Each tensor and its row distance."""
-        for n in names:
-            t = getattr(self, n)
-            yield t
-            yield 0 if t is None else t.stride(0) if self.s.T > 1 else t.shape[1]
-
     def _common(self):
         return (self.dt, self.s.T, L.ctypes.pointer(self.sh), self.s.eps, self.turns, self.pos, self.gq, self.gk,
                 *self._rows("q", "k"))
-
-    def _apart(self, names, outputs):
-        """Refuses outputs that overlap one another or an input of their call."""
-        tensors = {n: t for n in names if (t := getattr(self, n)) is not None}
-        own = {"qo": "q", "ko": "k", "dq": "dqo", "dk": "dko"}
-        for o, out in ((o, tensors[o]) for o in outputs if o in tensors):
-            for n, t in tensors.items():
-                if n == o or not _overlap(out, t):
-                    continue
-                if n == own.get(o) and out.data_ptr() == t.data_ptr() and (self.s.T == 1 or out.stride(0) == t.stride(0)):
-                    continue
-                raise ValueError(f"{o} overlaps {n}")
 
     def _prepare_forward(self):
         self._apart(self._FORWARD, ("qo", "ko"))
@@ -588,21 +604,168 @@ class QkRotary:
         return self._convert_backward()
 
     def _convert_forward(self):
-        self._fwd = L.Prepared("lr_qk_fwd", *self._common(), *self._rows("qo", "ko"))
-        return self._fwd
+        made = self._calls["fwd"] = L.Prepared("lr_qk_fwd", *self._common(), *self._rows("qo", "ko"))
+        return made
 
     def _convert_backward(self):
-        self._bwd = L.Prepared("lr_qk_bwd", *self._common(), *self._rows("dqo", "dko", "dq", "dk"), self.dgq, self.dgk,
-                               self.ws, L._nbytes(self.ws))
-        return self._bwd
+        made = self._calls["bwd"] = L.Prepared("lr_qk_bwd", *self._common(), *self._rows("dqo", "dko", "dq", "dk"),
+                                               self.dgq, self.dgk, self.ws, L._nbytes(self.ws))
+        return made
 
     def forward(self, stream=None):
-        (self._fwd or self._prepare_forward())(stream)
+        (self._calls.get("fwd") or self._prepare_forward())(stream)
         return self.qo, self.ko
 
     def backward(self, stream=None):
-        (self._bwd or self._prepare_backward())(stream)
+        (self._calls.get("bwd") or self._prepare_backward())(stream)
         return self.dq, self.dk
+
+    def step(self, stream=None):
+        self.forward(stream)
+        self.backward(stream)
+
+
+class PackedAttention(_Assigned):
+    """Causal attention over sequences of different lengths, one behind the other in the rows, with query heads that
+    share key heads; device resident, bf16.
+
+    case: q [T, Hq*dh], k, v [T, Hk*dh] (rows may be further apart: columns of a packed matrix), offs int32 [nseq + 1]
+    (sequence i is rows offs[i] to offs[i + 1] - 1) and, for backward(), dout [T, Hq*dh].  forward() writes o and lse
+    [T, Hq] fp32 (the log-sum-exp of each row's scores); backward() reads them and writes dq, dk, dv.  Rows of no
+    sequence are not written (the outputs' memory is not initialised).  Offsets are read on the device: where they are
+    not in order nothing is written, and lr_check_device_error says so.
+
+    The tensors are attributes, and may be replaced by others of their size and type on the same device, 16-byte
+    aligned: new offsets, or the o and lse of another forward.  The calls' arguments are converted once for each
+    assignment: a tensor that is given other memory by other means is to be assigned again.  Outputs overlap no other
+    tensor of their call.  The shape is fixed.
+    """
+
+    _FORWARD = ("offs", "q", "k", "v", "o", "lse", "ws")
+    _BACKWARD = ("offs", "q", "k", "v", "o", "lse", "dout", "dq", "dk", "dv", "ws_b")
+    _TENSORS = frozenset(_FORWARD + _BACKWARD)
+    _WHOLE = ("offs", "lse", "ws", "ws_b")
+    _FIXED = ("s", "dt", "sh", "scale")
+
+    def __init__(self, shape: PackedShape, case: Dict[str, object], device="cuda"):
+        s, td = shape, _tdt(shape.dtype)
+        self.s, self.dt = shape, _dt(shape.dtype)
+        self.sh = L.lr_packed_shape(s.T, s.nseq, s.Hq, s.Hk, s.dh)
+        self.scale = float(s.dh ** -0.5 if s.scale is None else s.scale)
+        q, k = (s.T, s.Hq * s.dh), (s.T, s.Hk * s.dh)
+        self._fits = {"offs": ((s.nseq + 1,), torch.int32), "lse": ((s.T, s.Hq), torch.float32), "ws": (None, _U8),
+                      "ws_b": (None, _U8), **{n: (q, td) for n in ("q", "o", "dout", "dq")},
+                      **{n: (k, td) for n in ("k", "v", "dk", "dv")}}
+        size = L.lr_packed_attn_fwd_workspace_bytes(self.sh)
+        if not size:
+            raise ValueError(L.lr_last_error())
+        ws = _buf(size, device)
+        self._device = ws.device
+        self.ws = ws
+        for n in ("offs", "q", "k", "v", "dout"):
+            t = case.get(n)
+            setattr(self, n, None if t is None else self._fit(n, t).to(device))
+        self.o = torch.empty(q, dtype=td, device=device)
+        self.lse = torch.empty(s.T, s.Hq, dtype=torch.float32, device=device)
+        back = self.dout is not None
+        self.dq = torch.empty(q, dtype=td, device=device) if back else None
+        self.dk, self.dv = (torch.empty(k, dtype=td, device=device) if back else None for _ in range(2))
+        self.ws_b = _buf(L.lr_packed_attn_bwd_workspace_bytes(self.sh), device) if back else None
+
+    def _common(self):
+        return (self.dt, L.ctypes.pointer(self.sh), self.scale, self.offs, *self._rows("q", "k", "v", "o"), self.lse)
+
+    def _prepare(self, name):
+        if name == "fwd":
+            self._apart(self._FORWARD, ("o", "lse", "ws"))
+            made = L.Prepared("lr_packed_attn_fwd", *self._common(), self.ws, L._nbytes(self.ws))
+        else:
+            if self.dout is None or self.ws_b is None:
+                raise ValueError("no upstream gradient dout was given")
+            self._apart(self._BACKWARD, ("dq", "dk", "dv", "ws_b"))
+            made = L.Prepared("lr_packed_attn_bwd", *self._common(), *self._rows("dout", "dq", "dk", "dv"), self.ws_b,
+                              L._nbytes(self.ws_b))
+        self._calls[name] = made
+        return made
+
+    def forward(self, stream=None):
+        (self._calls.get("fwd") or self._prepare("fwd"))(stream)
+        return self.o
+
+    def backward(self, stream=None):
+        (self._calls.get("bwd") or self._prepare("bwd"))(stream)
+        return self.dq, self.dk, self.dv
+
+    def step(self, stream=None):
+        self.forward(stream)
+        self.backward(stream)
+
+
+class TokenLogProbs(_Assigned):
+    """Log probabilities of given tokens under logits, the entropy of each row's distribution and its most probable
+    tokens; device resident.
+
+    case: logits [T, V] (rows may be further apart), target int32 [T] (outside 0 .. V-1: the row has none) and, for
+    backward(), dlogp [T] fp32 and dentropy [T] fp32 (None: the entropy has no gradient).  forward() writes logp,
+    entropy and lse [T] fp32 and, with shape.top, top_ids int32 and top_logp fp32 [T, top]; backward() reads lse and
+    entropy and writes dlogits.
+
+    The tensors are attributes, and may be replaced as those of PackedAttention; dlogits may be logits itself (a
+    backward in place).
+    """
+
+    _FORWARD = ("logits", "target", "logp", "entropy", "lse", "top_ids", "top_logp", "ws")
+    _BACKWARD = ("logits", "target", "lse", "entropy", "dlogp", "dentropy", "dlogits")
+    _TENSORS = frozenset(_FORWARD + _BACKWARD)
+    _WHOLE = ("target", "logp", "entropy", "lse", "top_ids", "top_logp", "dlogp", "dentropy", "ws")
+    _FIXED = ("s", "dt")
+    _OWN = {"dlogits": "logits"}
+
+    def __init__(self, shape: LogProbShape, case: Dict[str, object], device="cuda"):
+        s, f32 = shape, torch.float32
+        self.s, self.dt = shape, _dt(shape.dtype)
+        each, top = (s.T,), (s.T, s.top)
+        self._fits = {"logits": ((s.T, s.V), _tdt(s.dtype)), "dlogits": ((s.T, s.V), _tdt(s.dtype)),
+                      "target": (each, torch.int32), "top_ids": (top, torch.int32), "top_logp": (top, f32),
+                      "ws": (None, _U8), **{n: (each, f32) for n in ("logp", "entropy", "lse", "dlogp", "dentropy")}}
+        size = L.lr_logprob_workspace_bytes(self.dt, s.T, s.V, s.top)
+        if not size:
+            raise ValueError(L.lr_last_error())
+        ws = _buf(size, device)
+        self._device = ws.device
+        self.ws = ws
+        for n in ("logits", "target", "dlogp", "dentropy"):
+            t = case.get(n)
+            setattr(self, n, None if t is None else self._fit(n, t).to(device))
+        for n in ("logp", "entropy", "lse"):
+            setattr(self, n, torch.empty(each, dtype=f32, device=device))
+        self.top_ids = torch.empty(top, dtype=torch.int32, device=device) if s.top else None
+        self.top_logp = torch.empty(top, dtype=f32, device=device) if s.top else None
+        self.dlogits = torch.empty_like(self.logits, memory_format=torch.contiguous_format) if self.dlogp is not None else None
+
+    def _prepare(self, name):
+        s = self.s
+        if name == "fwd":
+            self._apart(self._FORWARD, ("logp", "entropy", "lse", "top_ids", "top_logp", "ws"))
+            made = L.Prepared("lr_logprob_fwd", self.dt, s.T, s.V, s.scale, s.top, *self._rows("logits"), self.target,
+                              self.logp, self.entropy, self.lse, self.top_ids, self.top_logp, self.ws,
+                              L._nbytes(self.ws))
+        else:
+            if self.dlogp is None or self.dlogits is None:
+                raise ValueError("no upstream gradient dlogp was given")
+            self._apart(self._BACKWARD, ("dlogits",))
+            made = L.Prepared("lr_logprob_bwd", self.dt, s.T, s.V, s.scale, *self._rows("logits"), self.target, self.lse,
+                              self.entropy, self.dlogp, self.dentropy, *self._rows("dlogits"))
+        self._calls[name] = made
+        return made
+
+    def forward(self, stream=None):
+        (self._calls.get("fwd") or self._prepare("fwd"))(stream)
+        return self.logp
+
+    def backward(self, stream=None):
+        (self._calls.get("bwd") or self._prepare("bwd"))(stream)
+        return self.dlogits
 
     def step(self, stream=None):
         self.forward(stream)
