@@ -2687,6 +2687,7 @@ lr_status lr_packed_attn_fwd(lr_dtype dt, const lr_packed_shape* sh, float scale
   LR_TRY(check_size(ws_bytes, packed_attn_fwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk), "ws"));
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c));
+  PdlOff serial;  // see lr_block_fwd
   const PackedArgs a = packed_args(*sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse);
   const double rows = 2.0 * sh->T * sh->dh;
   LaunchScope scope("packed_attn_fwd", c.st, 0, rows * (2.0 * sh->Hq + 2.0 * sh->Hk));
@@ -2709,6 +2710,7 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
   LR_TRY(check_size(ws_bytes, packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk), "ws"));
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c));
+  PdlOff serial;  // see lr_block_fwd
   PackedArgs a = packed_args(*sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse);
   a.dout = packed_rows(dout, lddout);
   a.dq = packed_rows(dq, lddq);

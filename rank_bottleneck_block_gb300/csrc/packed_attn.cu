@@ -1,5 +1,5 @@
-// lr_packed_attn_fwd / lr_packed_attn_bwd, the plain form: a warp per row and head (dk, dv: per row and key head), each
-// lane four channels, one key (or query) at a time with a running maximum and sum.
+// lr_packed_attn_bwd, the plain form: a warp per row and head (dk, dv: per row and key head), each lane four channels,
+// one key (or query) at a time.
 #include "packed_attn.cuh"
 
 #include <algorithm>
@@ -8,7 +8,6 @@ namespace lr {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -73,31 +72,6 @@ __device__ __forceinline__ bool sequence(const PackedArgs& a, int t, int& begin,
   return true;
 }
 
-__global__ void __launch_bounds__(32 * kWarps) fwd_kernel(PackedArgs a, const int* ok) {
-  const long long id = 1LL * blockIdx.x * kWarps + (threadIdx.x >> 5);
-  int b, e;
-  if (!*ok || id >= 1LL * a.T * a.Hq) return;
-  const int t = static_cast<int>(id / a.Hq), h = static_cast<int>(id % a.Hq), hk = h / (a.Hq / a.Hk);
-  if (!sequence(a, t, b, e)) return;
-  const float c = a.scale * kLog2e;
-  const Vec q = load(a.q, t, h, a.dh);
-  Vec o{};
-  float m = -INFINITY, l = 0.f;
-  for (int j = b; j <= t; ++j) {
-    const float s = c * dot(q, load(a.k, j, hk, a.dh));
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o.v[i] *= f;
-    axpy(o, p, load(a.v, j, hk, a.dh));
-    m = mn;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o.v[i] /= l;
-  store(a.o, t, h, a.dh, o);
-  if ((threadIdx.x & 31) == 0) a.lse[1LL * t * a.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
-}
-
 __global__ void __launch_bounds__(32 * kWarps) dq_kernel(PackedArgs a, const int* ok, float* D) {
   const long long id = 1LL * blockIdx.x * kWarps + (threadIdx.x >> 5);
   int b, e;
@@ -139,15 +113,7 @@ unsigned blocks(long long warps) { return static_cast<unsigned>((warps + kWarps 
 
 }  // namespace
 
-size_t packed_attn_fwd_ws_bytes(int, int, int, int) { return 256; }
 size_t packed_attn_bwd_ws_bytes(int T, int, int Hq, int) { return 256 + sizeof(float) * T * Hq; }
-
-cudaError_t launch_packed_attn_fwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st) {
-  int* ok = static_cast<int*>(ws);
-  check_kernel<<<1, 1024, 0, st>>>(a, ok, err);
-  fwd_kernel<<<blocks(1LL * a.T * a.Hq), 32 * kWarps, 0, st>>>(a, ok);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_packed_attn_bwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st) {
   int* ok = static_cast<int*>(ws);

@@ -1,0 +1,136 @@
+// Pieces that the packed-attention kernels share: how the sequences are cut into items, the list of them that a first
+// launch makes on the device, the ring through which a block's warps receive items, and loads of head rows.
+//
+// A row tile is 128 rows of the matrix instruction: tq = 128 / G tokens with the G query heads of one key head each
+// (token-major, rows tq G .. 127 unused).  Grouped heads then share the loads of their keys, a tile of few tokens is
+// still full, and its causal edge is as long as its tokens, not as its rows.
+//
+// The list holds blocks of one sequence, the ones with the most work first (a counting sort by work, in bins); an item
+// is a block with a key head.  Items are taken in groups of key heads whose operands stay in L2.
+#pragma once
+
+#include "attn_flash.cuh"
+#include "packed_attn.cuh"
+
+namespace lr {
+namespace packed {
+
+using namespace flash;
+
+constexpr int kItems = 4;  // slots of the item ring
+
+// What the first launch leaves in the workspace.
+struct Plan {
+  unsigned* next;  // items taken beyond the blocks' first ones
+  int* nblocks;
+  int4* blocks;    // first row, length of the sequence, place of the block's first token in it, 0
+  int* starts;     // [nseq + 1] blocks before each sequence
+};
+
+// A list of blocks of `tokens` tokens.
+inline long long plan_capacity(int T, int nseq, int tokens) {
+  const long long n = T / tokens + 1LL * nseq;
+  return n < T ? n : T;
+}
+size_t plan_layout(int T, int nseq, int tokens, void* base, Plan* plan);
+// work: +1: a block's work grows with its place (queries), -1: with what follows it (keys).
+cudaError_t launch_plan(const PackedArgs& a, int tokens, int work, const Plan& plan, unsigned* err, cudaStream_t st);
+
+// The block's t-th item: false past the end.
+struct Order {
+  int nblocks, heads, group;
+  __device__ __forceinline__ bool item(unsigned t, int& block, int& head) const {
+    const unsigned all = static_cast<unsigned>(nblocks) * heads;
+    if (t >= all) return false;
+    const unsigned per = static_cast<unsigned>(group) * nblocks, gi = t / per, r = t - gi * per;
+    const unsigned gh = min(group, heads - static_cast<int>(gi) * group);
+    block = static_cast<int>(r / gh);
+    head = static_cast<int>(gi * group + r % gh);
+    return true;
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Instruction descriptor for M = 128 and a run-time N (a multiple of 16).
+template <bool B_MN>
+__device__ __forceinline__ uint32_t idesc_n(int n) {
+  return idesc_m128<B_MN, 16>() - (2u << 17) + (static_cast<uint32_t>(n >> 3) << 17);
+}
+
+// Heads of T rows: boxes of 64 channels x `heads` heads x `tokens` rows, channels beyond dh read as 0.
+inline bool encode_heads(CUtensorMap* m, const PackedRows& x, int T, int H, int dh, int heads, int tokens) {
+  const long long dims[3] = {dh, H, T}, strides[2] = {dh, x.ld};
+  const int box[3] = {64, heads, tokens};
+  return umma::encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x.p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// r / G for r < 128, G <= 128: ceil(2^16 / G) is above 2^16 / G by less than 1, which 128 times stays below 2^16 / 128.
+__host__ __device__ __forceinline__ unsigned group_magic(int G) { return (65536u + G - 1) / G; }
+__device__ __forceinline__ int group_div(int r, unsigned magic) {
+  return static_cast<int>((static_cast<unsigned>(r) * magic) >> 16);
+}
+
+// Zeroes rows a .. b - 1 of a tile of `halves` 64-column halves (a whole warp).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int a, int b, int halves) {
+  const int lane = threadIdx.x & 31, per = 8 * halves;
+  for (int i = lane; i < (b - a) * per; i += 32) {
+    const int r = a + i / per, c = i % per;
+    sts128(smem_addr(tile) + (c >> 3) * kHalf + r * 128 + ((c & 7) << 4), 0u, 0u, 0u, 0u);
+  }
+}
+
+// Waits of a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
+                                          unsigned code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
+}
+
+// Waits, for a limited time, for a copy or MMA in flight before the block ends (error paths).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_test(bar, parity) && global_timer_ns() - t0 < umma::kWaitLimitNs) {
+  }
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int R>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+}  // namespace packed
+}  // namespace lr

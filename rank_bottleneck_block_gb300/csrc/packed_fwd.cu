@@ -1,0 +1,475 @@
+// Forward of causal attention over packed sequences (tcgen05).
+//
+// An item is two row tiles (2 x 128 rows: consecutive tokens of a sequence with the G heads of a key head, see
+// packed_device.cuh) against the keys up to their last token, 128 at a time.  Per tile t and key block j:
+//
+//   S_t = Q_t K_j^T            MMA, fp32 in TMEM
+//   P_t = 2^(c S_t - m)        softmax warps, one row a thread, c = scale log2(e); m is the row's running maximum of
+//                              c S, raised lazily; P (bf16) goes back over the first columns of S_t
+//   O_t += P_t V_j             MMA with A = P from TMEM, fp32 accumulator in TMEM
+//
+// with l = sum 2^(c S - m) in fp32 of the unrounded terms.  m is raised only when a block's maximum passes it by more
+// than 8 (powers of two), and O and l are scaled then: every formula holds for any m, and P stays below 2^8.  The two
+// tiles take turns: while the softmax works on one, the tensor cores work on the other (O_0 += P_0 V_j, then the next
+// S_0, then the same of tile 1), which is why an item has two.  A single tile per block left them waiting for each
+// softmax.
+//
+// Keys past a row's token are masked in S by selection, so nothing that K holds there matters; P is 0 there, and so
+// that 0 times V stays 0, rows of V past the end of the sequence are zeroed in shared memory before their product.
+// Products run over the keys that any row of a tile can see, in steps of 16.
+//
+// Warps: 0 TMA producer (Q_t per item; K_j, V_j into a ring of four 32 KB stages), 1 TMEM allocator and MMA issuer, 2
+// idle, 3 takes the items (the first is the block's own number, the others come from a counter), 4-7 and 8-11 softmax
+// and output of tile 0 and 1.  TMEM: S_t at columns 128 t, O_t at 256 + 128 t.
+// Every wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is freed).
+#include <algorithm>
+
+#include "packed_device.cuh"
+
+namespace lr {
+namespace packed {
+namespace fwd {
+
+constexpr int kStages = 4;
+constexpr int kStageOut = 4096;  // a warp's 32 rows x 64 columns of the output
+constexpr int kSmem = 1024 + 2 * kTile + kStages * kTile + 8 * kStageOut + 512;
+constexpr float kLazy = 8.f;
+// Registers a thread: the launch gives 168; the first four warps keep 80, the softmax warps take 208 (80 + 2 x 208 is
+// below 3 x 168).
+constexpr int kRegs = 168, kRegsFew = 80, kRegsMany = 208;
+static_assert(kRegsFew + 2 * kRegsMany <= 3 * kRegs, "register split");
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+struct Args {
+  PackedRows o;
+  float* lse;
+  float scale;
+  int Hq, dh, G, tq;  // tq: tokens of a row tile
+  unsigned magic;     // of G
+  const int* nblocks;
+  const int4* blocks;
+  unsigned* next;
+  int heads, group;   // key heads, and how many are worked on together
+  unsigned* err;
+};
+
+// What an item needs, from its ring slot.
+struct Item {
+  int row0, len, t0, head;  // the sequence's first row and length, the item's first token in it, the key head
+  __device__ __forceinline__ int tokens(int tile, int tq) const { return min(tq, len - t0 - tile * tq); }  // may be < 1
+  // Keys that some row of the tile sees, and the key blocks they are in.
+  __device__ __forceinline__ int keys(int tile, int tq) const {
+    const int n = tokens(tile, tq);
+    return n > 0 ? t0 + tile * tq + n : 0;
+  }
+  __device__ __forceinline__ int nblocks(int tile, int tq) const { return (keys(tile, tq) + kRows - 1) / kRows; }
+};
+
+// The softmax of one row over NC chunks of 32 keys of a block, and P written back.
+template <int NC>
+__device__ __forceinline__ void softmax_block(uint32_t ts, uint32_t to, int ocols, float c, int lim, bool masked,
+                                              bool valid, float& m, float& l, bool first) {
+  float x[32 * NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
+  tmem_ld_wait();
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < 32 * NC; ++i)
+      if (i > lim) x[i] = -INFINITY;
+  }
+  float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int i = 4; i < 32 * NC; i += 8) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], x[i + u]), i + u + 4 < 32 * NC ? x[i + u + 4] : x[i + u]);
+  }
+  const float bm = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const bool raise = valid && (first || bm > m + kLazy);
+  const float m_new = raise ? (first ? bm : fmaxf(m, bm)) : m;
+  const float alpha = raise && !first ? exp2f(m - m_new) : 1.f;
+  if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+    // S of this block complete implies that the product of the block before is: they are issued in that order.
+    for (int cc = 0; cc < ocols; cc += 32) {
+      float o[32];
+      tmem_ld32(to + cc, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 32; ++u) o[u] *= alpha;
+      tmem_st32(to + cc, o);
+    }
+  }
+  l *= alpha;
+  m = m_new;
+  const uint64_t cc = f2_pack(c, c), nm = f2_pack(-m, -m);
+  uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      float a, b;
+      f2_unpack(f2_fma(f2_pack(x[32 * i + 2 * u], x[32 * i + 2 * u + 1]), cc, nm), a, b);
+      a = ex2_ftz(a);
+      b = ex2_ftz(b);
+      ls[u & 3] = f2_add(ls[u & 3], f2_pack(a, b));
+      pk[u] = pack_bf16x2(a, b);
+    }
+    tmem_st16u(ts + 16 * i, pk);
+  }
+  float s[8];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) f2_unpack(ls[u], s[2 * u], s[2 * u + 1]);
+  l += ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+__global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_constant__ Maps maps, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                   // [2]
+  uint8_t* sKV = sQ + 2 * kTile;        // [kStages], K and V of a block by turns
+  uint8_t* sO = sKV + kStages * kTile;  // [8 warps]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sO + 8 * kStageOut);
+  uint64_t* q_full = bars;        // [2]
+  uint64_t* q_free = bars + 2;    // [2] the tile's last S has read Q
+  uint64_t* kv_full = bars + 4;   // [kStages]
+  uint64_t* kv_empty = bars + 8;  // [kStages]
+  uint64_t* s_full = bars + 12;   // [2]
+  uint64_t* p_full = bars + 14;   // [2]
+  uint64_t* o_last = bars + 16;   // [2] the tile's last product is complete
+  uint64_t* o_free = bars + 18;   // [2] its output has been read
+  uint64_t* drain = bars + 20;
+  uint64_t* item_full = bars + 22;           // [kItems]
+  uint64_t* item_empty = item_full + kItems;  // [kItems]
+  int4* sitem = reinterpret_cast<int4*>(item_empty + kItems);  // [kItems], 16-byte aligned
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sitem + kItems);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kReaders = 2 + 8;  // producer, MMA issuer, softmax warps
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_last[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kReaders);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int halves = a.dh > 64 ? 2 : 1, ksteps = (a.dh + 15) / 16, dh16 = ksteps * 16;
+  pdl_wait();
+
+  // Item `it` of this block; false when the wait gave up.  head < 0: there are no more.
+  auto next_item = [&](int it, Item& x) -> bool {
+    const int slot = it % kItems;
+    if (!mbar_wait(&item_full[slot], static_cast<uint32_t>((it / kItems) & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_MMA))
+      return false;
+    const volatile int* p = reinterpret_cast<const volatile int*>(&sitem[slot]);
+    x = Item{p[0], p[1], p[2], p[3]};
+    return true;
+  };
+
+  if (warp < 4) {
+    regs_down<kRegsFew>();
+    if (warp == 3 && lane == 0) {
+      // ------------------------------------------------ scheduler
+      const Order order{*a.nblocks, a.heads, a.group};
+      unsigned t = blockIdx.x;
+      for (int it = 0;; ++it) {
+        const int slot = it % kItems;
+        int block = 0, head = -1;
+        int4 v = make_int4(0, 0, 0, -1);
+        if (order.item(t, block, head)) {
+          v = a.blocks[block];
+          v.w = head;
+        }
+        if (!mbar_wait(&item_empty[slot], static_cast<uint32_t>((it / kItems) & 1) ^ 1u, abort_flag, a.err,
+                       DEV_ERR_TIMEOUT_PRODUCER))
+          break;
+        sitem[slot] = v;
+        mbar_arrive(&item_full[slot]);  // release: the readers see the item
+        if (head < 0) break;
+        t = gridDim.x + atomicAdd(a.next, 1u);
+      }
+    } else if (warp == 0 && lane == 0) {
+      // ------------------------------------------------ producer
+      bool ok = true;
+      int g = 0, q_issued[2] = {0, 0};
+      auto load_tile = [&](const CUtensorMap* map, int row, int head) {
+        const int st = g % kStages;
+        if (!mbar_wait(&kv_empty[st], static_cast<uint32_t>((g / kStages) & 1) ^ 1u, abort_flag, a.err,
+                       DEV_ERR_TIMEOUT_PRODUCER))
+          return false;
+        mbar_expect_tx(&kv_full[st], halves * kHalf);
+        for (int h = 0; h < halves; ++h)
+          tma_load_3d(sKV + st * kTile + h * kHalf, map, &kv_full[st], 64 * h, head, row);
+        ++g;
+        return true;
+      };
+      auto load_q = [&](int tile, const Item& x) {
+        if (!mbar_wait(&q_free[tile], static_cast<uint32_t>(q_issued[tile] & 1) ^ 1u, abort_flag, a.err,
+                       DEV_ERR_TIMEOUT_PRODUCER))
+          return false;
+        mbar_expect_tx(&q_full[tile], halves * a.G * a.tq * 128);
+        for (int h = 0; h < halves; ++h)
+          tma_load_3d(sQ + tile * kTile + h * kHalf, &maps.q, &q_full[tile], 64 * h, x.head * a.G,
+                      x.row0 + x.t0 + tile * a.tq);
+        ++q_issued[tile];
+        return true;
+      };
+      for (int it = 0; ok; ++it) {
+        Item x;
+        ok = next_item(it, x);
+        if (!ok) break;
+        mbar_arrive(&item_empty[it % kItems]);
+        if (x.head < 0) break;
+        const int n1 = x.nblocks(1, a.tq), nmax = max(x.nblocks(0, a.tq), n1);
+        ok = load_q(0, x);
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int row = x.row0 + j * kRows;
+          ok = load_tile(&maps.k, row, x.head);
+          if (ok && j == 0 && n1 > 0) ok = load_q(1, x);
+          ok = ok && load_tile(&maps.v, row, x.head);
+        }
+      }
+      if (!ok) {  // the copies in flight end before the block does
+        for (int k = max(0, g - kStages); k < g; ++k) drain_wait(&kv_full[k % kStages], (k / kStages) & 1);
+        for (int t = 0; t < 2; ++t)
+          if (q_issued[t]) drain_wait(&q_full[t], (q_issued[t] - 1) & 1);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issuer: the warp waits together, one lane issues
+      const uint32_t id_s = idesc_n<false>(kRows);  // S = Q K^T: both K-major
+      const uint32_t id_o = idesc_n<true>(dh16);    // O += P V: P from TMEM, V MN-major
+      const uint32_t q_base = smem_addr(sQ), kv_base = smem_addr(sKV);
+      const bool issuer = lane == 0;
+      bool ok = true;
+      int g = 0;
+      int s_of[2] = {0, 0}, items_of[2] = {0, 0};  // S and items of each tile so far
+      auto wait = [&](uint64_t* bar, int phase) {
+        return warp_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (issuer) commit1(bar);
+      };
+      for (int it = 0; ok; ++it) {
+        Item x;
+        ok = __all_sync(0xffffffffu, next_item(it, x));
+        if (!ok) break;
+        __syncwarp();
+        if (issuer) mbar_arrive(&item_empty[it % kItems]);
+        if (x.head < 0) break;
+        const int n[2] = {x.nblocks(0, a.tq), x.nblocks(1, a.tq)}, nmax = max(n[0], n[1]);
+        const int keys[2] = {x.keys(0, a.tq), x.keys(1, a.tq)};
+        const int left = x.len - (nmax - 1) * kRows;  // keys of the last block that the sequence has
+        auto issue_s = [&](int t, int j) {
+          const int k = g + 2 * j, st = k % kStages;
+          if ((j == 0 && !wait(&q_full[t], items_of[t])) || !wait(&kv_full[st], k / kStages)) return false;
+          tc_fence_after();
+          const uint32_t qt = q_base + t * kTile, kt = kv_base + st * kTile;
+          if (issuer)
+            for (int kk = 0; kk < ksteps; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+              mma1(tmem + t * kRows, sdesc(qt + off, 16, 1024), sdesc(kt + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
+            }
+          commit(&s_full[t]);
+          if (j + 1 == n[t]) commit(&q_free[t]);
+          return true;
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && n[t] > 0) ok = issue_s(t, 0);
+        if (ok) commit(&kv_empty[g % kStages]);
+        for (int j = 0; j < nmax && ok; ++j) {
+          const int v = g + 2 * j + 1, st = v % kStages;
+          uint8_t* vt = sKV + st * kTile;
+          bool clean = j + 1 < nmax || left >= kRows || left % 16 == 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || j >= n[t]) continue;
+            ok = wait(&kv_full[st], v / kStages);
+            if (ok && !clean) {  // rows past the sequence's end that the product's last step reads
+              zero_rows(vt, left, (left + 15) / 16 * 16, halves);
+              fence_async_smem();
+              __syncwarp();
+              clean = true;
+            }
+            ok = ok && wait(&p_full[t], s_of[t]++) && (j > 0 || wait(&o_free[t], items_of[t] + 1));
+            if (!ok) continue;
+            tc_fence_after();
+            const int steps = (min(kRows, keys[t] - j * kRows) + 15) / 16;
+            if (issuer)
+              for (int kk = 0; kk < steps; ++kk)
+                mma1_ta(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
+                        sdesc(smem_addr(vt) + kk * 2048, kHalf, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            if (j + 1 == n[t]) commit(&o_last[t]);
+            else ok = issue_s(t, j + 1);
+          }
+          if (!ok) break;
+          commit(&kv_empty[st]);
+          if (j + 1 < nmax) commit(&kv_empty[(v + 1) % kStages]);
+        }
+        g += 2 * nmax;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) items_of[t] += n[t] > 0 ? 1 : 0;
+      }
+      if (issuer) {
+        commit1(drain);  // every MMA issued here is complete once this flips
+        drain_wait(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_up<kRegsMany>();
+    // ------------------------------------------------ softmax and output
+    const int tile = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + tile * kRows, to = tmem + lanes + 2 * kRows + tile * kRows;
+    const float c = a.scale * kLog2e;
+    const int tok = group_div(row, a.magic);
+    const uint32_t stage = smem_addr(sO + (warp - 4) * kStageOut);
+    int s_of = 0, items_of = 0;
+    for (int it = 0;; ++it) {
+      Item x;
+      if (!__all_sync(0xffffffffu, next_item(it, x))) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[it % kItems]);
+      if (x.head < 0) break;
+      const int n = x.nblocks(tile, a.tq);
+      if (n == 0) continue;
+      const int first = x.t0 + tile * a.tq, keys = x.keys(tile, a.tq);  // the tile's first token, the keys it sees
+      const int place = first + tok;
+      const bool valid = tok < a.tq && place < x.len;
+      float m = 0.f, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        ok = warp_wait(&s_full[tile], static_cast<uint32_t>(s_of++ & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_EPILOGUE);
+        if (!ok) break;
+        tc_fence_after();
+        const int lim = place - j * kRows;             // the last key of the block that the row sees
+        const bool masked = first < j * kRows + kRows - 1;  // some row does not see all of them
+        if (keys - j * kRows > 64)
+          softmax_block<4>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0);
+        else
+          softmax_block<2>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tile]);
+      }
+      if (!ok) break;
+      if (!warp_wait(&o_last[tile], static_cast<uint32_t>(items_of++ & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_EPILOGUE))
+        break;
+      tc_fence_after();
+      // O / l, 64 columns at a time through the warp's staging rows, so that eight lanes write 128 bytes of a row.
+      const float inv = 1.f / l;
+      if (valid)
+        a.lse[1LL * (x.row0 + place) * a.Hq + x.head * a.G + (row - tok * a.G)] = (m + log2f(l)) * kLn2;
+      for (int h = 0; h < halves; ++h) {
+        float o[64];
+        tmem_ld32(to + 64 * h, o);
+        tmem_ld32(to + 64 * h + 32, o + 32);
+        tmem_ld_wait();
+        if (h + 1 == halves) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free[tile]);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          sts128(stage + lane * 128 + ((u ^ (lane & 7)) << 4), pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
+                 pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv), pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                 pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+        __syncwarp();
+        const int col = 64 * h + 8 * (lane & 7);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = 4 * u + (lane >> 3), full = quarter * 32 + r, t = group_div(full, a.magic);
+          uint4 w;
+          umma::lds128(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), w.x, w.y, w.z, w.w);
+          if (t < a.tq && first + t < x.len && col < a.dh)
+            *reinterpret_cast<uint4*>(a.o.p + (x.row0 + first + t) * a.o.ld +
+                                      1LL * (x.head * a.G + full - t * a.G) * a.dh + col) = w;
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace fwd
+}  // namespace packed
+
+size_t packed_attn_fwd_ws_bytes(int T, int nseq, int Hq, int Hk) {
+  return packed::plan_layout(T, nseq, 2 * (packed::kRows / (Hq / Hk)), nullptr, nullptr);
+}
+
+cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st) {
+  using namespace packed;
+  using namespace packed::fwd;
+  static int configured_mask = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 32) return cudaErrorInvalidDevice;
+  if (!(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
+    cudaError_t e = cudaFuncSetAttribute(packed_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    // The register split must fit what the kernel is launched with: the softmax warps would wait for it forever.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, packed_fwd_kernel);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kThreads < 128 * kRegsFew + 256 * kRegsMany) return cudaErrorInvalidConfiguration;
+    __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_RELEASE);
+  }
+  const int G = p.Hq / p.Hk, tq = kRows / G;
+  fwd::Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!encode_heads(&maps.q, p.q, p.T, p.Hq, p.dh, G, tq) || !encode_heads(&maps.k, p.k, p.T, p.Hk, p.dh, 1, kRows) ||
+      !encode_heads(&maps.v, p.v, p.T, p.Hk, p.dh, 1, kRows))
+    return cudaErrorInvalidValue;
+  Plan plan;
+  plan_layout(p.T, p.nseq, 2 * tq, ws, &plan);
+  cudaError_t e = launch_plan(p, 2 * tq, 1, plan, err, st);
+  if (e != cudaSuccess) return e;
+  fwd::Args a{p.o, p.lse, p.scale, p.Hq, p.dh, G, tq, group_magic(G), plan.nblocks, plan.blocks, plan.next, p.Hk,
+              heads_per_group(p.Hk, 4LL * p.T * p.dh), err};
+  const long long items = plan_capacity(p.T, p.nseq, 2 * tq) * p.Hk;
+  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
+  return launch_pdl(packed_fwd_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
+}
+
+}  // namespace lr
