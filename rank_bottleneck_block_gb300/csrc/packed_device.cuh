@@ -17,7 +17,7 @@ namespace packed {
 
 using namespace flash;
 
-constexpr int kItems = 4;  // slots of the item ring
+constexpr int kItems = 2;  // slots of the item ring
 
 // What the first launch leaves in the workspace.
 struct Plan {
@@ -64,6 +64,94 @@ __device__ __forceinline__ uint32_t idesc_n(int n) {
   return idesc_m128<B_MN, 16>() - (2u << 17) + (static_cast<uint32_t>(n >> 3) << 17);
 }
 
+// One thread issues a tile's matrix instructions and stands still until the tensor cores take each (64 cycles at
+// N = 128), so what it computes between them is lost to them: 17 instructions each made 86 cycles of it beside busy softmax
+// warps, a loop over the steps 130 to 200.  The forms below come out at 64: all counts of steps are unrolled, only
+// the low words of descriptors move, and the one thread is elected where it issues (not by its lane), which lets the
+// compiler keep the operands in the registers of the whole warp.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+  __device__ __forceinline__ Desc at(int bytes) const {  // addresses are below 2^18: no carry out of their field
+    Desc d = *this;
+    d.lo += static_cast<uint32_t>(bytes >> 4);
+    return d;
+  }
+};
+
+__device__ __forceinline__ void mma_ss1(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts1(uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// d = A B^T over `steps` (1 to 8) steps of 16 channels, both K-major tiles of 64-column halves.
+template <int STEPS>
+__device__ __forceinline__ void mma_ss_n(uint32_t d, Desc a, Desc b, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) {
+    const int off = (kk >> 2) * kHalf + (kk & 3) * 32;
+    mma_ss1(d, a.at(off), b.at(off), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, Desc b, uint32_t idesc, int steps) {
+  switch (steps) {
+    case 8: return mma_ss_n<8>(d, a, b, idesc);
+    case 7: return mma_ss_n<7>(d, a, b, idesc);
+    case 6: return mma_ss_n<6>(d, a, b, idesc);
+    case 5: return mma_ss_n<5>(d, a, b, idesc);
+    case 4: return mma_ss_n<4>(d, a, b, idesc);
+    case 3: return mma_ss_n<3>(d, a, b, idesc);
+    case 2: return mma_ss_n<2>(d, a, b, idesc);
+    default: return mma_ss_n<1>(d, a, b, idesc);
+  }
+}
+
+// d (+)= A B over `steps` (1 to 4) steps of 16 rows: A packed bf16 in TMEM, 8 columns a step, B an MN-major tile.
+template <int STEPS>
+__device__ __forceinline__ void mma_ts_n(uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t acc) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) mma_ts1(d, a + 8 * kk, b.at(2048 * kk), idesc, kk > 0 ? 1u : acc);
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t idesc, uint32_t acc, int steps) {
+  switch (steps) {
+    case 1: return mma_ts_n<1>(d, a, b, idesc, acc);
+    case 2: return mma_ts_n<2>(d, a, b, idesc, acc);
+    case 3: return mma_ts_n<3>(d, a, b, idesc, acc);
+    default: return mma_ts_n<4>(d, a, b, idesc, acc);
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Heads of T rows: boxes of 64 channels x `heads` heads x `tokens` rows, channels beyond dh read as 0.
 inline bool encode_heads(CUtensorMap* m, const PackedRows& x, int T, int H, int dh, int heads, int tokens) {
   const long long dims[3] = {dh, H, T}, strides[2] = {dh, x.ld};
@@ -86,11 +174,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int a, int b, int halve
   }
 }
 
-// Waits of a whole warp.
+// Waits of a whole warp (the same answer in every lane).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
                                           unsigned code) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, code));
 }
+
+// A value that every lane holds, known to the compiler as one of the whole warp: what follows from it is computed once
+// and is at hand for the matrix instructions, which take their operands from such registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // Waits, for a limited time, for a copy or MMA in flight before the block ends (error paths).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {

@@ -18,11 +18,14 @@
 // that 0 times V stays 0, rows of V past the end of the sequence are zeroed in shared memory before their product.
 // Products run over the keys that any row of a tile can see, in steps of 16.
 //
-// Warps: 0 TMA producer (Q_t per item; K_j, V_j into a ring of four 32 KB stages), 1 TMEM allocator and MMA issuer, 2
-// idle, 3 takes the items (the first is the block's own number, the others come from a counter), 4-7 and 8-11 softmax
-// and output of tile 0 and 1.  TMEM: S_t at columns 128 t, O_t at 256 + 128 t.
+// Warps: 0 takes the items (the first is the block's own number, the others come from a counter) and loads them by TMA
+// (Q_t per item; K_j, V_j into a ring of four 32 KB stages), 1 and 2 MMA issuers of tile 0 and 1 (1 also allocates TMEM),
+// 3 idle, 4-7 and 8-11 softmax and output of tile 0 and 1.  An issuer stands still until the tensor cores take its
+// instruction, so with a single issuer each of its waits (some 200 cycles, also when there is nothing to wait for) left
+// them idle: 2900 cycles for a tile's block where its instructions take 1024.  TMEM: S_t at columns 128 t, O_t at 256 + 128 t.
 // Every wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is freed).
 #include <algorithm>
+#include <type_traits>
 
 #include "packed_device.cuh"
 
@@ -34,9 +37,9 @@ constexpr int kStages = 4;
 constexpr int kStageOut = 4096;  // a warp's 32 rows x 64 columns of the output
 constexpr int kSmem = 1024 + 2 * kTile + kStages * kTile + 8 * kStageOut + 512;
 constexpr float kLazy = 8.f;
-// Registers a thread: the launch gives 168; the first four warps keep 80, the softmax warps take 208 (80 + 2 x 208 is
-// below 3 x 168).
-constexpr int kRegs = 168, kRegsFew = 80, kRegsMany = 208;
+// Registers a thread: the launch gives 168; the first four warps keep 88, the softmax warps take 208 (88 + 2 x 208 is
+// 3 x 168).
+constexpr int kRegs = 168, kRegsFew = 88, kRegsMany = 208;
 static_assert(kRegsFew + 2 * kRegsMany <= 3 * kRegs, "register split");
 
 struct Maps {
@@ -68,10 +71,19 @@ struct Item {
   __device__ __forceinline__ int nblocks(int tile, int tq) const { return (keys(tile, tq) + kRows - 1) / kRows; }
 };
 
-// The softmax of one row over NC chunks of 32 keys of a block, and P written back.
+// This warp's part of P (of 64 keys) is in TMEM.
+__device__ __forceinline__ void p_ready(uint64_t* bar) {
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The softmax of one row over NC chunks of 32 keys of a block, and P written back, 64 keys at a time: the product of the
+// first half runs while the second is computed.
 template <int NC>
 __device__ __forceinline__ void softmax_block(uint32_t ts, uint32_t to, int ocols, float c, int lim, bool masked,
-                                              bool valid, float& m, float& l, bool first) {
+                                              bool valid, float& m, float& l, bool first, uint64_t* p_full) {
   float x[32 * NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) tmem_ld32(ts + 32 * i, x + 32 * i);
@@ -81,12 +93,11 @@ __device__ __forceinline__ void softmax_block(uint32_t ts, uint32_t to, int ocol
     for (int i = 0; i < 32 * NC; ++i)
       if (i > lim) x[i] = -INFINITY;
   }
-  float mx[4] = {x[0], x[1], x[2], x[3]};
+  float mx[4];
 #pragma unroll
-  for (int i = 4; i < 32 * NC; i += 8) {
+  for (int u = 0; u < 4; ++u) mx[u] = max3(x[3 * u], x[3 * u + 1], x[3 * u + 2]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mx[u] = fmaxf(fmaxf(mx[u], x[i + u]), i + u + 4 < 32 * NC ? x[i + u + 4] : x[i + u]);
-  }
+  for (int i = 12; i + 1 < 32 * NC; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], x[i], x[i + 1]);
   const float bm = c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const bool raise = valid && (first || bm > m + kLazy);
   const float m_new = raise ? (first ? bm : fmaxf(m, bm)) : m;
@@ -119,6 +130,7 @@ __device__ __forceinline__ void softmax_block(uint32_t ts, uint32_t to, int ocol
       pk[u] = pack_bf16x2(a, b);
     }
     tmem_st16u(ts + 16 * i, pk);
+    if (i & 1) p_ready(p_full + (i >> 1));
   }
   float s[8];
 #pragma unroll
@@ -138,33 +150,36 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
   uint64_t* kv_full = bars + 4;   // [kStages]
   uint64_t* kv_empty = bars + 8;  // [kStages]
   uint64_t* s_full = bars + 12;   // [2]
-  uint64_t* p_full = bars + 14;   // [2]
-  uint64_t* o_last = bars + 16;   // [2] the tile's last product is complete
-  uint64_t* o_free = bars + 18;   // [2] its output has been read
-  uint64_t* drain = bars + 20;
-  uint64_t* item_full = bars + 22;           // [kItems]
+  uint64_t* p_full = bars + 14;   // [2][2] P of 64 keys
+  uint64_t* o_last = bars + 18;   // [2] the tile's last product is complete
+  uint64_t* o_free = bars + 20;   // [2] its output has been read
+  uint64_t* drain = bars + 22;    // [2]
+  uint64_t* turn = bars + 24;     // [2] the tile's issuer may issue
+  uint64_t* item_full = bars + 26;            // [kItems]
   uint64_t* item_empty = item_full + kItems;  // [kItems]
   int4* sitem = reinterpret_cast<int4*>(item_empty + kItems);  // [kItems], 16-byte aligned
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sitem + kItems);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kReaders = 2 + 8;  // producer, MMA issuer, softmax warps
+  constexpr int kReaders = 2 + 8;  // MMA issuers, softmax warps
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_free[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_last[i], 1);
       mbar_init(&o_free[i], 4);
+      mbar_init(&drain[i], 1);
+      mbar_init(&turn[i], 1);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
-    mbar_init(drain, 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&item_full[i], 1);
       mbar_init(&item_empty[i], kReaders);
@@ -197,28 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
 
   if (warp < 4) {
     regs_down<kRegsFew>();
-    if (warp == 3 && lane == 0) {
-      // ------------------------------------------------ scheduler
-      const Order order{*a.nblocks, a.heads, a.group};
-      unsigned t = blockIdx.x;
-      for (int it = 0;; ++it) {
-        const int slot = it % kItems;
-        int block = 0, head = -1;
-        int4 v = make_int4(0, 0, 0, -1);
-        if (order.item(t, block, head)) {
-          v = a.blocks[block];
-          v.w = head;
-        }
-        if (!mbar_wait(&item_empty[slot], static_cast<uint32_t>((it / kItems) & 1) ^ 1u, abort_flag, a.err,
-                       DEV_ERR_TIMEOUT_PRODUCER))
-          break;
-        sitem[slot] = v;
-        mbar_arrive(&item_full[slot]);  // release: the readers see the item
-        if (head < 0) break;
-        t = gridDim.x + atomicAdd(a.next, 1u);
-      }
-    } else if (warp == 0 && lane == 0) {
-      // ------------------------------------------------ producer
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------ scheduler and producer
       bool ok = true;
       int g = 0, q_issued[2] = {0, 0};
       auto load_tile = [&](const CUtensorMap* map, int row, int head) {
@@ -243,16 +238,30 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
         ++q_issued[tile];
         return true;
       };
+      const Order order{*a.nblocks, a.heads, a.group};
+      unsigned t = blockIdx.x;
       for (int it = 0; ok; ++it) {
-        Item x;
-        ok = next_item(it, x);
+        int block = 0, head = -1;
+        int4 v = make_int4(0, 0, 0, -1);
+        if (order.item(t, block, head)) {
+          v = a.blocks[block];
+          v.w = head;
+        }
+        const int slot = it % kItems;
+        ok = mbar_wait(&item_empty[slot], static_cast<uint32_t>((it / kItems) & 1) ^ 1u, abort_flag, a.err,
+                       DEV_ERR_TIMEOUT_PRODUCER);
         if (!ok) break;
-        mbar_arrive(&item_empty[it % kItems]);
-        if (x.head < 0) break;
+        sitem[slot] = v;
+        mbar_arrive(&item_full[slot]);  // release: the readers see the item
+        if (head < 0) break;
+        const Item x{v.x, v.y, v.z, v.w};
         const int n1 = x.nblocks(1, a.tq), nmax = max(x.nblocks(0, a.tq), n1);
         ok = load_q(0, x);
         for (int j = 0; j < nmax && ok; ++j) {
           const int row = x.row0 + j * kRows;
+          // The next item is taken as late as the loads that are left cover the counter's latency: taken earlier, it
+          // would bind the last items to blocks that are still busy.
+          if (j == max(0, nmax - 2)) t = gridDim.x + atomicAdd(a.next, 1u);
           ok = load_tile(&maps.k, row, x.head);
           if (ok && j == 0 && n1 > 0) ok = load_q(1, x);
           ok = ok && load_tile(&maps.v, row, x.head);
@@ -263,85 +272,92 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
         for (int t = 0; t < 2; ++t)
           if (q_issued[t]) drain_wait(&q_full[t], (q_issued[t] - 1) & 1);
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------ MMA issuer: the warp waits together, one lane issues
+    } else if (warp == 1 || warp == 2) {
+      // ------------------------------------------------ MMA issuers, one for each tile
+      const int t = uniform(warp - 1);
       const uint32_t id_s = idesc_n<false>(kRows);  // S = Q K^T: both K-major
       const uint32_t id_o = idesc_n<true>(dh16);    // O += P V: P from TMEM, V MN-major
-      const uint32_t q_base = smem_addr(sQ), kv_base = smem_addr(sKV);
-      const bool issuer = lane == 0;
+      const uint32_t ts = uniform(tmem) + t * kRows, to = ts + 2 * kRows;
+      const Desc qd = sdesc(smem_addr(sQ + t * kTile), 16, 1024), kd = sdesc(smem_addr(sKV), 16, 1024),
+                 vd = sdesc(smem_addr(sKV) + kTile, kHalf, 1024);
       bool ok = true;
-      int g = 0;
-      int s_of[2] = {0, 0}, items_of[2] = {0, 0};  // S and items of each tile so far
-      auto wait = [&](uint64_t* bar, int phase) {
-        return warp_wait(bar, static_cast<uint32_t>(phase & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
+      uint32_t b = 0;  // key blocks so far: K of block b in stage 2 (b & 1), V in the one behind it
+      uint32_t p_of = 0, p_second = 0, items = 0, turns = 0;  // the tile's blocks, second halves of P, items and turns
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return warp_wait(bar, phase & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
       };
-      auto commit = [&](uint64_t* bar) {
-        if (issuer) commit1(bar);
+      auto take_turn = [&] {
+        ++turns;
+        return wait(&turn[t], t ? turns + 1 : turns);
+      };
+      auto pass_turn = [&] {
+        if (elect()) mbar_arrive(&turn[1 - t]);
       };
       for (int it = 0; ok; ++it) {
         Item x;
         ok = __all_sync(0xffffffffu, next_item(it, x));
         if (!ok) break;
-        __syncwarp();
-        if (issuer) mbar_arrive(&item_empty[it % kItems]);
+        x = Item{uniform(x.row0), uniform(x.len), uniform(x.t0), uniform(x.head)};
+        if (elect()) mbar_arrive(&item_empty[it % kItems]);
         if (x.head < 0) break;
-        const int n[2] = {x.nblocks(0, a.tq), x.nblocks(1, a.tq)}, nmax = max(n[0], n[1]);
-        const int keys[2] = {x.keys(0, a.tq), x.keys(1, a.tq)};
-        const int left = x.len - (nmax - 1) * kRows;  // keys of the last block that the sequence has
-        auto issue_s = [&](int t, int j) {
-          const int k = g + 2 * j, st = k % kStages;
-          if ((j == 0 && !wait(&q_full[t], items_of[t])) || !wait(&kv_full[st], k / kStages)) return false;
-          tc_fence_after();
-          const uint32_t qt = q_base + t * kTile, kt = kv_base + st * kTile;
-          if (issuer)
-            for (int kk = 0; kk < ksteps; ++kk) {
-              const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-              mma1(tmem + t * kRows, sdesc(qt + off, 16, 1024), sdesc(kt + off, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-            }
-          commit(&s_full[t]);
-          if (j + 1 == n[t]) commit(&q_free[t]);
-          return true;
-        };
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && n[t] > 0) ok = issue_s(t, 0);
-        if (ok) commit(&kv_empty[g % kStages]);
-        for (int j = 0; j < nmax && ok; ++j) {
-          const int v = g + 2 * j + 1, st = v % kStages;
-          uint8_t* vt = sKV + st * kTile;
-          bool clean = j + 1 < nmax || left >= kRows || left % 16 == 0;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || j >= n[t]) continue;
-            ok = wait(&kv_full[st], v / kStages);
-            if (ok && !clean) {  // rows past the sequence's end that the product's last step reads
-              zero_rows(vt, left, (left + 15) / 16 * 16, halves);
-              fence_async_smem();
-              __syncwarp();
-              clean = true;
-            }
-            ok = ok && wait(&p_full[t], s_of[t]++) && (j > 0 || wait(&o_free[t], items_of[t] + 1));
-            if (!ok) continue;
-            tc_fence_after();
-            const int steps = (min(kRows, keys[t] - j * kRows) + 15) / 16;
-            if (issuer)
-              for (int kk = 0; kk < steps; ++kk)
-                mma1_ta(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
-                        sdesc(smem_addr(vt) + kk * 2048, kHalf, 1024), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 == n[t]) commit(&o_last[t]);
-            else ok = issue_s(t, j + 1);
+        const int n = x.nblocks(t, a.tq), nmax = max(x.nblocks(0, a.tq), x.nblocks(1, a.tq));
+        const int last = x.keys(t, a.tq) - (n - 1) * kRows;  // keys of the tile's last block that some row sees
+        auto issue_s = [&](int j, uint32_t blk) {  // S of block j, which is the blk-th of all; the turn passes
+          if (elect()) {
+            mma_ss(ts, qd, kd.at(2 * kTile * (blk & 1)), id_s, ksteps);
+            mbar_arrive(&turn[1 - t]);
+            commit1(&s_full[t]);
+            commit1(&kv_empty[2 * (blk & 1)]);
+            if (j + 1 == n) commit1(&q_free[t]);
           }
+        };
+        ok = (n == 0 || (wait(&q_full[t], items) && wait(&kv_full[2 * (b & 1)], b >> 1))) && take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        if (n > 0) issue_s(0, b);
+        else pass_turn();
+        for (int j = 0; j < nmax && ok; ++j, ++b) {
+          uint64_t* v_full = &kv_full[2 * (b & 1) + 1];
+          uint64_t* v_empty = &kv_empty[2 * (b & 1) + 1];
+          if (j >= n) {  // the other tile's block: this one's part of its release, once it is there
+            ok = wait(&kv_full[2 * (b & 1)], b >> 1) && wait(v_full, b >> 1) && take_turn();
+            if (ok && elect()) {
+              mbar_arrive(&kv_empty[2 * (b & 1)]);
+              mbar_arrive(v_empty);
+            }
+            pass_turn();
+            continue;
+          }
+          ok = wait(v_full, b >> 1) && (j + 1 == n || wait(&kv_full[2 * ((b + 1) & 1)], (b + 1) >> 1));
+          const int steps = j + 1 < n ? 8 : (last + 15) / 16, left = x.len - j * kRows;
+          if (ok && left < 16 * steps) {  // rows past the sequence's end that the product's last step reads
+            zero_rows(sKV + (2 * (b & 1) + 1) * kTile, left, 16 * steps, halves);  // (both issuers: the same zeroes)
+            fence_async_smem();
+            __syncwarp();
+          }
+          ok = ok && (j > 0 || wait(&o_free[t], items + 1)) && wait(&p_full[2 * t], p_of++) && take_turn();
           if (!ok) break;
-          commit(&kv_empty[st]);
-          if (j + 1 < nmax) commit(&kv_empty[(v + 1) % kStages]);
+          tc_fence_after();
+          const Desc v = vd.at(2 * kTile * (b & 1));
+          if (elect()) mma_ts(to, ts, v, id_o, j > 0 ? 1u : 0u, min(4, steps));
+          if (steps > 4) {
+            ok = wait(&p_full[2 * t + 1], p_second++);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect()) mma_ts(to, ts + 32, v.at(4 * 2048), id_o, 1u, steps - 4);
+          }
+          if (elect()) {
+            commit1(v_empty);
+            if (j + 1 == n) commit1(&o_last[t]);
+          }
+          if (j + 1 < n) issue_s(j + 1, b + 1);
+          else pass_turn();
         }
-        g += 2 * nmax;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) items_of[t] += n[t] > 0 ? 1 : 0;
+        if (n > 0) ++items;
       }
-      if (issuer) {
-        commit1(drain);  // every MMA issued here is complete once this flips
-        drain_wait(drain, 0);
+      if (elect()) {
+        commit1(&drain[t]);  // every MMA issued here is complete once this flips
+        drain_wait(&drain[t], 0);
       }
       __syncwarp();
     }
@@ -376,13 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
         const int lim = place - j * kRows;             // the last key of the block that the row sees
         const bool masked = first < j * kRows + kRows - 1;  // some row does not see all of them
         if (keys - j * kRows > 64)
-          softmax_block<4>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0);
+          softmax_block<4>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0, &p_full[2 * tile]);
         else
-          softmax_block<2>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tile]);
+          softmax_block<2>(ts, to, dh16, c, lim, masked, valid, m, l, j == 0, &p_full[2 * tile]);
       }
       if (!ok) break;
       if (!warp_wait(&o_last[tile], static_cast<uint32_t>(items_of++ & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_EPILOGUE))
