@@ -1,0 +1,460 @@
+// dK and dV of causal attention over packed sequences (tcgen05).
+//
+// An item is a block of 128 keys of one key head against the row tiles (128 rows: tokens with the G heads of the key
+// head, see packed_device.cuh) from the first that holds one of its tokens to the sequence's last.  With the keys on the
+// MMA rows, per row tile i:
+//
+//   S^T = K Q_i^T, dP^T = V dO_i^T      MMA, fp32 in TMEM
+//   P^T = 2^(c S^T - lse log2 e)        element-wise warps, two threads a key; bf16 back over the columns of S^T
+//   dS^T = P^T (dP^T - D)               the same over those of dP^T
+//   dV += P^T dO_i, dK += dS^T Q_i      MMA with A from TMEM; dK takes the scale at the end
+//
+// The heads of a group add up in the same accumulators, in a fixed order.  TMEM is full (S^T, dP^T, dV and dK, 128
+// columns each), so S^T and dP^T have one buffer; what keeps the tensor cores at work is that they belong to two chains:
+// one issuer takes dV of tile i and then S^T of tile i + 1, the other dK of tile i and then dP^T of tile i + 1, by
+// turns, and the element-wise warps compute P while the second has its turn and dS while the first has.
+//
+// Rows past the end of the sequence get P = dS = 0 by selection, and rows of dO and Q there are zeroed in shared memory
+// before their products.  Rows of a tile that no token has (128 is no multiple of G) stay zero from the start.
+//
+// Warps: 0 takes the items and loads them by TMA (K, V per item; Q_i, dO_i into a ring of two stages), 1 issuer of S^T
+// and dV, which also allocates TMEM, 2 issuer of dP^T and dK, 3 loads lse and D of each tile, 4-11 element-wise and output
+// (warp group h takes rows 64 h .. 64 h + 63 of a tile and columns 64 h .. of dK and dV).  TMEM: S^T at column 0, dP^T at
+// 128, dV at 256, dK at 384.  Every wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is
+// freed).
+#include <algorithm>
+
+#include "packed_device.cuh"
+
+namespace lr {
+namespace packed {
+namespace dkv {
+
+constexpr int kStages = 2;
+constexpr int kStageOut = 2048;  // a warp's 32 rows x 32 columns of dK or dV
+constexpr int kSmem = 1024 + (2 + 2 * kStages) * kTile + 8 * kStageOut + kStages * 2 * kRows * 4 + 512;
+static_assert(kSmem <= umma::kMaxSmem, "shared memory");
+
+struct Maps {
+  CUtensorMap q, dout, k, v;
+};
+
+struct Args {
+  PackedRows dk, dv;
+  const float *lse, *D;
+  float scale;
+  int Hq, dh, G, tq;
+  unsigned magic;
+  Taken taken;
+  unsigned* err;
+};
+
+// The row tiles of an item's key block.
+struct Tiles {
+  int first, n;
+  __device__ __forceinline__ Tiles(const Item& x, int tq) : first(x.t0 / tq), n((x.len + tq - 1) / tq - first) {}
+};
+
+__global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_constant__ Maps maps, const Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + kTile;
+  uint8_t* sQ = sV + kTile;              // [kStages]
+  uint8_t* sdO = sQ + kStages * kTile;   // [kStages]
+  uint8_t* sOut = sdO + kStages * kTile;  // [8 warps]
+  float* sL = reinterpret_cast<float*>(sOut + 8 * kStageOut);  // [kStages][128] -lse log2 e
+  float* sD = sL + kStages * kRows;                            // [kStages][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + kStages * kRows);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_free = bars + 1;    // the item's last S^T and last dP^T have read K and V
+  uint64_t* qd_full = bars + 2;    // [kStages]
+  uint64_t* qd_empty = bars + 4;   // [kStages] dV and dK of the tile are complete
+  uint64_t* st_full = bars + 6;    // [kStages] lse and D
+  uint64_t* st_empty = bars + 8;   // [kStages]
+  uint64_t* s_full = bars + 10;
+  uint64_t* dp_full = bars + 11;
+  uint64_t* p_full = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* acc_full = bars + 14;  // the item's last dV and dK are complete
+  uint64_t* acc_free = bars + 15;  // they have been read
+  uint64_t* turn = bars + 16;      // [2]
+  uint64_t* drain = bars + 18;     // [2]
+  uint64_t* item_full = bars + 20;            // [kItems]
+  uint64_t* item_empty = item_full + kItems;  // [kItems]
+  int4* sitem = reinterpret_cast<int4*>(item_empty + kItems);  // [kItems], 16-byte aligned
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sitem + kItems);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kReaders = 3 + 8;  // issuers, loader of lse and D, element-wise warps
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_free, 2);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&qd_full[i], 1);
+      mbar_init(&qd_empty[i], 2);
+      mbar_init(&st_full[i], 1);
+      mbar_init(&st_empty[i], 8);
+      mbar_init(&turn[i], 1);
+      mbar_init(&drain[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(acc_full, 2);
+    mbar_init(acc_free, 8);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], kReaders);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (a.G * a.tq < kRows)  // rows that the loads never write
+    for (int i = warp; i < 2 * kStages; i += kThreads / 32) zero_rows(sQ + i * kTile, a.G * a.tq, kRows, 2);
+  fence_async_smem();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int halves = a.dh > 64 ? 2 : 1, ksteps = (a.dh + 15) / 16, dh16 = ksteps * 16;
+  pdl_wait();
+
+  // Item `it` of this block; false when the wait gave up.  head < 0: there are no more.
+  auto next_item = [&](int it, Item& x) -> bool {
+    const int slot = it % kItems;
+    if (!mbar_wait(&item_full[slot], static_cast<uint32_t>((it / kItems) & 1), abort_flag, a.err, DEV_ERR_TIMEOUT_MMA))
+      return false;
+    const volatile int* p = reinterpret_cast<const volatile int*>(&sitem[slot]);
+    x = Item{p[0], p[1], p[2], p[3]};
+    return true;
+  };
+
+  if (warp < 4) {
+    regs_down<kRegsFew>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------ scheduler and producer
+      bool ok = true;
+      int g = 0, issued = 0;  // row tiles, and items
+      auto wait = [&](uint64_t* bar, int phase) {
+        return mbar_wait(bar, static_cast<uint32_t>(phase & 1) ^ 1u, abort_flag, a.err, DEV_ERR_TIMEOUT_PRODUCER);
+      };
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
+        for (int h = 0; h < halves; ++h) tma_load_3d(dst + h * kHalf, map, bar, 64 * h, head, row);
+      };
+      unsigned t = blockIdx.x;
+      for (int it = 0; ok; ++it) {
+        const int4 v = a.taken.item(t);
+        const int slot = it % kItems;
+        ok = wait(&item_empty[slot], it / kItems);
+        if (!ok) break;
+        sitem[slot] = v;
+        mbar_arrive(&item_full[slot]);  // release: the readers see the item
+        if (v.w < 0) break;
+        const Item x{v.x, v.y, v.z, v.w};
+        const Tiles tiles(x, a.tq);
+        ok = wait(kv_free, issued);
+        if (!ok) break;
+        mbar_expect_tx(kv_full, 2 * halves * kHalf);
+        load(sK, &maps.k, kv_full, x.head, x.row0 + x.t0);
+        load(sV, &maps.v, kv_full, x.head, x.row0 + x.t0);
+        ++issued;
+        for (int i = 0; i < tiles.n && ok; ++i, ++g) {
+          if (i == max(0, tiles.n - 2)) t = gridDim.x + atomicAdd(a.taken.next, 1u);  // late: see the forward
+          const int st = g % kStages;
+          ok = wait(&qd_empty[st], g / kStages);
+          if (!ok) break;
+          const int row = x.row0 + (tiles.first + i) * a.tq;
+          mbar_expect_tx(&qd_full[st], 2 * halves * a.G * a.tq * 128);
+          load(sQ + st * kTile, &maps.q, &qd_full[st], x.head * a.G, row);
+          load(sdO + st * kTile, &maps.dout, &qd_full[st], x.head * a.G, row);
+        }
+      }
+      if (!ok) {  // the copies in flight end before the block does
+        for (int k = max(0, g - kStages); k < g; ++k) drain_wait(&qd_full[k % kStages], (k / kStages) & 1);
+        if (issued) drain_wait(kv_full, (issued - 1) & 1);
+      }
+    } else if (warp == 1 || warp == 2) {
+      // ------------------------------------------------ issuers: 0 of S^T and dV, 1 of dP^T and dK
+      const int w = uniform(warp - 1);
+      const uint32_t id_s = idesc_n<false>(kRows);  // K Q^T, V dO^T: all K-major
+      const uint32_t id_g = idesc_n<true>(dh16);    // P^T dO, dS^T Q: A from TMEM, B MN-major
+      const uint32_t ts = uniform(tmem) + w * kRows, tg = ts + 2 * kRows;
+      uint8_t* sS = w ? sdO : sQ;  // B of the scores
+      uint8_t* sG = w ? sQ : sdO;  // B of the gradient
+      const Desc ad = sdesc(smem_addr(w ? sV : sK), 16, 1024), sd = sdesc(smem_addr(sS), 16, 1024),
+                 gd = sdesc(smem_addr(sG), kHalf, 1024);
+      uint64_t* score_full = w ? dp_full : s_full;
+      uint64_t* mine_full = w ? ds_full : p_full;
+      bool ok = true;
+      uint32_t g = 0, items = 0, turns = 0;
+      auto wait = [&](uint64_t* bar, uint32_t phase) {
+        return warp_wait(bar, phase & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
+      };
+      auto take_turn = [&] {
+        ++turns;
+        return wait(&turn[w], w ? turns + 1 : turns);
+      };
+      for (int it = 0; ok; ++it, ++items) {
+        Item x;
+        ok = __all_sync(0xffffffffu, next_item(it, x));
+        if (!ok) break;
+        x = Item{uniform(x.row0), uniform(x.len), uniform(x.t0), uniform(x.head)};
+        if (elect()) mbar_arrive(&item_empty[it % kItems]);
+        if (x.head < 0) break;
+        const Tiles tiles(x, a.tq);
+        const int left = min(a.tq, x.len - (tiles.first + tiles.n - 1) * a.tq) * a.G;  // rows of the last tile
+        auto issue_score = [&](int i) {  // of the item's tile i; the turn passes
+          if (elect()) {
+            mma_ss(ts, ad, sd.at((g + i) % kStages * kTile), id_s, ksteps);
+            mbar_arrive(&turn[1 - w]);
+            commit1(score_full);
+            if (i + 1 == tiles.n) commit1(kv_free);
+          }
+        };
+        ok = wait(kv_full, items) && wait(&qd_full[g % kStages], g / kStages) && take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        issue_score(0);
+        for (int i = 0; i < tiles.n && ok; ++i) {
+          const uint32_t b = g + i, st = b % kStages;
+          const bool last = i + 1 == tiles.n;
+          const int rows = last ? left : a.tq * a.G, steps = (rows + 15) / 16;
+          if (last && left < 16 * steps && left < a.tq * a.G) {  // rows past the sequence's end that the last step reads
+            zero_rows(sG + st * kTile, left, 16 * steps, halves);
+            fence_async_smem();
+            __syncwarp();
+          }
+          ok = (last || wait(&qd_full[(b + 1) % kStages], (b + 1) / kStages)) && (i > 0 || wait(acc_free, items + 1)) &&
+               wait(mine_full, b) && take_turn();
+          if (!ok) break;
+          tc_fence_after();
+          if (elect()) {
+            mma_ts(tg, ts, gd.at(st * kTile), id_g, i > 0 ? 1u : 0u, min(4, steps));
+            if (steps > 4) mma_ts(tg, ts + 64, gd.at(st * kTile + 4 * 2048), id_g, 1u, steps - 4);
+            commit1(&qd_empty[st]);
+            if (last) {
+              commit1(acc_full);
+              mbar_arrive(&turn[1 - w]);
+            }
+          }
+          if (!last) issue_score(i + 1);
+        }
+        g += tiles.n;
+      }
+      if (elect()) {
+        commit1(&drain[w]);  // every MMA issued here is complete once this flips
+        drain_wait(&drain[w], 0);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------------------ lse and D of the tiles' rows
+      bool ok = true;
+      uint32_t g = 0;
+      for (int it = 0; ok; ++it) {
+        Item x;
+        ok = __all_sync(0xffffffffu, next_item(it, x));
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[it % kItems]);
+        if (x.head < 0) break;
+        const Tiles tiles(x, a.tq);
+        for (int i = 0; i < tiles.n && ok; ++i, ++g) {
+          const int st = g % kStages, t0 = (tiles.first + i) * a.tq;
+          float l[4], d[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = lane + 32 * u, tok = group_div(r, a.magic), place = t0 + tok;
+            l[u] = -INFINITY;
+            d[u] = 0.f;
+            if (tok < a.tq && place < x.len) {
+              const long long at = 1LL * (x.row0 + place) * a.Hq + x.head * a.G + (r - tok * a.G);
+              l[u] = -a.lse[at] * kLog2e;
+              d[u] = a.D[at];
+            }
+          }
+          ok = warp_wait(&st_empty[st], ((g / kStages) & 1) ^ 1u, abort_flag, a.err, DEV_ERR_TIMEOUT_PRODUCER);
+          if (!ok) break;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            sL[st * kRows + lane + 32 * u] = l[u];
+            sD[st * kRows + lane + 32 * u] = d[u];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&st_full[st]);
+        }
+      }
+    }
+  } else {
+    regs_up<kRegsMany>();
+    // ------------------------------------------------ element-wise warps and output
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // the key within the block
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kRows, tv = ts + 2 * kRows;
+    const float c = a.scale * kLog2e;
+    const uint32_t stage = smem_addr(sOut + (warp - 4) * kStageOut);
+    uint32_t g = 0, items = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return warp_wait(bar, phase & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_EPILOGUE);
+    };
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    for (int it = 0; ok; ++it, ++items) {
+      Item x;
+      ok = __all_sync(0xffffffffu, next_item(it, x));
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[it % kItems]);
+      if (x.head < 0) break;
+      const Tiles tiles(x, a.tq);
+      for (int i = 0; i < tiles.n; ++i, ++g) {
+        const int st = g % kStages, t0 = (tiles.first + i) * a.tq;
+        const int rows = min(a.tq, x.len - t0) * a.G - 64 * half;  // of the tile, from this thread's first
+        const bool any = rows > 0;
+        // The rows that see this key begin at G (key - t0); a tile before the block's last key, or past the end of the
+        // sequence, is masked.
+        const int from = (x.t0 + row - t0) * a.G - 64 * half;
+        const bool masked = t0 < x.t0 + kRows - 1 || x.len - t0 < a.tq;
+        const float* L = sL + st * kRows + 64 * half;
+        const float* D = sD + st * kRows + 64 * half;
+        ok = wait(&st_full[st], g / kStages) && wait(s_full, g);
+        if (!ok) break;
+        float p[64];
+        if (any) {
+          tc_fence_after();
+          tmem_ld32(ts, p);
+          tmem_ld32(ts + 32, p + 32);
+          tmem_ld_wait();
+          uint32_t w[32];
+          const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+          for (int u = 0; u < 64; u += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(L + u);
+            f2_unpack(f2_fma(f2_pack(p[u], p[u + 1]), c2, f2_pack(l4.x, l4.y)), p[u], p[u + 1]);
+            f2_unpack(f2_fma(f2_pack(p[u + 2], p[u + 3]), c2, f2_pack(l4.z, l4.w)), p[u + 2], p[u + 3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[u + e] = ex2_ftz(p[u + e]);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (u + e < from || u + e >= rows) p[u + e] = 0.f;
+            }
+            w[u >> 1] = pack_bf16x2(p[u], p[u + 1]);
+            w[(u >> 1) + 1] = pack_bf16x2(p[u + 2], p[u + 3]);
+          }
+          tmem_st32u(ts, w);
+          tmem_st_wait();
+        }
+        arrive(p_full);
+        ok = wait(dp_full, g);
+        if (!ok) break;
+        if (any) {
+          tc_fence_after();
+          float d[64];
+          tmem_ld32(tp, d);
+          tmem_ld32(tp + 32, d + 32);
+          tmem_ld_wait();
+          uint32_t w[32];
+#pragma unroll
+          for (int u = 0; u < 64; u += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(D + u);
+            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+            float e4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4[e] = p[u + e] * (d[u + e] - dv[e]);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (u + e < from || u + e >= rows) e4[e] = 0.f;
+            }
+            w[u >> 1] = pack_bf16x2(e4[0], e4[1]);
+            w[(u >> 1) + 1] = pack_bf16x2(e4[2], e4[3]);
+          }
+          tmem_st32u(tp, w);
+          tmem_st_wait();
+        }
+        arrive(ds_full);
+        if (lane == 0) mbar_arrive(&st_empty[st]);
+      }
+      if (!ok) break;
+      ok = wait(acc_full, items);
+      if (!ok) break;
+      tc_fence_after();
+      // 32 columns at a time through the warp's staging rows, so that four lanes write 64 bytes of a row.
+      const int ncol = a.dh - 64 * half, nkey = x.len - x.t0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // dV, dV, dK, dK
+        const int h = k & 1;
+        const PackedRows& out = k < 2 ? a.dv : a.dk;
+        const float f = k < 2 ? 1.f : a.scale;
+        if (32 * h < ncol) {
+          float o[32];
+          tmem_ld32(tv + (k >> 1) * kRows + 32 * h, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float* v = o + 8 * u;
+            sts128(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(f * v[0], f * v[1]),
+                   pack_bf16x2(f * v[2], f * v[3]), pack_bf16x2(f * v[4], f * v[5]), pack_bf16x2(f * v[6], f * v[7]));
+          }
+        }
+        if (k == 3) arrive(acc_free);
+        __syncwarp();
+        if (32 * h < ncol) {
+          const int col = 32 * h + 8 * (lane & 3);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = 8 * u + (lane >> 2), key = quarter * 32 + r;
+            uint4 v;
+            umma::lds128(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
+            if (key < nkey && col < ncol)
+              *reinterpret_cast<uint4*>(out.p + (x.row0 + x.t0 + key) * out.ld + 1LL * x.head * a.dh + 64 * half + col) = v;
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+}  // namespace dkv
+
+cudaError_t launch_packed_dkv(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st) {
+  using namespace dkv;
+  cudaError_t e = configure<packed_dkv_kernel, kSmem>();
+  if (e != cudaSuccess) return e;
+  const int G = p.Hq / p.Hk, tq = kRows / G;
+  dkv::Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!encode_heads(&maps.q, p.q, p.T, p.Hq, p.dh, G, tq) || !encode_heads(&maps.dout, p.dout, p.T, p.Hq, p.dh, G, tq) ||
+      !encode_heads(&maps.k, p.k, p.T, p.Hk, p.dh, 1, kRows) || !encode_heads(&maps.v, p.v, p.T, p.Hk, p.dh, 1, kRows))
+    return cudaErrorInvalidValue;
+  const dkv::Args a{p.dk, p.dv, p.lse, D, p.scale, p.Hq, p.dh, G, tq, group_magic(G),
+                    taken(plan, p.Hk, 4LL * p.T * G * p.dh), err};
+  const long long items = plan_capacity(p.T, p.nseq, kRows) * p.Hk;
+  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
+  return launch_pdl(packed_dkv_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
+}
+
+}  // namespace packed
+}  // namespace lr

@@ -27,28 +27,80 @@ struct Plan {
   int* starts;     // [nseq + 1] blocks before each sequence
 };
 
-// A list of blocks of `tokens` tokens.
+// The most blocks of `tokens` tokens that the sequences can have.
 inline long long plan_capacity(int T, int nseq, int tokens) {
   const long long n = T / tokens + 1LL * nseq;
   return n < T ? n : T;
 }
 size_t plan_layout(int T, int nseq, int tokens, void* base, Plan* plan);
-// work: +1: a block's work grows with its place (queries), -1: with what follows it (keys).
-cudaError_t launch_plan(const PackedArgs& a, int tokens, int work, const Plan& plan, unsigned* err, cudaStream_t st);
 
-// The block's t-th item: false past the end.
-struct Order {
-  int nblocks, heads, group;
-  __device__ __forceinline__ bool item(unsigned t, int& block, int& head) const {
-    const unsigned all = static_cast<unsigned>(nblocks) * heads;
-    if (t >= all) return false;
-    const unsigned per = static_cast<unsigned>(group) * nblocks, gi = t / per, r = t - gi * per;
+struct PlanJob {
+  Plan plan;
+  int tokens;
+  int work;  // +1: a block's work grows with its place (its keys), -1: with what follows it (its queries)
+};
+// One launch: the lists, and (D not null) D[t, h] = dout.o of every row and head.
+cudaError_t launch_prepare(const PackedArgs& a, const PlanJob* jobs, int njobs, float* D, unsigned* err, cudaStream_t st);
+
+// What an item needs, from its ring slot.
+struct Item {
+  int row0, len, t0, head;  // the sequence's first row and length, the item's first token in it, the key head
+  // Tokens of a row tile of tq, the keys that some row of it sees, and the key blocks they are in.
+  __device__ __forceinline__ int tokens(int tile, int tq) const { return min(tq, len - t0 - tile * tq); }  // may be < 1
+  __device__ __forceinline__ int keys(int tile, int tq) const {
+    const int n = tokens(tile, tq);
+    return n > 0 ? t0 + tile * tq + n : 0;
+  }
+  __device__ __forceinline__ int nblocks(int tile, int tq) const { return (keys(tile, tq) + kRows - 1) / kRows; }
+};
+
+// The items of a launch, in the order they are taken.
+struct Taken {
+  const int* nblocks;
+  const int4* blocks;
+  unsigned* next;
+  int heads, group;  // key heads, and how many are worked on together
+  // The t-th: an Item, its head negative past the end.
+  __device__ __forceinline__ int4 item(unsigned t) const {
+    const unsigned n = static_cast<unsigned>(*nblocks);
+    if (t >= n * heads) return make_int4(0, 0, 0, -1);
+    const unsigned per = group * n, gi = t / per, r = t - gi * per;
     const unsigned gh = min(group, heads - static_cast<int>(gi) * group);
-    block = static_cast<int>(r / gh);
-    head = static_cast<int>(gi * group + r % gh);
-    return true;
+    int4 v = blocks[r / gh];
+    v.w = static_cast<int>(gi * group + r % gh);
+    return v;
   }
 };
+inline Taken taken(const Plan& plan, int heads, long long bytes_per_head) {
+  return Taken{plan.nblocks, plan.blocks, plan.next, heads, heads_per_group(heads, bytes_per_head)};
+}
+
+// Registers a thread of the kernels of 12 warps: the launch gives 168; the first four warps keep 88, the others take 208
+// (88 + 2 x 208 is 3 x 168).
+constexpr int kRegs = 168, kRegsFew = 88, kRegsMany = 208;
+static_assert(kRegsFew + 2 * kRegsMany <= 3 * kRegs, "register split");
+
+// Once per device: the shared memory of a kernel, and that its registers allow the split (warps would wait for them
+// forever).
+template <auto Kernel, int Smem>
+cudaError_t configure() {
+  static int done = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 32) return cudaErrorInvalidDevice;
+  if (__atomic_load_n(&done, __ATOMIC_ACQUIRE) & (1 << dev)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, Kernel);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * kThreads < 128 * kRegsFew + 256 * kRegsMany) return cudaErrorInvalidConfiguration;
+  __atomic_fetch_or(&done, 1 << dev, __ATOMIC_RELEASE);
+  return cudaSuccess;
+}
+
+cudaError_t launch_packed_dq(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st);
+cudaError_t launch_packed_dkv(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st);
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(

@@ -37,10 +37,6 @@ constexpr int kStages = 4;
 constexpr int kStageOut = 4096;  // a warp's 32 rows x 64 columns of the output
 constexpr int kSmem = 1024 + 2 * kTile + kStages * kTile + 8 * kStageOut + 512;
 constexpr float kLazy = 8.f;
-// Registers a thread: the launch gives 168; the first four warps keep 88, the softmax warps take 208 (88 + 2 x 208 is
-// 3 x 168).
-constexpr int kRegs = 168, kRegsFew = 88, kRegsMany = 208;
-static_assert(kRegsFew + 2 * kRegsMany <= 3 * kRegs, "register split");
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -52,23 +48,8 @@ struct Args {
   float scale;
   int Hq, dh, G, tq;  // tq: tokens of a row tile
   unsigned magic;     // of G
-  const int* nblocks;
-  const int4* blocks;
-  unsigned* next;
-  int heads, group;   // key heads, and how many are worked on together
+  Taken taken;
   unsigned* err;
-};
-
-// What an item needs, from its ring slot.
-struct Item {
-  int row0, len, t0, head;  // the sequence's first row and length, the item's first token in it, the key head
-  __device__ __forceinline__ int tokens(int tile, int tq) const { return min(tq, len - t0 - tile * tq); }  // may be < 1
-  // Keys that some row of the tile sees, and the key blocks they are in.
-  __device__ __forceinline__ int keys(int tile, int tq) const {
-    const int n = tokens(tile, tq);
-    return n > 0 ? t0 + tile * tq + n : 0;
-  }
-  __device__ __forceinline__ int nblocks(int tile, int tq) const { return (keys(tile, tq) + kRows - 1) / kRows; }
 };
 
 // This warp's part of P (of 64 keys) is in TMEM.
@@ -238,22 +219,16 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
         ++q_issued[tile];
         return true;
       };
-      const Order order{*a.nblocks, a.heads, a.group};
       unsigned t = blockIdx.x;
       for (int it = 0; ok; ++it) {
-        int block = 0, head = -1;
-        int4 v = make_int4(0, 0, 0, -1);
-        if (order.item(t, block, head)) {
-          v = a.blocks[block];
-          v.w = head;
-        }
+        const int4 v = a.taken.item(t);
         const int slot = it % kItems;
         ok = mbar_wait(&item_empty[slot], static_cast<uint32_t>((it / kItems) & 1) ^ 1u, abort_flag, a.err,
                        DEV_ERR_TIMEOUT_PRODUCER);
         if (!ok) break;
         sitem[slot] = v;
         mbar_arrive(&item_full[slot]);  // release: the readers see the item
-        if (head < 0) break;
+        if (v.w < 0) break;
         const Item x{v.x, v.y, v.z, v.w};
         const int n1 = x.nblocks(1, a.tq), nmax = max(x.nblocks(0, a.tq), n1);
         ok = load_q(0, x);
@@ -261,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
           const int row = x.row0 + j * kRows;
           // The next item is taken as late as the loads that are left cover the counter's latency: taken earlier, it
           // would bind the last items to blocks that are still busy.
-          if (j == max(0, nmax - 2)) t = gridDim.x + atomicAdd(a.next, 1u);
+          if (j == max(0, nmax - 2)) t = gridDim.x + atomicAdd(a.taken.next, 1u);
           ok = load_tile(&maps.k, row, x.head);
           if (ok && j == 0 && n1 > 0) ok = load_q(1, x);
           ok = ok && load_tile(&maps.v, row, x.head);
@@ -453,32 +428,19 @@ size_t packed_attn_fwd_ws_bytes(int T, int nseq, int Hq, int Hk) {
 cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st) {
   using namespace packed;
   using namespace packed::fwd;
-  static int configured_mask = 0;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 32) return cudaErrorInvalidDevice;
-  if (!(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & (1 << dev))) {
-    cudaError_t e = cudaFuncSetAttribute(packed_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    // The register split must fit what the kernel is launched with: the softmax warps would wait for it forever.
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, packed_fwd_kernel);
-    if (e != cudaSuccess) return e;
-    if (fa.numRegs * kThreads < 128 * kRegsFew + 256 * kRegsMany) return cudaErrorInvalidConfiguration;
-    __atomic_fetch_or(&configured_mask, 1 << dev, __ATOMIC_RELEASE);
-  }
+  cudaError_t e = configure<packed_fwd_kernel, kSmem>();
+  if (e != cudaSuccess) return e;
   const int G = p.Hq / p.Hk, tq = kRows / G;
   fwd::Maps maps;
   memset(&maps, 0, sizeof(maps));
   if (!encode_heads(&maps.q, p.q, p.T, p.Hq, p.dh, G, tq) || !encode_heads(&maps.k, p.k, p.T, p.Hk, p.dh, 1, kRows) ||
       !encode_heads(&maps.v, p.v, p.T, p.Hk, p.dh, 1, kRows))
     return cudaErrorInvalidValue;
-  Plan plan;
-  plan_layout(p.T, p.nseq, 2 * tq, ws, &plan);
-  cudaError_t e = launch_plan(p, 2 * tq, 1, plan, err, st);
+  PlanJob job{{}, 2 * tq, 1};
+  plan_layout(p.T, p.nseq, job.tokens, ws, &job.plan);
+  e = launch_prepare(p, &job, 1, nullptr, err, st);
   if (e != cudaSuccess) return e;
-  fwd::Args a{p.o, p.lse, p.scale, p.Hq, p.dh, G, tq, group_magic(G), plan.nblocks, plan.blocks, plan.next, p.Hk,
-              heads_per_group(p.Hk, 4LL * p.T * p.dh), err};
+  const fwd::Args a{p.o, p.lse, p.scale, p.Hq, p.dh, G, tq, group_magic(G), taken(job.plan, p.Hk, 4LL * p.T * p.dh), err};
   const long long items = plan_capacity(p.T, p.nseq, 2 * tq) * p.Hk;
   const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
   return launch_pdl(packed_fwd_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);

@@ -1,8 +1,9 @@
-// The list of blocks of the packed-attention kernels (packed_device.cuh), made by one thread block: it checks the
+// The first launch of the packed-attention calls.  One thread block for each list of blocks (packed_device.cuh): it checks the
 // offsets (any that is out of order leaves an empty list and an error bit), counts each sequence's blocks, and sorts
 // the blocks into 1024 bins of work.  Blocks of one bin may come in any order; no result depends on it.
 //
-// It takes 3 to 4 us for the sequences of a usual batch, most of it its barriers, and about 20 us for 16384 blocks.
+// In the backward the other blocks take D = dout.o of every row and head: 8 or 16 lanes a head, 16 bytes of both tensors a
+// lane, four heads in flight (rows of no sequence too: nothing reads theirs).
 #include "packed_device.cuh"
 
 #include <algorithm>
@@ -37,10 +38,9 @@ __device__ __forceinline__ int scan(int v, int* warps, int& total) {
   return before + s - v;
 }
 
-__global__ void __launch_bounds__(kThreads) plan_kernel(PackedArgs a, int tokens, int work, Plan plan, unsigned* err) {
+__device__ __forceinline__ void make_list(const PackedArgs& a, int tokens, int work, const Plan& plan, unsigned* err) {
   __shared__ int warps[32], bins[kBins], s_bad, s_longest;
   const int tid = threadIdx.x;
-  pdl_wait();
   if (tid == 0) s_bad = s_longest = 0;
   bins[tid] = 0;
   __syncthreads();
@@ -107,6 +107,49 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedArgs a, int tokens
   }
 }
 
+struct Jobs {
+  PlanJob job[2];
+};
+
+// D of four consecutive (row, head) for each group of `lanes` lanes.
+__device__ __forceinline__ void row_dots(const PackedArgs& a, float* D, int block, int lanes) {
+  const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes, c = 8 * lane;
+  const long long first = (1LL * block * (kThreads / lanes) + group) * 4, all = 1LL * a.T * a.Hq;
+  uint4 x[4], y[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const long long id = first + u;
+    x[u] = y[u] = make_uint4(0, 0, 0, 0);
+    if (id < all && c < a.dh) {
+      const long long t = id / a.Hq, col = (id - t * a.Hq) * a.dh + c;
+      x[u] = *reinterpret_cast<const uint4*>(a.o.p + t * a.o.ld + col);
+      y[u] = *reinterpret_cast<const uint4*>(a.dout.p + t * a.dout.ld + col);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float v[8], w[8], s = 0.f;
+    load8(reinterpret_cast<const bf16*>(&x[u]), v);
+    load8(reinterpret_cast<const bf16*>(&y[u]), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(v[e], w[e], s);
+    for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && first + u < all) D[first + u] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) prepare_kernel(PackedArgs a, Jobs jobs, int njobs, float* D, int lanes,
+                                                           unsigned* err) {
+  pdl_wait();
+  const int b = static_cast<int>(blockIdx.x);
+  if (b < njobs) {
+    const PlanJob j = b == 0 ? jobs.job[0] : jobs.job[1];
+    make_list(a, j.tokens, j.work, j.plan, err);
+  } else {
+    row_dots(a, D, b - njobs, lanes);
+  }
+}
+
 }  // namespace
 
 size_t plan_layout(int T, int nseq, int tokens, void* base, Plan* plan) {
@@ -125,8 +168,14 @@ size_t plan_layout(int T, int nseq, int tokens, void* base, Plan* plan) {
   return (at + 255) / 256 * 256;
 }
 
-cudaError_t launch_plan(const PackedArgs& a, int tokens, int work, const Plan& plan, unsigned* err, cudaStream_t st) {
-  return launch_pdl(plan_kernel, dim3(1), dim3(kThreads), 0, st, a, tokens, work, plan, err);
+cudaError_t launch_prepare(const PackedArgs& a, const PlanJob* jobs, int njobs, float* D, unsigned* err,
+                           cudaStream_t st) {
+  Jobs j{};
+  for (int i = 0; i < njobs; ++i) j.job[i] = jobs[i];
+  const int lanes = a.dh > 64 ? 16 : 8;
+  const long long each = kThreads / lanes * 4, dots = D ? (1LL * a.T * a.Hq + each - 1) / each : 0;
+  return launch_pdl(prepare_kernel, dim3(static_cast<unsigned>(njobs + dots)), dim3(kThreads), 0, st, a, j, njobs, D, lanes,
+                    err);
 }
 
 }  // namespace packed
