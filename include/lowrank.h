@@ -357,7 +357,7 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
  * dlogp: fp32 [T]; dentropy: fp32 [T] or NULL (entropy is then unused and may be NULL);
  * lse, entropy: the forward's.  dlogits may be logits (the same pointer and row distance).
  * Rows without a gradient (no target or dlogp 0, and dentropy 0) are set to 0 unread.
- * scale finite and positive; V <= 2^20, T <= 2^24; every pointer 16-byte aligned (rows need not be).
+ * scale finite and positive; V <= 2^19, T <= 2^24; every pointer 16-byte aligned (rows need not be).
  * Sums are fp32; the gradient is rounded once.
  */
 size_t lr_logprob_workspace_bytes(lr_dtype dt, int T, int V, int top);

@@ -2,15 +2,14 @@
 //
 // Both are bound by memory: the forward reads each logit once, the backward reads it and writes its gradient.  A block
 // takes one row's chunk; a warp reads 256 consecutive logits at a time, each lane 8 of them (16 bytes of bf16, 32 of
-// fp32), four such groups in flight.  Rows may begin anywhere (an odd V leaves no row but the first on a 16-byte
+// fp32), 64 bytes a lane in flight.  Rows may begin anywhere (an odd V leaves no row but the first on a 16-byte
 // boundary): groups are cut at aligned addresses, and the first and last of a row are read element by element.
 // A long row of few is cut over blocks, whose parts the join adds up in a fixed order.
 //
-// The largest logits: the maximum of each segment of 256 or 1024 logits is kept beside the sums (a warp reduction and
-// 4 bytes for 256 logits).  By (value descending, index ascending) the K largest logits lie in the K segments whose
+// The largest logits: the maximum of each segment of 256 logits is kept beside the sums (a warp reduction and 4 bytes).  By (value descending, index ascending) the K largest logits lie in the K segments whose
 // maxima are the largest by the same order; so the join ranks the segments and reads K of them again.  Ranking a list
-// takes its threads' own maxima first: the K-th of these bounds what can be among the K largest, and only what reaches
-// it is compared with each other (K times a thread's share at most, whatever the values).
+// takes the maxima of 64 groups of threads first: the K-th of these bounds what can be among the K largest, and only what
+// reaches it is compared with each other (K times a group's share at most, whatever the values).
 #include "logprob_kernels.cuh"
 
 #include <algorithm>
@@ -22,7 +21,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kGroup = 8;            // logits of a lane's load
 constexpr int kWarpRun = 32 * kGroup;  // of a warp's
-constexpr int kUnroll = 4;           // groups in flight
+template <typename ST>
+constexpr int kUnroll = 8 / sizeof(ST);  // groups in flight: 64 bytes a lane
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Differences to the maximum are cut off here (2^-200 is 0 in fp32), so that a logit of -inf gives 0 and not 0 * inf.
@@ -75,6 +75,19 @@ __device__ __forceinline__ void load_group(const ST* row, int i, int V, float* v
     load_edge(row, i, V, v);
 }
 
+// kUnroll groups of a lane, `stride` logits apart: all loads before the first conversion.
+template <typename ST>
+__device__ __forceinline__ void load_groups(const ST* p, int stride, float (*v)[kGroup]) {
+  constexpr int n = sizeof(ST) / 2;  // 16-byte loads of a group
+  uint4 raw[kUnroll<ST>][n];
+#pragma unroll
+  for (int u = 0; u < kUnroll<ST>; ++u)
+#pragma unroll
+    for (int i = 0; i < n; ++i) raw[u][i] = reinterpret_cast<const uint4*>(p + u * stride)[i];
+#pragma unroll
+  for (int u = 0; u < kUnroll<ST>; ++u) load8(reinterpret_cast<const ST*>(raw[u]), v[u]);
+}
+
 // m, s, w of a part of a row.
 struct Part {
   float m, s, w;
@@ -93,7 +106,7 @@ __device__ __forceinline__ Part join(Part a, Part b, float c) {
 }
 
 __device__ __forceinline__ Part warp_join(Part p, float c) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1)
     p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
                      __shfl_xor_sync(0xffffffffu, p.w, o)}, c);
@@ -106,15 +119,18 @@ __device__ __forceinline__ float log_prob(float x, const Part& p, float scale) {
   return x == neg_inf() ? x : fmaf(scale, x - p.m, -kLn2 * log2f(p.s));
 }
 
+// The logit of a row's target.
 template <typename ST>
-__device__ __forceinline__ void finish(const LogprobFwd& a, int t, Part p) {
+__device__ __forceinline__ float target_logit(const LogprobFwd& a, int t, bool& has) {
   const int k = a.target[t];
+  has = k >= 0 && k < a.V;
+  return has ? to_float(static_cast<const ST*>(a.logits)[t * a.ld + k]) : 0.f;
+}
+
+__device__ __forceinline__ void finish(const LogprobFwd& a, int t, Part p, float x, bool has) {
   const float l2 = log2f(p.s), nan = __int_as_float(0x7fc00000);
   const bool none = p.m == neg_inf(), bad = !(p.m <= kMax);
-  float logp = bad ? nan : 0.f;
-  if (k >= 0 && k < a.V)
-    logp = log_prob(to_float(static_cast<const ST*>(a.logits)[t * a.ld + k]), p, a.scale);
-  a.logp[t] = logp;
+  a.logp[t] = has ? log_prob(x, p, a.scale) : bad ? nan : 0.f;
   a.entropy[t] = bad ? nan : none ? 0.f : kLn2 * (l2 - p.w / p.s);
   a.lse[t] = bad ? nan : none ? neg_inf() : fmaf(a.scale, p.m, kLn2 * l2);
 }
@@ -127,49 +143,52 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 template <typename ST, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(LogprobFwd a, LogprobPlan plan) {
+__global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 ? 5 : 6) logprob_fwd_kernel(LogprobFwd a, LogprobPlan plan) {
   __shared__ Part warps[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.x / plan.splits), split = static_cast<int>(blockIdx.x - 1u * t * plan.splits);
   const ST* row = static_cast<const ST*>(a.logits) + t * a.ld;
   const float c = a.scale * kLog2e;
   pdl_wait();
+  pdl_trigger();
   const int shift = lead(row);
   // places in the row, counted from the boundary before it
   const long long begin = 1LL * split * plan.chunk;
   const int end = static_cast<int>(min(begin + plan.chunk, 1LL * a.V + shift));
   Part p{neg_inf(), 0.f, 0.f};
-  constexpr int kRun = kWarpRun * kUnroll;
+  constexpr int kU = kUnroll<ST>, kRun = kWarpRun * kU;
   for (int i = static_cast<int>(begin) + warp * kRun; i < end; i += kWarps * kRun) {
-    float v[kUnroll][kGroup];
+    float v[kU][kGroup];
+    const int at = i + lane * kGroup - shift;
     if (i >= shift && i + kRun <= end && i + kRun <= a.V + shift) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) load8(row + (i + u * kWarpRun + lane * kGroup - shift), v[u]);
+      load_groups(row + at, kWarpRun, v);
     } else {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) load_group(row, i + u * kWarpRun + lane * kGroup - shift, a.V, v[u]);
+      for (int u = 0; u < kU; ++u) load_group(row, at + u * kWarpRun, a.V, v[u]);
     }
     float gm = neg_inf();
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float um = v[u][0];
+    for (int u = 0; u < kU; u += 2) {
+      float um[2];
 #pragma unroll
-      for (int e = 1; e < kGroup; ++e) um = max_nan(um, v[u][e]);
-      gm = max_nan(gm, um);
-      if (TOP && plan.seg == kWarpRun) {
-        const float r = warp_max(um);
-        const int run = i + u * kWarpRun;
-        if (lane == 0 && run < end) a.segmax[1LL * t * plan.nseg + run / kWarpRun] = r;
+      for (int w = 0; w < 2; ++w) {
+        um[w] = v[u + w][0];
+#pragma unroll
+        for (int e = 1; e < kGroup; ++e) um[w] = max_nan(um[w], v[u + w][e]);
+        gm = max_nan(gm, um[w]);
       }
-    }
-    if (TOP && plan.seg == kRun) {
-      const float r = warp_max(gm);
-      if (lane == 0) a.segmax[1LL * t * plan.nseg + i / kRun] = r;
+      if (TOP) {
+        const int run = i + u * kWarpRun;
+        float* seg = a.segmax + 1LL * t * plan.nseg + run / kLogprobSeg;
+        const float r0 = warp_max(um[0]), r1 = warp_max(um[1]);
+        if (lane == 0 && run < end) seg[0] = r0;
+        if (lane == 0 && run + kWarpRun < end) seg[1] = r1;
+      }
     }
     if (!(gm <= p.m)) p = join(p, Part{gm, 0.f, 0.f}, c);
     if (p.m > neg_inf()) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < kU; ++u) {
         float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < kGroup; ++e) {
@@ -186,12 +205,15 @@ __global__ void __launch_bounds__(kThreads) logprob_fwd_kernel(LogprobFwd a, Log
   if (lane == 0) warps[warp] = p;
   __syncthreads();
   if (threadIdx.x == 0) {
-#pragma unroll
+#pragma unroll 1
     for (int i = 1; i < kWarps; ++i) p = join(p, warps[i], c);
-    if (TOP || plan.splits > 1)
+    if (TOP || plan.splits > 1) {
       a.part[1LL * t * plan.splits + split] = make_float4(p.m, p.s, p.w, 0.f);
-    else
-      finish<ST>(a, t, p);
+    } else {
+      bool has;
+      const float x = target_logit<ST>(a, t, has);
+      finish(a, t, p, x, has);
+    }
   }
 }
 
@@ -204,106 +226,128 @@ __device__ __forceinline__ unsigned order(float v) {
 __device__ __forceinline__ unsigned long long key_of(float v, int place) {
   return static_cast<unsigned long long>(order(v)) << 32 | (0xffffffffu - static_cast<unsigned>(place));
 }
+__device__ __forceinline__ float value_of(unsigned long long key) {
+  const unsigned o = static_cast<unsigned>(key >> 32);
+  return __uint_as_float(o & 0x80000000u ? (o == 0xffffffffu ? 0x7fc00000u : o & 0x7fffffffu) : ~o);
+}
 __device__ __forceinline__ int place_of(unsigned long long key) {
   return static_cast<int>(0xffffffffu - static_cast<unsigned>(key));
 }
 
-constexpr int kLongSeg = kWarpRun * kUnroll;
-constexpr int kSegs = kLogprobMaxV / kLongSeg + 1;  // per row at most
-// Logits that can reach the bound: K times a thread's share of K segments.
-constexpr int kKept = kLogprobMaxTop * (kLogprobMaxTop * kLongSeg / kThreads);
+static_assert(kLogprobSeg == kWarpRun, "a segment is what a warp reads at a time");
+// Logits that can reach the bound: K times the share of four threads of K segments.
+constexpr int kKept = kLogprobMaxTop * (4 * kLogprobMaxTop * kLogprobSeg / kThreads);
+static_assert((kLogprobMaxV / kLogprobSeg / kThreads + 1) * 4 <= kKept / kLogprobMaxTop, "segments that can reach it");
 
-// Of the block's threads' own keys (0: none), the K-th largest; 0 where there are fewer.
-__device__ __forceinline__ unsigned long long kth(unsigned long long own, int K, unsigned long long* each,
-                                                  unsigned long long* bound) {
-  each[threadIdx.x] = own;
-  if (threadIdx.x == 0) *bound = 0;
+struct TopShared {
+  unsigned long long keys[kKept], each[kThreads / 4], bound;
+  int picked[kLogprobMaxTop];  // segments
+  int count;
+  Part part;
+};
+
+// Of 64 maxima of the keys of four threads each (0: none), the K-th largest; 0 where there are fewer.
+__device__ __forceinline__ unsigned long long kth(unsigned long long own, int K, TopShared& s) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) own = max(own, __shfl_xor_sync(0xffffffffu, own, o));
+  const int part = threadIdx.x & 3;
+  if (part == 0) s.each[threadIdx.x >> 2] = own;
   __syncthreads();
-  if (own) {
-    int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < kThreads; ++j) rank += each[j] > own;
-    if (rank == K - 1) *bound = own;
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < 16; ++j) rank += s.each[16 * part + j] > own;
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+  if (own && rank == K - 1) s.bound = own;  // four threads, the same value
+  __syncthreads();
+  return s.bound;
+}
+
+// Leaves in s.keys the keys that reach the K-th of the groups' maxima.  each(f) calls f for this thread's keys.
+template <typename F>
+__device__ __forceinline__ void reach_bound(int K, TopShared& s, F each) {
+  if (threadIdx.x == 0) {
+    s.bound = 0;
+    s.count = 0;
   }
+  unsigned long long own = 0;
+  each([&](unsigned long long k) { own = max(own, k); });
+  const unsigned long long bound = max(kth(own, K, s), 1ull);
+  if (own >= bound)
+    each([&](unsigned long long k) {
+      if (k >= bound) s.keys[atomicAdd(&s.count, 1)] = k;
+    });
   __syncthreads();
-  return *bound;
+}
+
+// Calls use(rank, key) for the K largest of the kept keys: 16 lanes count the larger ones of each.
+template <typename F>
+__device__ __forceinline__ void rank_keys(const TopShared& s, int K, F use) {
+  const int part = threadIdx.x & 15, n = s.count;
+#pragma unroll 1
+  for (int base = 0; base < n; base += kThreads / 16) {
+    const int i = base + (threadIdx.x >> 4);
+    const unsigned long long k = i < n ? s.keys[i] : 0;
+    int rank = 0;
+#pragma unroll 2
+    for (int j = part; j < n; j += 16) rank += s.keys[j] > k;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (part == 0 && i < n && rank < K) use(rank, k);
+  }
 }
 
 // One block per row.
 template <typename ST>
 __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, LogprobPlan plan) {
-  __shared__ Part s_part;
-  __shared__ unsigned long long keys[kKept], each[kThreads], s_bound;
-  __shared__ int picked[kLogprobMaxTop];
-  __shared__ int s_count[2];
+  __shared__ __align__(16) TopShared s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x, K = a.top;
   const float c = a.scale * kLog2e;
   pdl_wait();
+  bool has = false;
+  float target = 0.f;
+  if (threadIdx.x == kThreads - 1) target = target_logit<ST>(a, t, has);  // asked for early, used at the end
   if (warp == 0) {
     Part p{neg_inf(), 0.f, 0.f};
+#pragma unroll 1
     for (int i = lane; i < plan.splits; i += 32) {
       const float4 v = a.part[1LL * t * plan.splits + i];
       p = join(p, Part{v.x, v.y, v.z}, c);
     }
     p = warp_join(p, c);
-    if (lane == 0) {
-      s_part = p;
-      finish<ST>(a, t, p);
-    }
+    if (lane == 0) s.part = p;
   }
-  if (K == 0) return;
   const ST* row = static_cast<const ST*>(a.logits) + t * a.ld;
   const int shift = lead(row);
-  const int nseg = (a.V + shift + plan.seg - 1) / plan.seg;  // of this row
-  if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
-
-  // The K best segments (all where there are fewer).
-  unsigned long long own = 0;
-  for (int i = threadIdx.x; i < nseg; i += kThreads) own = max(own, key_of(a.segmax[1LL * t * plan.nseg + i], i));
-  unsigned long long bound = kth(own, K, each, &s_bound);
-  for (int i = threadIdx.x; i < nseg; i += kThreads) {
-    const unsigned long long k = key_of(a.segmax[1LL * t * plan.nseg + i], i);
-    if (k >= bound) keys[atomicAdd(&s_count[0], 1)] = k;
+  const int nseg = (a.V + shift + kLogprobSeg - 1) / kLogprobSeg;  // of this row
+  if (K > 0) {  // the K best segments (all where there are fewer)
+    const float* segmax = a.segmax + 1LL * t * plan.nseg;
+    reach_bound(K, s, [&](auto&& use) {
+      for (int i = threadIdx.x; i < nseg; i += kThreads) use(key_of(segmax[i], i));
+    });
+    rank_keys(s, K, [&](int rank, unsigned long long k) { s.picked[rank] = place_of(k); });
   }
   __syncthreads();
-  const int reach = s_count[0];
-  for (int i = threadIdx.x; i < reach; i += kThreads) {
-    const unsigned long long k = keys[i];
-    int rank = 0;
-    for (int j = 0; j < reach; ++j) rank += keys[j] > k;
-    if (rank < K) picked[rank] = place_of(k);
-  }
-  __syncthreads();
-
+  if (threadIdx.x == kThreads - 1) finish(a, t, s.part, target, has);
+  if (K == 0) return;
   // The K largest logits of these segments.
-  const int per = plan.seg / kGroup, groups = min(K, nseg) * per;
-  auto walk = [&](auto&& use) {
+  constexpr int kPer = kLogprobSeg / kGroup;
+  const int groups = min(K, nseg) * kPer;
+  reach_bound(K, s, [&](auto&& use) {
+#pragma unroll 4
     for (int g = threadIdx.x; g < groups; g += kThreads) {
-      const int i = picked[g / per] * plan.seg + (g % per) * kGroup - shift;
-      if (i >= a.V || i + kGroup <= 0) continue;
+      const int i = s.picked[g / kPer] * kLogprobSeg + g % kPer * kGroup - shift;
       float v[kGroup];
       load_group(row, i, a.V, v);
 #pragma unroll
       for (int e = 0; e < kGroup; ++e)
         if (i + e >= 0 && i + e < a.V) use(key_of(v[e], i + e));
     }
-  };
-  own = 0;
-  walk([&](unsigned long long k) { own = max(own, k); });
-  bound = kth(own, K, each, &s_bound);
-  walk([&](unsigned long long k) {
-    if (k >= bound) keys[atomicAdd(&s_count[1], 1)] = k;
   });
-  __syncthreads();
-  const int n = s_count[1];
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const unsigned long long k = keys[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > k;
-    if (rank >= K) continue;
+  rank_keys(s, K, [&](int rank, unsigned long long k) {
     a.top_ids[1LL * t * K + rank] = place_of(k);
-    a.top_logp[1LL * t * K + rank] = log_prob(to_float(row[place_of(k)]), s_part, a.scale);
-  }
+    a.top_logp[1LL * t * K + rank] = log_prob(value_of(k), s.part, a.scale);
+  });
 }
 
 // 2^x of the gradient: bf16 takes the hardware approximation (its 2^-22 is far below the rounding of the result), fp32
@@ -326,52 +370,72 @@ struct Prob<float> {
 };
 
 template <typename ST, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int chunks, int chunk) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_bwd_kernel(LogprobBwd a, int chunks, int chunk) {
   const int t = static_cast<int>(blockIdx.x / chunks), part = static_cast<int>(blockIdx.x - 1u * t * chunks);
   const ST* row = static_cast<const ST*>(a.logits) + t * a.ld;
   ST* out = static_cast<ST*>(a.out) + t * a.ldo;
   pdl_wait();
   const int k = a.target[t];
-  const float lse = a.lse[t];
-  const float dl = k >= 0 && k < a.V ? a.dlogp[t] : 0.f;
+  const float lse = a.lse[t], given = a.dlogp[t];
   const float de = ENTROPY ? a.dentropy[t] : 0.f, h = ENTROPY ? a.entropy[t] : 0.f;
+  const float dl = k >= 0 && k < a.V ? given : 0.f;
+  // d_j = scale (p_j (-de (lp_j + H) - dl) + [j = target] dl) = p_j (e lp_j + f) + [j = target] hit
+  const float e = -de * a.scale, hit = dl * a.scale;
+  const float f = fmaf(e, h, -hit) + (lse - lse);  // NaN where lse is
   const int shift = lead(row), oshift = lead(out);
   const long long begin = 1LL * part * chunk;
   const int end = static_cast<int>(min(begin + chunk, 1LL * a.V + shift));
-  // no gradient, or no distribution (every logit -inf)
-  const bool zero = (dl == 0.f && de == 0.f) || lse == neg_inf();
-  const float nan = lse - lse;  // 0, or NaN where lse is
-  for (int i = static_cast<int>(begin) + threadIdx.x * kGroup; i < end; i += kThreads * kGroup * kUnroll) {
-    float v[kUnroll][kGroup];
-    if (!zero) {
+  constexpr int kU = kUnroll<ST>, kStride = kThreads * kGroup;
+  const bool zero = (dl == 0.f && de == 0.f) || lse == neg_inf();  // no gradient, or no distribution
+  const bool whole = oshift == shift;  // both rows can be taken in aligned groups
+  auto gradient = [&](float* v, int at) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int at = i + u * kThreads * kGroup;
-        if (at < end) load_group(row, at - shift, a.V, v[u]);
-      }
+    for (int i = 0; i < kGroup; ++i) {
+      float lp, p;
+      Prob<ST>::get(v[i], a.scale, lse, lp, p);
+      v[i] = p * (ENTROPY ? fmaf(e, lp, f) : f);
     }
+    if (static_cast<unsigned>(k - at) < kGroup && hit != 0.f) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int at = i + u * kThreads * kGroup - shift;
-      if (at + shift >= end) break;
+      for (int i = 0; i < kGroup; ++i)
+        if (at + i == k) v[i] += hit;
+    }
+  };
+  for (int i = static_cast<int>(begin); i < end; i += kU * kStride) {
+    const int at = i + threadIdx.x * kGroup - shift;
+    float v[kU][kGroup];
+    if (whole && i >= shift && i + kU * kStride <= end && i + kU * kStride <= a.V + shift) {
+      if (zero) {
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) {
-        float d = 0.f;
-        if (!zero) {
-          float lp, p;
-          Prob<ST>::get(v[u][e], a.scale, lse, lp, p);
-          d = -p * (ENTROPY ? fmaf(de, lp + h, dl) : dl) + nan;
-          if (at + e == k) d += dl;
-          d *= a.scale;
-        }
-        v[u][e] = d;
-      }
-      if (at >= 0 && at + kGroup <= a.V && oshift == shift) {
-        store8(out + at, v[u]);
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int n = 0; n < kGroup; ++n) v[u][n] = 0.f;
       } else {
+        load_groups(row + at, kStride, v);
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e)
-          if (at + e >= 0 && at + e < a.V) out[at + e] = from_float<ST>(v[u][e]);
+        for (int u = 0; u < kU; ++u) gradient(v[u], at + u * kStride);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) store8(out + at + u * kStride, v[u]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int j = at + u * kStride;
+        if (j + shift >= end) break;
+        if (zero) {
+#pragma unroll
+          for (int n = 0; n < kGroup; ++n) v[u][n] = 0.f;
+        } else {
+          load_group(row, j, a.V, v[u]);
+          gradient(v[u], j);
+        }
+        if (whole && j >= 0 && j + kGroup <= a.V) {
+          store8(out + j, v[u]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < kGroup; ++n)
+            if (j + n >= 0 && j + n < a.V) out[j + n] = from_float<ST>(v[u][n]);
+        }
       }
     }
   }
@@ -382,15 +446,13 @@ __global__ void __launch_bounds__(kThreads) logprob_bwd_kernel(LogprobBwd a, int
 LogprobPlan logprob_plan(int T, int V, int es, int sms) {
   LogprobPlan p;
   const int most = V + 16 / es - 1;  // places of a row, counted from a 16-byte boundary
-  p.seg = most <= kWarpRun * kSegs ? kWarpRun : kLongSeg;
-  p.nseg = (most + p.seg - 1) / p.seg;
-  // One block to a row where rows fill the GPU (four blocks an SM); else a row over several, each with one load of all
-  // of its threads at least.
-  constexpr int step = kThreads * kGroup * kUnroll;
-  const int fit = (most + step - 1) / step;
-  const int want = (4 * sms + T - 1) / T;
+  p.nseg = (most + kLogprobSeg - 1) / kLogprobSeg;
+  // One block to a row where rows fill the GPU three times over (five blocks an SM); else a row over several, each with
+  // one load of half its threads at least.
+  const int fit = (most + 4095) / 4096;
+  const int want = (15 * sms + T - 1) / T;
   const int s = std::min({want, fit, kLogprobMaxSplits});
-  p.chunk = (fit + s - 1) / s * step;
+  p.chunk = ((most + s - 1) / s + 1023) / 1024 * 1024;
   p.splits = (most + p.chunk - 1) / p.chunk;
   return p;
 }
@@ -408,18 +470,23 @@ cudaError_t launch_logprob_join(const LogprobFwd& a, const LogprobPlan& plan, cu
 }
 
 template <typename ST>
-cudaError_t launch_logprob_bwd(const LogprobBwd& a, cudaStream_t st) {
-  constexpr int chunk = kThreads * kGroup * kUnroll;
-  const int chunks = (a.V + 16 / static_cast<int>(sizeof(ST)) - 1 + chunk - 1) / chunk;
+cudaError_t launch_logprob_bwd(const LogprobBwd& a, int sms, cudaStream_t st) {
+  // Chunks of up to four rounds of a block's loads, so that the row's scalars are read less often; of one where there are
+  // not enough for eight blocks an SM.
+  constexpr int step = kThreads * kGroup * kUnroll<ST>;
+  const int steps = (a.V + 16 / static_cast<int>(sizeof(ST)) - 1 + step - 1) / step;
+  const long long rounds = 1LL * a.T * steps / (8LL * sms);
+  const int per = static_cast<int>(std::max(1LL, std::min({rounds, 4LL, 1LL * steps})));
+  const int chunks = (steps + per - 1) / per;
   const dim3 grid(static_cast<unsigned>(1LL * a.T * chunks));
-  return a.dentropy ? launch_pdl(logprob_bwd_kernel<ST, true>, grid, dim3(kThreads), 0, st, a, chunks, chunk)
-                    : launch_pdl(logprob_bwd_kernel<ST, false>, grid, dim3(kThreads), 0, st, a, chunks, chunk);
+  return a.dentropy ? launch_pdl(logprob_bwd_kernel<ST, true>, grid, dim3(kThreads), 0, st, a, chunks, per * step)
+                    : launch_pdl(logprob_bwd_kernel<ST, false>, grid, dim3(kThreads), 0, st, a, chunks, per * step);
 }
 
 #define LR_INSTANTIATE(ST)                                                                         \
   template cudaError_t launch_logprob_fwd<ST>(const LogprobFwd&, const LogprobPlan&, cudaStream_t);  \
   template cudaError_t launch_logprob_join<ST>(const LogprobFwd&, const LogprobPlan&, cudaStream_t); \
-  template cudaError_t launch_logprob_bwd<ST>(const LogprobBwd&, cudaStream_t);
+  template cudaError_t launch_logprob_bwd<ST>(const LogprobBwd&, int, cudaStream_t);
 LR_INSTANTIATE(bf16)
 LR_INSTANTIATE(float)
 #undef LR_INSTANTIATE

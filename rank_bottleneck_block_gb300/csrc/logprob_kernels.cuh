@@ -14,15 +14,15 @@
 namespace lr {
 
 constexpr int kLogprobMaxTop = 32;
-constexpr int kLogprobMaxV = 1 << 20;
+constexpr int kLogprobMaxV = 1 << 19;
 constexpr int kLogprobMaxSplits = 64;
+constexpr int kLogprobSeg = 256;
 
 // How a forward cuts its rows.
 struct LogprobPlan {
-  int seg;     // logits whose maximum is kept as one (top > 0): 256, or 1024 in long rows
-  int nseg;    // such segments per row
+  int nseg;    // segments of kLogprobSeg logits per row, whose maxima are kept (top > 0)
   int splits;  // blocks per row, of
-  int chunk;   // this many logits each, a multiple of seg
+  int chunk;   // this many logits each, a multiple of 1024
 };
 LogprobPlan logprob_plan(int T, int V, int es, int sms);
 
@@ -56,6 +56,6 @@ struct LogprobBwd {
   float scale;
 };
 template <typename ST>
-cudaError_t launch_logprob_bwd(const LogprobBwd& a, cudaStream_t st);
+cudaError_t launch_logprob_bwd(const LogprobBwd& a, int sms, cudaStream_t st);
 
 }  // namespace lr

@@ -2797,7 +2797,7 @@ lr_status lr_logprob_fwd(lr_dtype dt, int T, int V, float scale, int top, const 
     if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities: %s", cudaGetErrorString(e));
   }
   if (logprob_joins(plan, top)) {
-    LaunchScope scope("logprob_join", c.st, 0, 1.0 * c.es * T * top * plan.seg);
+    LaunchScope scope("logprob_join", c.st, 0, 1.0 * c.es * T * top * kLogprobSeg);
     cudaError_t e = dt == LR_BF16 ? launch_logprob_join<bf16>(a, plan, c.st) : launch_logprob_join<float>(a, plan, c.st);
     if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities (join): %s", cudaGetErrorString(e));
   }
@@ -2823,7 +2823,7 @@ lr_status lr_logprob_bwd(lr_dtype dt, int T, int V, float scale, const void* log
   LR_TRY(make_ctx(dt, stream, &c));
   LogprobBwd a{logits, ld, target, lse, entropy, dlogp, dentropy, dlogits, lddlogits, T, V, scale};
   LaunchScope scope("logprob_bwd", c.st, 0, 2.0 * c.es * T * V);
-  cudaError_t e = dt == LR_BF16 ? launch_logprob_bwd<bf16>(a, c.st) : launch_logprob_bwd<float>(a, c.st);
+  cudaError_t e = dt == LR_BF16 ? launch_logprob_bwd<bf16>(a, c.sms, c.st) : launch_logprob_bwd<float>(a, c.sms, c.st);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "log probabilities backward: %s", cudaGetErrorString(e));
   return LR_OK;
 }

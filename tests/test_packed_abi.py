@@ -95,7 +95,7 @@ def _lbwd(L, dt=1, T=4, V=100, scale=1.0, logits=P, ld=100, target=P, lse=P, ent
 
 
 @pytest.mark.parametrize("over,status", [
-    (dict(dt=2), 4), (dict(T=0), 2), (dict(T=(1 << 24) + 1), 2), (dict(V=0), 2), (dict(V=(1 << 20) + 1, ld=1 << 21), 2),
+    (dict(dt=2), 4), (dict(T=0), 2), (dict(T=(1 << 24) + 1), 2), (dict(V=0), 2), (dict(V=(1 << 19) + 1, ld=1 << 21), 2),
     (dict(scale=0.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(logits=None), 1),
     (dict(logits=P + 2), 3), (dict(ld=99), 2), (dict(ld=1 << 32), 2), (dict(target=None), 1), (dict(target=P + 4), 3),
     (dict(lse=None), 1),
