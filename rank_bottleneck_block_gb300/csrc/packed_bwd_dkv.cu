@@ -17,7 +17,12 @@
 // Rows past the end of the sequence get P = dS = 0 by selection, and rows of dO and Q there are zeroed in shared memory
 // before their products.  Rows of a tile that no token has (128 is no multiple of G) stay zero from the start.
 //
-// Warps: 0 takes the items and loads them by TMA (K, V per item; Q_i, dO_i into a ring of two stages), 1 issuer of S^T
+// Q_i is needed from S^T of tile i to dK of tile i, four turns, and dO_i from dP^T to dV, two; so Q has three stages and dO
+// two (with two of both, loads came 600 cycles late for each tile).  That leaves 3 KB of shared memory: dK and dV are
+// written straight from registers, and the tiles begin at the start of the block's shared memory, whose alignment is
+// checked.
+//
+// Warps: 0 takes the items and loads them by TMA (K, V per item; Q_i, dO_i into their rings), 1 issuer of S^T
 // and dV, which also allocates TMEM, 2 issuer of dP^T and dK, 3 loads lse and D of each tile, 4-11 element-wise and output
 // (warp group h takes rows 64 h .. 64 h + 63 of a tile and columns 64 h .. of dK and dV).  TMEM: S^T at column 0, dP^T at
 // 128, dV at 256, dK at 384.  Every wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is
@@ -30,9 +35,9 @@ namespace lr {
 namespace packed {
 namespace dkv {
 
-constexpr int kStages = 2;
-constexpr int kStageOut = 2048;  // a warp's 32 rows x 32 columns of dK or dV
-constexpr int kSmem = 1024 + (2 + 2 * kStages) * kTile + 8 * kStageOut + kStages * 2 * kRows * 4 + 512;
+constexpr int kStagesQ = 3, kStagesO = 2;
+constexpr int kStages = 2;  // of lse and D
+constexpr int kSmem = (2 + kStagesQ + kStagesO) * kTile + kStages * 2 * kRows * 4 + 512;
 static_assert(kSmem <= umma::kMaxSmem, "shared memory");
 
 struct Maps {
@@ -55,32 +60,75 @@ struct Tiles {
   __device__ __forceinline__ Tiles(const Item& x, int tq) : first(x.t0 / tq), n((x.len + tq - 1) / tq - first) {}
 };
 
+// P of 64 rows (L: -lse log2 e of them) of one key from its scores, in place, and packed.  MASK: rows before `from` or from
+// `rows` on do not see the key.
+template <bool MASK>
+__device__ __forceinline__ void exps(float* p, const float* L, float c, int from, int rows, uint32_t* w) {
+  const uint64_t c2 = f2_pack(c, c);
+#pragma unroll
+  for (int u = 0; u < 64; u += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(L + u);
+    f2_unpack(f2_fma(f2_pack(p[u], p[u + 1]), c2, f2_pack(l.x, l.y)), p[u], p[u + 1]);
+    f2_unpack(f2_fma(f2_pack(p[u + 2], p[u + 3]), c2, f2_pack(l.z, l.w)), p[u + 2], p[u + 3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      p[u + e] = ex2_ftz(p[u + e]);
+      if (MASK && (u + e < from || u + e >= rows)) p[u + e] = 0.f;
+    }
+    w[u >> 1] = pack_bf16x2(p[u], p[u + 1]);
+    w[(u >> 1) + 1] = pack_bf16x2(p[u + 2], p[u + 3]);
+  }
+}
+
+// dS = P (dP - D) of the same rows, packed (nD: -D of them).
+template <bool MASK>
+__device__ __forceinline__ void grads(const float* p, const float* d, const float* nD, int from, int rows, uint32_t* w) {
+#pragma unroll
+  for (int u = 0; u < 64; u += 4) {
+    const float4 n = *reinterpret_cast<const float4*>(nD + u);
+    float g[4];
+    f2_unpack(f2_mul(f2_pack(p[u], p[u + 1]), f2_add(f2_pack(d[u], d[u + 1]), f2_pack(n.x, n.y))), g[0], g[1]);
+    f2_unpack(f2_mul(f2_pack(p[u + 2], p[u + 3]), f2_add(f2_pack(d[u + 2], d[u + 3]), f2_pack(n.z, n.w))), g[2], g[3]);
+    if (MASK) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (u + e < from || u + e >= rows) g[e] = 0.f;
+    }
+    w[u >> 1] = pack_bf16x2(g[0], g[1]);
+    w[(u >> 1) + 1] = pack_bf16x2(g[2], g[3]);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_constant__ Maps maps, const Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023u) {  // the swizzled tiles need it
+    if (threadIdx.x == 0) atomicOr(a.err, DEV_ERR_TMEM);
+    return;
+  }
   uint8_t* sK = smem;
   uint8_t* sV = sK + kTile;
-  uint8_t* sQ = sV + kTile;              // [kStages]
-  uint8_t* sdO = sQ + kStages * kTile;   // [kStages]
-  uint8_t* sOut = sdO + kStages * kTile;  // [8 warps]
-  float* sL = reinterpret_cast<float*>(sOut + 8 * kStageOut);  // [kStages][128] -lse log2 e
-  float* sD = sL + kStages * kRows;                            // [kStages][128]
+  uint8_t* sQ = sV + kTile;               // [kStagesQ]
+  uint8_t* sdO = sQ + kStagesQ * kTile;   // [kStagesO]
+  float* sL = reinterpret_cast<float*>(sdO + kStagesO * kTile);  // [kStages][128] -lse log2 e
+  float* sD = sL + kStages * kRows;                            // [kStages][128] -D
   uint64_t* bars = reinterpret_cast<uint64_t*>(sD + kStages * kRows);
   uint64_t* kv_full = bars;
   uint64_t* kv_free = bars + 1;    // the item's last S^T and last dP^T have read K and V
-  uint64_t* qd_full = bars + 2;    // [kStages]
-  uint64_t* qd_empty = bars + 4;   // [kStages] dV and dK of the tile are complete
-  uint64_t* st_full = bars + 6;    // [kStages] lse and D
-  uint64_t* st_empty = bars + 8;   // [kStages]
-  uint64_t* s_full = bars + 10;
-  uint64_t* dp_full = bars + 11;
-  uint64_t* p_full = bars + 12;
-  uint64_t* ds_full = bars + 13;
-  uint64_t* acc_full = bars + 14;  // the item's last dV and dK are complete
-  uint64_t* acc_free = bars + 15;  // they have been read
-  uint64_t* turn = bars + 16;      // [2]
-  uint64_t* drain = bars + 18;     // [2]
-  uint64_t* item_full = bars + 20;            // [kItems]
+  uint64_t* q_full = bars + 2;     // [kStagesQ]
+  uint64_t* q_empty = bars + 5;    // [kStagesQ] dK of the tile is complete (it needs S^T of it, which is then too)
+  uint64_t* o_full = bars + 8;     // [kStagesO]
+  uint64_t* o_empty = bars + 10;   // [kStagesO] dP^T and dV of the tile are complete
+  uint64_t* st_full = bars + 12;   // [kStages] lse and D
+  uint64_t* st_empty = bars + 14;  // [kStages]
+  uint64_t* s_full = bars + 16;
+  uint64_t* dp_full = bars + 17;
+  uint64_t* p_full = bars + 18;
+  uint64_t* ds_full = bars + 19;
+  uint64_t* acc_full = bars + 20;  // the item's last dV and dK are complete
+  uint64_t* acc_free = bars + 21;  // they have been read
+  uint64_t* turn = bars + 22;      // [2]
+  uint64_t* drain = bars + 24;     // [2]
+  uint64_t* item_full = bars + 26;            // [kItems]
   uint64_t* item_empty = item_full + kItems;  // [kItems]
   int4* sitem = reinterpret_cast<int4*>(item_empty + kItems);  // [kItems], 16-byte aligned
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sitem + kItems);
@@ -92,9 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     mbar_init(kv_free, 2);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&qd_full[i], 1);
-      mbar_init(&qd_empty[i], 2);
+    for (int i = 0; i < kStagesQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], 2);
       mbar_init(&st_full[i], 1);
       mbar_init(&st_empty[i], 8);
       mbar_init(&turn[i], 1);
@@ -114,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (a.G * a.tq < kRows)  // rows that the loads never write
-    for (int i = warp; i < 2 * kStages; i += kThreads / 32) zero_rows(sQ + i * kTile, a.G * a.tq, kRows, 2);
+    for (int i = warp; i < kStagesQ + kStagesO; i += kThreads / 32) zero_rows(sQ + i * kTile, a.G * a.tq, kRows, 2);
   fence_async_smem();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot))
@@ -169,17 +221,24 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
         ++issued;
         for (int i = 0; i < tiles.n && ok; ++i, ++g) {
           if (i == max(0, tiles.n - 2)) t = gridDim.x + atomicAdd(a.taken.next, 1u);  // late: see the forward
-          const int st = g % kStages;
-          ok = wait(&qd_empty[st], g / kStages);
-          if (!ok) break;
+          const int sq = g % kStagesQ, so = g % kStagesO, bytes = halves * a.G * a.tq * 128;
           const int row = x.row0 + (tiles.first + i) * a.tq;
-          mbar_expect_tx(&qd_full[st], 2 * halves * a.G * a.tq * 128);
-          load(sQ + st * kTile, &maps.q, &qd_full[st], x.head * a.G, row);
-          load(sdO + st * kTile, &maps.dout, &qd_full[st], x.head * a.G, row);
+          ok = wait(&q_empty[sq], g / kStagesQ);
+          if (!ok) break;
+          mbar_expect_tx(&q_full[sq], bytes);
+          load(sQ + sq * kTile, &maps.q, &q_full[sq], x.head * a.G, row);
+          ok = wait(&o_empty[so], g / kStagesO);
+          if (!ok) {
+            drain_wait(&q_full[sq], (g / kStagesQ) & 1);
+            break;
+          }
+          mbar_expect_tx(&o_full[so], bytes);
+          load(sdO + so * kTile, &maps.dout, &o_full[so], x.head * a.G, row);
         }
       }
       if (!ok) {  // the copies in flight end before the block does
-        for (int k = max(0, g - kStages); k < g; ++k) drain_wait(&qd_full[k % kStages], (k / kStages) & 1);
+        for (int k = max(0, g - kStagesQ); k < g; ++k) drain_wait(&q_full[k % kStagesQ], (k / kStagesQ) & 1);
+        for (int k = max(0, g - kStagesO); k < g; ++k) drain_wait(&o_full[k % kStagesO], (k / kStagesO) & 1);
         if (issued) drain_wait(kv_full, (issued - 1) & 1);
       }
     } else if (warp == 1 || warp == 2) {
@@ -192,6 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
       uint8_t* sG = w ? sQ : sdO;  // B of the gradient
       const Desc ad = sdesc(smem_addr(w ? sV : sK), 16, 1024), sd = sdesc(smem_addr(sS), 16, 1024),
                  gd = sdesc(smem_addr(sG), kHalf, 1024);
+      uint64_t* bs_full = w ? o_full : q_full;
+      uint64_t* bg_full = w ? q_full : o_full;
+      uint64_t* bg_empty = w ? q_empty : o_empty;
+      const uint32_t ns = w ? kStagesO : kStagesQ, ng = w ? kStagesQ : kStagesO;
       uint64_t* score_full = w ? dp_full : s_full;
       uint64_t* mine_full = w ? ds_full : p_full;
       bool ok = true;
@@ -214,33 +277,36 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
         const int left = min(a.tq, x.len - (tiles.first + tiles.n - 1) * a.tq) * a.G;  // rows of the last tile
         auto issue_score = [&](int i) {  // of the item's tile i; the turn passes
           if (elect()) {
-            mma_ss(ts, ad, sd.at((g + i) % kStages * kTile), id_s, ksteps);
+            mma_ss(ts, ad, sd.at((g + i) % ns * kTile), id_s, ksteps);
             mbar_arrive(&turn[1 - w]);
             commit1(score_full);
+            if (w) commit1(&o_empty[(g + i) % ns]);
             if (i + 1 == tiles.n) commit1(kv_free);
           }
         };
-        ok = wait(kv_full, items) && wait(&qd_full[g % kStages], g / kStages) && take_turn();
+        ok = wait(kv_full, items) && wait(&bs_full[g % ns], g / ns) && take_turn();
         if (!ok) break;
         tc_fence_after();
         issue_score(0);
         for (int i = 0; i < tiles.n && ok; ++i) {
-          const uint32_t b = g + i, st = b % kStages;
+          const uint32_t b = g + i, st = b % ng;
           const bool last = i + 1 == tiles.n;
           const int rows = last ? left : a.tq * a.G, steps = (rows + 15) / 16;
-          if (last && left < 16 * steps && left < a.tq * a.G) {  // rows past the sequence's end that the last step reads
+          ok = wait(&bg_full[st], b / ng);
+          if (ok && last && left < 16 * steps && left < a.tq * a.G) {
+            // rows past the sequence's end that the product's last step reads
             zero_rows(sG + st * kTile, left, 16 * steps, halves);
             fence_async_smem();
             __syncwarp();
           }
-          ok = (last || wait(&qd_full[(b + 1) % kStages], (b + 1) / kStages)) && (i > 0 || wait(acc_free, items + 1)) &&
+          ok = ok && (last || wait(&bs_full[(b + 1) % ns], (b + 1) / ns)) && (i > 0 || wait(acc_free, items + 1)) &&
                wait(mine_full, b) && take_turn();
           if (!ok) break;
           tc_fence_after();
           if (elect()) {
             mma_ts(tg, ts, gd.at(st * kTile), id_g, i > 0 ? 1u : 0u, min(4, steps));
             if (steps > 4) mma_ts(tg, ts + 64, gd.at(st * kTile + 4 * 2048), id_g, 1u, steps - 4);
-            commit1(&qd_empty[st]);
+            commit1(&bg_empty[st]);
             if (last) {
               commit1(acc_full);
               mbar_arrive(&turn[1 - w]);
@@ -278,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
             if (tok < a.tq && place < x.len) {
               const long long at = 1LL * (x.row0 + place) * a.Hq + x.head * a.G + (r - tok * a.G);
               l[u] = -a.lse[at] * kLog2e;
-              d[u] = a.D[at];
+              d[u] = -a.D[at];
             }
           }
           ok = warp_wait(&st_empty[st], ((g / kStages) & 1) ^ 1u, abort_flag, a.err, DEV_ERR_TIMEOUT_PRODUCER);
@@ -301,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + 64 * half, tp = ts + kRows, tv = ts + 2 * kRows;
     const float c = a.scale * kLog2e;
-    const uint32_t stage = smem_addr(sOut + (warp - 4) * kStageOut);
     uint32_t g = 0, items = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -339,22 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
           tmem_ld32(ts + 32, p + 32);
           tmem_ld_wait();
           uint32_t w[32];
-          const uint64_t c2 = f2_pack(c, c);
-#pragma unroll
-          for (int u = 0; u < 64; u += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(L + u);
-            f2_unpack(f2_fma(f2_pack(p[u], p[u + 1]), c2, f2_pack(l4.x, l4.y)), p[u], p[u + 1]);
-            f2_unpack(f2_fma(f2_pack(p[u + 2], p[u + 3]), c2, f2_pack(l4.z, l4.w)), p[u + 2], p[u + 3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p[u + e] = ex2_ftz(p[u + e]);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (u + e < from || u + e >= rows) p[u + e] = 0.f;
-            }
-            w[u >> 1] = pack_bf16x2(p[u], p[u + 1]);
-            w[(u >> 1) + 1] = pack_bf16x2(p[u + 2], p[u + 3]);
-          }
+          if (masked) exps<true>(p, L, c, from, rows, w);
+          else exps<false>(p, L, c, from, rows, w);
           tmem_st32u(ts, w);
           tmem_st_wait();
         }
@@ -368,21 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
           tmem_ld32(tp + 32, d + 32);
           tmem_ld_wait();
           uint32_t w[32];
-#pragma unroll
-          for (int u = 0; u < 64; u += 4) {
-            const float4 d4 = *reinterpret_cast<const float4*>(D + u);
-            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
-            float e4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) e4[e] = p[u + e] * (d[u + e] - dv[e]);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (u + e < from || u + e >= rows) e4[e] = 0.f;
-            }
-            w[u >> 1] = pack_bf16x2(e4[0], e4[1]);
-            w[(u >> 1) + 1] = pack_bf16x2(e4[2], e4[3]);
-          }
+          if (masked) grads<true>(p, d, D, from, rows, w);
+          else grads<false>(p, d, D, from, rows, w);
           tmem_st32u(tp, w);
           tmem_st_wait();
         }
@@ -393,38 +431,27 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
       ok = wait(acc_full, items);
       if (!ok) break;
       tc_fence_after();
-      // 32 columns at a time through the warp's staging rows, so that four lanes write 64 bytes of a row.
-      const int ncol = a.dh - 64 * half, nkey = x.len - x.t0;
+      const int ncol = a.dh - 64 * half;
+      const bool valid = row < x.len - x.t0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // dV, dV, dK, dK
         const int h = k & 1;
         const PackedRows& out = k < 2 ? a.dv : a.dk;
         const float f = k < 2 ? 1.f : a.scale;
-        if (32 * h < ncol) {
-          float o[32];
-          tmem_ld32(tv + (k >> 1) * kRows + 32 * h, o);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float* v = o + 8 * u;
-            sts128(stage + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(f * v[0], f * v[1]),
-                   pack_bf16x2(f * v[2], f * v[3]), pack_bf16x2(f * v[4], f * v[5]), pack_bf16x2(f * v[6], f * v[7]));
-          }
-        }
+        float o[32];
+        tmem_ld32(tv + (k >> 1) * kRows + 32 * h, o);
+        tmem_ld_wait();
         if (k == 3) arrive(acc_free);
-        __syncwarp();
-        if (32 * h < ncol) {
-          const int col = 32 * h + 8 * (lane & 3);
+        if (!valid) continue;
+        bf16* to = out.p + (x.row0 + x.t0 + row) * out.ld + 1LL * x.head * a.dh + 64 * half + 32 * h;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = 8 * u + (lane >> 2), key = quarter * 32 + r;
-            uint4 v;
-            umma::lds128(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4), v.x, v.y, v.z, v.w);
-            if (key < nkey && col < ncol)
-              *reinterpret_cast<uint4*>(out.p + (x.row0 + x.t0 + key) * out.ld + 1LL * x.head * a.dh + 64 * half + col) = v;
+        for (int u = 0; u < 4; ++u)
+          if (32 * h + 8 * u < ncol) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = f * o[8 * u + e];
+            store8(to + 8 * u, v);
           }
-        }
-        __syncwarp();
       }
     }
   }
