@@ -185,18 +185,19 @@ struct PdlOff {
 
 // Programmatic dependent launch is on unless the environment sets LR_PDL=0 (read once) or a
 // PdlOff guard is active.
-inline bool pdl_enabled() {
+inline bool pdl_allowed() {
   static const bool on = [] {
     const char* e = getenv("LR_PDL");
     return !(e && e[0] == '0');
   }();
-  return on && pdl_suppressed() == 0;
+  return on;
 }
+inline bool pdl_enabled() { return pdl_allowed() && pdl_suppressed() == 0; }
 
-// Launches kern<<<grid, block, smem, st>>>(args...) with the programmatic-serialisation attribute.
+// Launches kern<<<grid, block, smem, st>>>(args...), with the programmatic-serialisation attribute if `pdl`.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args&&... args) {
+cudaError_t launch_as(bool pdl, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      Args&&... args) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
@@ -207,10 +208,16 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  cfg.numAttrs = pdl ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+// The same with the attribute wherever it is on.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  return launch_as(pdl_enabled(), kern, grid, block, smem, st, std::forward<Args>(args)...);
 }
 
 }  // namespace lr

@@ -19,15 +19,14 @@
 //
 // Q_i is needed from S^T of tile i to dK of tile i, four turns, and dO_i from dP^T to dV, two; so Q has three stages and dO
 // two (with two of both, loads came 600 cycles late for each tile).  That leaves 3 KB of shared memory: dK and dV are
-// written straight from registers, and the tiles begin at the start of the block's shared memory, whose alignment is
-// checked.
+// written straight from registers.
 //
 // Warps: 0 takes the items and loads them by TMA (K, V per item; Q_i, dO_i into their rings), 1 issuer of S^T
 // and dV, which also allocates TMEM, 2 issuer of dP^T and dK, 3 loads lse and D of each tile, 4-11 element-wise and output
 // (warp group h takes rows 64 h .. 64 h + 63 of a tile and columns 64 h .. of dK and dV).  TMEM: S^T at column 0, dP^T at
 // 128, dV at 256, dK at 384.  Every wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is
 // freed).
-#include <algorithm>
+#pragma once
 
 #include "packed_device.cuh"
 
@@ -39,20 +38,6 @@ constexpr int kStagesQ = 3, kStagesO = 2;
 constexpr int kStages = 2;  // of lse and D
 constexpr int kSmem = (2 + kStagesQ + kStagesO) * kTile + kStages * 2 * kRows * 4 + 512;
 static_assert(kSmem <= umma::kMaxSmem, "shared memory");
-
-struct Maps {
-  CUtensorMap q, dout, k, v;
-};
-
-struct Args {
-  PackedRows dk, dv;
-  const float *lse, *D;
-  float scale;
-  int Hq, dh, G, tq;
-  unsigned magic;
-  Taken taken;
-  unsigned* err;
-};
 
 // The row tiles of an item's key block.
 struct Tiles {
@@ -99,12 +84,9 @@ __device__ __forceinline__ void grads(const float* p, const float* d, const floa
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_constant__ Maps maps, const Args a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_addr(smem) & 1023u) {  // the swizzled tiles need it
-    if (threadIdx.x == 0) atomicOr(a.err, DEV_ERR_TMEM);
-    return;
-  }
+// One of `nblocks` blocks, the `block`-th.
+__device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsigned block, unsigned nblocks,
+                                     uint8_t* smem) {
   uint8_t* sK = smem;
   uint8_t* sV = sK + kTile;
   uint8_t* sQ = sV + kTile;               // [kStagesQ]
@@ -202,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
         for (int h = 0; h < halves; ++h) tma_load_3d(dst + h * kHalf, map, bar, 64 * h, head, row);
       };
-      unsigned t = blockIdx.x;
+      unsigned t = block;
       for (int it = 0; ok; ++it) {
         const int4 v = a.taken.item(t);
         const int slot = it % kItems;
@@ -220,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
         load(sV, &maps.v, kv_full, x.head, x.row0 + x.t0);
         ++issued;
         for (int i = 0; i < tiles.n && ok; ++i, ++g) {
-          if (i == max(0, tiles.n - 2)) t = gridDim.x + atomicAdd(a.taken.next, 1u);  // late: see the forward
+          if (i == max(0, tiles.n - 2)) t = nblocks + atomicAdd(a.taken.next, 1u);  // late: see the forward
           const int sq = g % kStagesQ, so = g % kStagesO, bytes = halves * a.G * a.tq * 128;
           const int row = x.row0 + (tiles.first + i) * a.tq;
           ok = wait(&q_empty[sq], g / kStagesQ);
@@ -465,23 +447,5 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dkv_kernel(const __grid_co
 }
 
 }  // namespace dkv
-
-cudaError_t launch_packed_dkv(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st) {
-  using namespace dkv;
-  cudaError_t e = configure<packed_dkv_kernel, kSmem>();
-  if (e != cudaSuccess) return e;
-  const int G = p.Hq / p.Hk, tq = kRows / G;
-  dkv::Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  if (!encode_heads(&maps.q, p.q, p.T, p.Hq, p.dh, G, tq) || !encode_heads(&maps.dout, p.dout, p.T, p.Hq, p.dh, G, tq) ||
-      !encode_heads(&maps.k, p.k, p.T, p.Hk, p.dh, 1, kRows) || !encode_heads(&maps.v, p.v, p.T, p.Hk, p.dh, 1, kRows))
-    return cudaErrorInvalidValue;
-  const dkv::Args a{p.dk, p.dv, p.lse, D, p.scale, p.Hq, p.dh, G, tq, group_magic(G),
-                    taken(plan, p.Hk, 4LL * p.T * G * p.dh), err};
-  const long long items = plan_capacity(p.T, p.nseq, kRows) * p.Hk;
-  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
-  return launch_pdl(packed_dkv_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
-}
-
 }  // namespace packed
 }  // namespace lr

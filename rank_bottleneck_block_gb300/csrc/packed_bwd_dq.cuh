@@ -22,7 +22,7 @@
 // S and dQ, which also allocates TMEM, 2 issuer of dP, 3 idle, 4-11 element-wise and output (warp group h takes keys
 // 64 h .. 64 h + 63 of a block and columns 64 h .. of dQ).  TMEM: S at columns 0 and 128, dP at 256, dQ at 384.  Every
 // wait is bounded (error word, abort flag; each role drains what it issued, and TMEM is freed).
-#include <algorithm>
+#pragma once
 
 #include "packed_device.cuh"
 
@@ -31,26 +31,12 @@ namespace packed {
 namespace dq {
 
 constexpr int kStagesK = 3, kStagesV = 2;
-constexpr int kSmem = 1024 + (2 + kStagesK + kStagesV) * kTile + 512;
+constexpr int kSmem = (2 + kStagesK + kStagesV) * kTile + 512;
 static_assert(kSmem <= umma::kMaxSmem, "shared memory");
 
-struct Maps {
-  CUtensorMap q, dout, k, v;
-};
-
-struct Args {
-  PackedRows dq;
-  const float *lse, *D;
-  float scale;
-  int Hq, dh, G, tq;
-  unsigned magic;
-  Taken taken;
-  unsigned* err;
-};
-
-__global__ void __launch_bounds__(kThreads, 1) packed_dq_kernel(const __grid_constant__ Maps maps, const Args a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+// One of `nblocks` blocks, the `block`-th.
+__device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsigned block, unsigned nblocks,
+                                     uint8_t* smem) {
   uint8_t* sQ = smem;
   uint8_t* sdO = sQ + kTile;
   uint8_t* sK = sdO + kTile;          // [kStagesK]
@@ -138,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dq_kernel(const __grid_con
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head, int row) {
         for (int h = 0; h < halves; ++h) tma_load_3d(dst + h * kHalf, map, bar, 64 * h, head, row);
       };
-      unsigned t = blockIdx.x;
+      unsigned t = block;
       for (int it = 0; ok; ++it) {
         const int4 v = a.taken.item(t);
         const int slot = it % kItems;
@@ -156,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dq_kernel(const __grid_con
         load(sdO, &maps.dout, qd_full, x.head * a.G, row);
         ++q_issued;
         for (int j = 0; j < n && ok; ++j, ++g) {
-          if (j == max(0, n - 2)) t = gridDim.x + atomicAdd(a.taken.next, 1u);  // late: see the forward
+          if (j == max(0, n - 2)) t = nblocks + atomicAdd(a.taken.next, 1u);  // late: see the forward
           const int sk = g % kStagesK, sv = g % kStagesV;
           ok = wait(&k_empty[sk], g / kStagesK);
           if (!ok) break;
@@ -397,23 +383,5 @@ __global__ void __launch_bounds__(kThreads, 1) packed_dq_kernel(const __grid_con
 }
 
 }  // namespace dq
-
-cudaError_t launch_packed_dq(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st) {
-  using namespace dq;
-  cudaError_t e = configure<packed_dq_kernel, kSmem>();
-  if (e != cudaSuccess) return e;
-  const int G = p.Hq / p.Hk, tq = kRows / G;
-  dq::Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  if (!encode_heads(&maps.q, p.q, p.T, p.Hq, p.dh, G, tq) || !encode_heads(&maps.dout, p.dout, p.T, p.Hq, p.dh, G, tq) ||
-      !encode_heads(&maps.k, p.k, p.T, p.Hk, p.dh, 1, kRows) || !encode_heads(&maps.v, p.v, p.T, p.Hk, p.dh, 1, kRows))
-    return cudaErrorInvalidValue;
-  const dq::Args a{p.dq, p.lse, D, p.scale, p.Hq, p.dh, G, tq, group_magic(G),
-                   taken(plan, p.Hk, 4LL * p.T * p.dh), err};
-  const long long items = plan_capacity(p.T, p.nseq, tq) * p.Hk;
-  const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
-  return launch_pdl(packed_dq_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
-}
-
 }  // namespace packed
 }  // namespace lr

@@ -39,7 +39,8 @@ struct PlanJob {
   int tokens;
   int work;  // +1: a block's work grows with its place (its keys), -1: with what follows it (its queries)
 };
-// One launch: the lists, and (D not null) D[t, h] = dout.o of every row and head.
+// One launch: the lists, and (D not null) D[t, h] = dout.o of every row and head.  It starts when everything before it has
+// ended, and lets the launch that follows it begin at once (that one waits for it before its first access).
 cudaError_t launch_prepare(const PackedArgs& a, const PlanJob* jobs, int njobs, float* D, unsigned* err, cudaStream_t st);
 
 // What an item needs, from its ring slot.
@@ -99,8 +100,30 @@ cudaError_t configure() {
   return cudaSuccess;
 }
 
-cudaError_t launch_packed_dq(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st);
-cudaError_t launch_packed_dkv(const PackedArgs& p, const float* D, const Plan& plan, unsigned* err, cudaStream_t st);
+// The tensor maps of the backward's kernels.
+struct BwdMaps {
+  CUtensorMap q, dout, k, v;
+};
+
+struct DqArgs {
+  PackedRows dq;
+  const float *lse, *D;
+  float scale;
+  int Hq, dh, G, tq;
+  unsigned magic;
+  Taken taken;
+  unsigned* err;
+};
+
+struct DkvArgs {
+  PackedRows dk, dv;
+  const float *lse, *D;
+  float scale;
+  int Hq, dh, G, tq;
+  unsigned magic;
+  Taken taken;
+  unsigned* err;
+};
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(

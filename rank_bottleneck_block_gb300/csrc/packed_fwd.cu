@@ -443,7 +443,7 @@ cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err,
   const fwd::Args a{p.o, p.lse, p.scale, p.Hq, p.dh, G, tq, group_magic(G), taken(job.plan, p.Hk, 4LL * p.T * p.dh), err};
   const long long items = plan_capacity(p.T, p.nseq, 2 * tq) * p.Hk;
   const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
-  return launch_pdl(packed_fwd_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
+  return launch_as(pdl_allowed(), packed_fwd_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);
 }
 
 }  // namespace lr

@@ -113,17 +113,21 @@ struct Jobs {
 
 // D of four consecutive (row, head) for each group of `lanes` lanes.
 __device__ __forceinline__ void row_dots(const PackedArgs& a, float* D, int block, int lanes) {
-  const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes, c = 8 * lane;
-  const long long first = (1LL * block * (kThreads / lanes) + group) * 4, all = 1LL * a.T * a.Hq;
+  const int shift = lanes == 16 ? 4 : 3, group = threadIdx.x >> shift, lane = threadIdx.x & (lanes - 1), c = 8 * lane;
+  const unsigned first = (static_cast<unsigned>(block) * (kThreads >> shift) + group) * 4, all = 1u * a.T * a.Hq;
+  unsigned t = first / a.Hq, h = first - t * a.Hq;
   uint4 x[4], y[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const long long id = first + u;
     x[u] = y[u] = make_uint4(0, 0, 0, 0);
-    if (id < all && c < a.dh) {
-      const long long t = id / a.Hq, col = (id - t * a.Hq) * a.dh + c;
+    if (first + u < all && c < a.dh) {
+      const int col = static_cast<int>(h) * a.dh + c;
       x[u] = *reinterpret_cast<const uint4*>(a.o.p + t * a.o.ld + col);
       y[u] = *reinterpret_cast<const uint4*>(a.dout.p + t * a.dout.ld + col);
+    }
+    if (++h == static_cast<unsigned>(a.Hq)) {
+      h = 0;
+      ++t;
     }
   }
 #pragma unroll
@@ -141,6 +145,7 @@ __device__ __forceinline__ void row_dots(const PackedArgs& a, float* D, int bloc
 __global__ void __launch_bounds__(kThreads) prepare_kernel(PackedArgs a, Jobs jobs, int njobs, float* D, int lanes,
                                                            unsigned* err) {
   pdl_wait();
+  pdl_trigger();
   const int b = static_cast<int>(blockIdx.x);
   if (b < njobs) {
     const PlanJob j = b == 0 ? jobs.job[0] : jobs.job[1];
@@ -174,8 +179,8 @@ cudaError_t launch_prepare(const PackedArgs& a, const PlanJob* jobs, int njobs, 
   for (int i = 0; i < njobs; ++i) j.job[i] = jobs[i];
   const int lanes = a.dh > 64 ? 16 : 8;
   const long long each = kThreads / lanes * 4, dots = D ? (1LL * a.T * a.Hq + each - 1) / each : 0;
-  return launch_pdl(prepare_kernel, dim3(static_cast<unsigned>(njobs + dots)), dim3(kThreads), 0, st, a, j, njobs, D, lanes,
-                    err);
+  return launch_as(false, prepare_kernel, dim3(static_cast<unsigned>(njobs + dots)), dim3(kThreads), 0, st, a, j, njobs, D,
+                   lanes, err);
 }
 
 }  // namespace packed
