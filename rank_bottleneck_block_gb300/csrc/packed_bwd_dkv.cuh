@@ -288,13 +288,13 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
           if (elect()) {
             mma_ts(tg, ts, gd.at(st * kTile), id_g, i > 0 ? 1u : 0u, min(4, steps));
             if (steps > 4) mma_ts(tg, ts + 64, gd.at(st * kTile + 4 * 2048), id_g, 1u, steps - 4);
-            commit1(&bg_empty[st]);
             if (last) {
-              commit1(acc_full);
               mbar_arrive(&turn[1 - w]);
+              commit1(acc_full);
             }
           }
           if (!last) issue_score(i + 1);
+          if (elect()) commit1(&bg_empty[st]);  // behind the turn: a commit takes its issuer some 100 cycles
         }
         g += tiles.n;
       }

@@ -321,12 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
             tc_fence_after();
             if (elect()) mma_ts(to, ts + 32, v.at(4 * 2048), id_o, 1u, steps - 4);
           }
-          if (elect()) {
-            commit1(v_empty);
-            if (j + 1 == n) commit1(&o_last[t]);
+          if (j + 1 < n) {
+            issue_s(j + 1, b + 1);
+          } else if (elect()) {
+            mbar_arrive(&turn[1 - t]);
+            commit1(&o_last[t]);
           }
-          if (j + 1 < n) issue_s(j + 1, b + 1);
-          else pass_turn();
+          if (elect()) commit1(v_empty);  // behind the turn: a commit takes its issuer some 100 cycles
         }
         if (n > 0) ++items;
       }
