@@ -137,9 +137,9 @@ __device__ __forceinline__ void finish(const LogprobFwd& a, int t, Part p, float
 
 // The largest of a warp's values; a NaN counts as the largest.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 template <typename ST, bool TOP>

@@ -2676,7 +2676,7 @@ size_t lr_packed_attn_fwd_workspace_bytes(const lr_packed_shape* sh) {
 size_t lr_packed_attn_bwd_workspace_bytes(const lr_packed_shape* sh) {
   t_last_error.clear();
   if (check_packed(LR_BF16, sh)) return 0;
-  return packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk);
+  return packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk, sh->dh);
 }
 
 lr_status lr_packed_attn_fwd(lr_dtype dt, const lr_packed_shape* sh, float scale, const int* offs, const void* q,
@@ -2707,7 +2707,7 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
   LR_TRY(check_rows(dq, lddq, sh->Hq, sh->dh, "dq"));
   LR_TRY(check_rows(dk, lddk, sh->Hk, sh->dh, "dk"));
   LR_TRY(check_rows(dv, lddv, sh->Hk, sh->dh, "dv"));
-  LR_TRY(check_size(ws_bytes, packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk), "ws"));
+  LR_TRY(check_size(ws_bytes, packed_attn_bwd_ws_bytes(sh->T, sh->nseq, sh->Hq, sh->Hk, sh->dh), "ws"));
   Ctx c;
   LR_TRY(make_ctx(dt, stream, &c));
   PdlOff serial;  // see lr_block_fwd

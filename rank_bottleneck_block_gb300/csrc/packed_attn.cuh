@@ -27,7 +27,7 @@ struct PackedArgs {
 };
 
 size_t packed_attn_fwd_ws_bytes(int T, int nseq, int Hq, int Hk);
-size_t packed_attn_bwd_ws_bytes(int T, int nseq, int Hq, int Hk);
+size_t packed_attn_bwd_ws_bytes(int T, int nseq, int Hq, int Hk, int dh);
 cudaError_t launch_packed_attn_fwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st);
 cudaError_t launch_packed_attn_bwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st);
 

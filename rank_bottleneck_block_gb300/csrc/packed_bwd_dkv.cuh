@@ -9,6 +9,9 @@
 //   dS^T = P^T (dP^T - D)               the same over those of dP^T
 //   dV += P^T dO_i, dK += dS^T Q_i      MMA with A from TMEM; dK takes the scale at the end
 //
+// Where there are few items, each is cut in parts of its row tiles, whose sums a further launch adds up in order
+// (one sequence of 1024 tokens, 32 over 8 heads: 64 items, of which the first had 32 tiles).
+//
 // The heads of a group add up in the same accumulators, in a fixed order.  TMEM is full (S^T, dP^T, dV and dK, 128
 // columns each), so S^T and dP^T have one buffer; what keeps the tensor cores at work is that they belong to two chains:
 // one issuer takes dV of tile i and then S^T of tile i + 1, the other dK of tile i and then dP^T of tile i + 1, by
@@ -39,10 +42,17 @@ constexpr int kStages = 2;  // of lse and D
 constexpr int kSmem = (2 + kStagesQ + kStagesO) * kTile + kStages * 2 * kRows * 4 + 512;
 static_assert(kSmem <= umma::kMaxSmem, "shared memory");
 
-// The row tiles of an item's key block.
+// An item's part of the row tiles of its key block; the head is taken out of the item's last word.
 struct Tiles {
-  int first, n;
-  __device__ __forceinline__ Tiles(const Item& x, int tq) : first(x.t0 / tq), n((x.len + tq - 1) / tq - first) {}
+  int first, n, part;
+  __device__ __forceinline__ Tiles(Item& x, int tq, int parts) {
+    part = x.head >> 24;
+    x.head &= 0xffffff;
+    first = x.t0 / tq;
+    const int all = (x.len + tq - 1) / tq - first, from = all * part / parts;
+    n = all * (part + 1) / parts - from;
+    first += from;
+  }
 };
 
 // P of 64 rows (L: -lse log2 e of them) of one key from its scores, in place, and packed.  MASK: rows before `from` or from
@@ -193,8 +203,12 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
         sitem[slot] = v;
         mbar_arrive(&item_full[slot]);  // release: the readers see the item
         if (v.w < 0) break;
-        const Item x{v.x, v.y, v.z, v.w};
-        const Tiles tiles(x, a.tq);
+        Item x{v.x, v.y, v.z, v.w};
+        const Tiles tiles(x, a.tq, a.taken.parts);
+        if (tiles.n == 0) {
+          t = nblocks + atomicAdd(a.taken.next, 1u);
+          continue;
+        }
         ok = wait(kv_free, issued);
         if (!ok) break;
         mbar_expect_tx(kv_full, 2 * halves * kHalf);
@@ -248,14 +262,15 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
         ++turns;
         return wait(&turn[w], w ? turns + 1 : turns);
       };
-      for (int it = 0; ok; ++it, ++items) {
+      for (int it = 0; ok; ++it) {
         Item x;
         ok = __all_sync(0xffffffffu, next_item(it, x));
         if (!ok) break;
         x = Item{uniform(x.row0), uniform(x.len), uniform(x.t0), uniform(x.head)};
         if (elect()) mbar_arrive(&item_empty[it % kItems]);
         if (x.head < 0) break;
-        const Tiles tiles(x, a.tq);
+        const Tiles tiles(x, a.tq, a.taken.parts);
+        if (tiles.n == 0) continue;
         const int left = min(a.tq, x.len - (tiles.first + tiles.n - 1) * a.tq) * a.G;  // rows of the last tile
         auto issue_score = [&](int i) {  // of the item's tile i; the turn passes
           if (elect()) {
@@ -297,6 +312,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
           if (elect()) commit1(&bg_empty[st]);  // behind the turn: a commit takes its issuer some 100 cycles
         }
         g += tiles.n;
+        ++items;
       }
       if (elect()) {
         commit1(&drain[w]);  // every MMA issued here is complete once this flips
@@ -314,7 +330,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[it % kItems]);
         if (x.head < 0) break;
-        const Tiles tiles(x, a.tq);
+        const Tiles tiles(x, a.tq, a.taken.parts);
         for (int i = 0; i < tiles.n && ok; ++i, ++g) {
           const int st = g % kStages, t0 = (tiles.first + i) * a.tq;
           float l[4], d[4];
@@ -359,14 +375,14 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    for (int it = 0; ok; ++it, ++items) {
+    for (int it = 0; ok; ++it) {
       Item x;
       ok = __all_sync(0xffffffffu, next_item(it, x));
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&item_empty[it % kItems]);
       if (x.head < 0) break;
-      const Tiles tiles(x, a.tq);
+      const Tiles tiles(x, a.tq, a.taken.parts);
       for (int i = 0; i < tiles.n; ++i, ++g) {
         const int st = g % kStages, t0 = (tiles.first + i) * a.tq;
         const int rows = min(a.tq, x.len - t0) * a.G - 64 * half;  // of the tile, from this thread's first
@@ -410,29 +426,39 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
         if (lane == 0) mbar_arrive(&st_empty[st]);
       }
       if (!ok) break;
-      ok = wait(acc_full, items);
-      if (!ok) break;
-      tc_fence_after();
       const int ncol = a.dh - 64 * half;
       const bool valid = row < x.len - x.t0;
+      const long long key = x.row0 + x.t0 + row;
+      if (tiles.n > 0) {
+        ok = wait(acc_full, items++);
+        if (!ok) break;
+        tc_fence_after();
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // dV, dV, dK, dK
         const int h = k & 1;
-        const PackedRows& out = k < 2 ? a.dv : a.dk;
         const float f = k < 2 ? 1.f : a.scale;
         float o[32];
-        tmem_ld32(tv + (k >> 1) * kRows + 32 * h, o);
-        tmem_ld_wait();
-        if (k == 3) arrive(acc_free);
+        if (tiles.n > 0) {
+          tmem_ld32(tv + (k >> 1) * kRows + 32 * h, o);
+          tmem_ld_wait();
+          if (k == 3) arrive(acc_free);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0.f;
+        }
         if (!valid) continue;
-        bf16* to = out.p + (x.row0 + x.t0 + row) * out.ld + 1LL * x.head * a.dh + 64 * half + 32 * h;
+        const PackedRows& out = k < 2 ? a.dv : a.dk;
+        bf16* to = out.p + key * out.ld + 1LL * x.head * a.dh + 64 * half + 32 * h;
+        float* part = (k < 2 ? a.part_dv : a.part_dk) + ((1LL * tiles.part * a.T + key) * a.Hk + x.head) * a.dh + 64 * half + 32 * h;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           if (32 * h + 8 * u < ncol) {
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = f * o[8 * u + e];
-            store8(to + 8 * u, v);
+            if (a.taken.parts > 1) store8(part + 8 * u, v);
+            else store8(to + 8 * u, v);
           }
       }
     }

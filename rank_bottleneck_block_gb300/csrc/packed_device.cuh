@@ -61,19 +61,21 @@ struct Taken {
   const int4* blocks;
   unsigned* next;
   int heads, group;  // key heads, and how many are worked on together
-  // The t-th: an Item, its head negative past the end.
+  int parts;         // an item is this many: each with a part of what it has to go through
+  // The t-th: an Item, its head negative past the end, its part in the bits above the head's 24.
   __device__ __forceinline__ int4 item(unsigned t) const {
-    const unsigned n = static_cast<unsigned>(*nblocks);
+    const unsigned n = static_cast<unsigned>(*nblocks), part = parts > 1 ? t % parts : 0;
+    if (parts > 1) t /= parts;
     if (t >= n * heads) return make_int4(0, 0, 0, -1);
     const unsigned per = group * n, gi = t / per, r = t - gi * per;
     const unsigned gh = min(group, heads - static_cast<int>(gi) * group);
     int4 v = blocks[r / gh];
-    v.w = static_cast<int>(gi * group + r % gh);
+    v.w = static_cast<int>(gi * group + r % gh + (part << 24));
     return v;
   }
 };
-inline Taken taken(const Plan& plan, int heads, long long bytes_per_head) {
-  return Taken{plan.nblocks, plan.blocks, plan.next, heads, heads_per_group(heads, bytes_per_head)};
+inline Taken taken(const Plan& plan, int heads, long long bytes_per_head, int parts = 1) {
+  return Taken{plan.nblocks, plan.blocks, plan.next, heads, heads_per_group(heads, bytes_per_head), parts};
 }
 
 // Registers a thread of the kernels of 12 warps: the launch gives 168; the first four warps keep 88, the others take 208
@@ -117,6 +119,8 @@ struct DqArgs {
 
 struct DkvArgs {
   PackedRows dk, dv;
+  float *part_dk, *part_dv;  // more than one part: their sums, [parts, T, Hk, dh]
+  int T, Hk;
   const float *lse, *D;
   float scale;
   int Hq, dh, G, tq;

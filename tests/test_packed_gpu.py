@@ -114,6 +114,10 @@ CASES = [  # lengths, Hq, Hk, dh, rows in front, rows behind
     ([257, 255], 2, 2, 88, 0, 0),
     ([64, 192, 320], 12, 4, 48, 0, 64),
     ([385], 4, 4, 32, 0, 0),
+    ([1024], 8, 2, 128, 0, 0),                  # few key blocks with many queries each: dK and dV in parts
+    ([600, 20, 0, 410], 4, 1, 64, 3, 5),
+    ([777], 5, 1, 72, 0, 0),
+    ([1500, 4], 16, 1, 40, 0, 2),
 ]
 
 
