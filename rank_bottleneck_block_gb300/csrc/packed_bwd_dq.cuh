@@ -51,11 +51,11 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
   uint64_t* s_full = bars + 12;   // [2]
   uint64_t* dp_full = bars + 14;
   uint64_t* dp_free = bars + 15;  // dP is in registers
-  uint64_t* ds_full = bars + 16;
-  uint64_t* dq_last = bars + 17;  // the item's last product is complete
+  uint64_t* ds_full = bars + 16;  // [2], as S: the element-wise warps can be a block ahead of the product
+  uint64_t* dq_last = bars + 20;  // the item's last product is complete
   uint64_t* dq_free = bars + 18;  // dQ has been read
-  uint64_t* drain = bars + 19;    // [2]
-  uint64_t* item_full = bars + 22;            // [kItems]
+  uint64_t* drain = bars + 21;    // [2]
+  uint64_t* item_full = bars + 24;            // [kItems]
   uint64_t* item_empty = item_full + kItems;  // [kItems]
   int4* sitem = reinterpret_cast<int4*>(item_empty + kItems);  // [kItems], 16-byte aligned
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sitem + kItems);
@@ -75,11 +75,11 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
+      mbar_init(&ds_full[i], 8);
       mbar_init(&drain[i], 1);
     }
     mbar_init(dp_full, 1);
     mbar_init(dp_free, 8);
-    mbar_init(ds_full, 8);
     mbar_init(dq_last, 1);
     mbar_init(dq_free, 8);
     for (int i = 0; i < kItems; ++i) {
@@ -197,7 +197,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t b = g + j, st = b % kStagesK;
           const int steps = j + 1 < n ? 8 : (last + 15) / 16, left = x.len - j * kRows;
-          ok = (j > 0 || wait(dq_free, items + 1)) && wait(ds_full, b);
+          ok = (j > 0 || wait(dq_free, items + 1)) && wait(&ds_full[b & 1], b >> 1);
           if (!ok) break;
           if (left < 16 * steps) {  // rows past the sequence's end that the product's last step reads
             zero_rows(sK + st * kTile, left, 16 * steps, halves);
@@ -346,7 +346,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
         } else {
           arrive(dp_free);
         }
-        arrive(ds_full);
+        arrive(&ds_full[g & 1]);
       }
       if (!ok) break;
       ok = wait(dq_last, items);

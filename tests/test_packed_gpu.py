@@ -250,6 +250,23 @@ def test_same_bits_every_time_and_in_a_graph():
     _check(shape, new, run)
 
 
+def test_many_calls_give_the_same_bits():
+    """Blocks that wait for slow loads beside others that do not: every call ends, and with the same gradients."""
+    shape = _shape([2048], 32, 8, 128)
+    case = I.make_packed_case(shape, [2048], seed=14, device="cuda")
+    run = _make(shape, case)
+    run.step()
+    _ok()
+    keep = {n: getattr(run, n).clone() for n in ROWS + ("lse",)}
+    for i in range(3000):
+        run.step()
+        if i % 300 == 0:
+            _ok()
+            assert all(torch.equal(getattr(run, n), t) for n, t in keep.items())
+    _ok()
+    assert all(torch.equal(getattr(run, n), t) for n, t in keep.items())
+
+
 def test_two_calls_on_two_streams():
     cases = []
     for i, lengths in enumerate(([300, 211], [64] * 7)):
