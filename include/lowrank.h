@@ -321,7 +321,10 @@ lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const 
  * softmax statistics, O, dQ, dK and dV are fp32 until they are rounded once.
  * Offsets live on the device and are read there: if they are not in order or leave the
  * rows, the call writes no result and lr_check_device_error reports LR_ERR_SHAPE.
- * Launched without programmatic dependent launch, as lr_attn_*.
+ * The workspace holds the list of work items, D and, in the backward of few and long
+ * sequences, partial sums of dK and dV (20 MB at most).  A call's first kernel starts when
+ * everything before it has ended (no programmatic dependent launch, as lr_attn_*); the
+ * second starts under it.
  */
 typedef struct {
   int T, nseq;

@@ -2691,7 +2691,9 @@ lr_status lr_packed_attn_fwd(lr_dtype dt, const lr_packed_shape* sh, float scale
   const PackedArgs a = packed_args(*sh, scale, offs, q, ldq, k, ldk, v, ldv, o, ldo, lse);
   const double rows = 2.0 * sh->T * sh->dh;
   LaunchScope scope("packed_attn_fwd", c.st, 0, rows * (2.0 * sh->Hq + 2.0 * sh->Hk));
-  cudaError_t e = launch_packed_attn_fwd(a, ws, c.err, c.st);
+  int launches = 1;
+  cudaError_t e = launch_packed_attn_fwd(a, ws, c.err, c.st, &launches);
+  s_launches.fetch_add(launches - 1, std::memory_order_relaxed);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "packed attention: %s", cudaGetErrorString(e));
   return LR_OK;
 }
@@ -2718,7 +2720,9 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
   a.dv = packed_rows(dv, lddv);
   const double rows = 2.0 * sh->T * sh->dh;
   LaunchScope scope("packed_attn_bwd", c.st, 0, rows * (4.0 * sh->Hq + 4.0 * sh->Hk));
-  cudaError_t e = launch_packed_attn_bwd(a, ws, c.err, c.st);
+  int launches = 1;
+  cudaError_t e = launch_packed_attn_bwd(a, ws, c.err, c.st, &launches);
+  s_launches.fetch_add(launches - 1, std::memory_order_relaxed);
   if (e != cudaSuccess) return fail(LR_ERR_CUDA, "packed attention backward: %s", cudaGetErrorString(e));
   return LR_OK;
 }

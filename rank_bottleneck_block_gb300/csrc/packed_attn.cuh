@@ -28,7 +28,8 @@ struct PackedArgs {
 
 size_t packed_attn_fwd_ws_bytes(int T, int nseq, int Hq, int Hk);
 size_t packed_attn_bwd_ws_bytes(int T, int nseq, int Hq, int Hk, int dh);
-cudaError_t launch_packed_attn_fwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st);
-cudaError_t launch_packed_attn_bwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st);
+// launches: the kernels that were launched.
+cudaError_t launch_packed_attn_fwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st, int* launches);
+cudaError_t launch_packed_attn_bwd(const PackedArgs& a, void* ws, unsigned* err, cudaStream_t st, int* launches);
 
 }  // namespace lr

@@ -94,7 +94,7 @@ size_t packed_attn_bwd_ws_bytes(int T, int nseq, int Hq, int Hk, int dh) {
   return packed::bwd_layout(T, nseq, Hq, Hk, dh, nullptr, nullptr);
 }
 
-cudaError_t launch_packed_attn_bwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st) {
+cudaError_t launch_packed_attn_bwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st, int* launches) {
   using namespace packed;
   cudaError_t e = configure<packed_bwd_kernel, kSmem>();
   if (e != cudaSuccess) return e;
@@ -117,6 +117,7 @@ cudaError_t launch_packed_attn_bwd(const PackedArgs& p, void* ws, unsigned* err,
   e = launch_prepare(p, w.jobs, 2, w.D, err, st);
   if (e != cudaSuccess) return e;
   e = launch_as(pdl_allowed(), packed_bwd_kernel, dim3(na + nb), dim3(kThreads), kSmem, st, maps, a, b, na);
+  *launches = w.parts == 1 ? 2 : 3;
   if (e != cudaSuccess || w.parts == 1) return e;
   const long long threads = 1LL * p.T * p.Hk * (p.dh / 8);
   return launch_as(pdl_allowed(), packed_join_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st,

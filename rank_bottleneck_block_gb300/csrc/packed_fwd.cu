@@ -426,7 +426,7 @@ size_t packed_attn_fwd_ws_bytes(int T, int nseq, int Hq, int Hk) {
   return packed::plan_layout(T, nseq, 2 * (packed::kRows / (Hq / Hk)), nullptr, nullptr);
 }
 
-cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st) {
+cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err, cudaStream_t st, int* launches) {
   using namespace packed;
   using namespace packed::fwd;
   cudaError_t e = configure<packed_fwd_kernel, kSmem>();
@@ -442,6 +442,7 @@ cudaError_t launch_packed_attn_fwd(const PackedArgs& p, void* ws, unsigned* err,
   e = launch_prepare(p, &job, 1, nullptr, err, st);
   if (e != cudaSuccess) return e;
   const fwd::Args a{p.o, p.lse, p.scale, p.Hq, p.dh, G, tq, group_magic(G), taken(job.plan, p.Hk, 4LL * p.T * p.dh), err};
+  *launches = 2;
   const long long items = plan_capacity(p.T, p.nseq, 2 * tq) * p.Hk;
   const int grid = static_cast<int>(std::min<long long>(items, device_sm_count()));
   return launch_as(pdl_allowed(), packed_fwd_kernel, dim3(grid), dim3(kThreads), kSmem, st, maps, a);

@@ -267,6 +267,55 @@ def test_many_calls_give_the_same_bits():
     assert all(torch.equal(getattr(run, n), t) for n, t in keep.items())
 
 
+@pytest.mark.parametrize("lengths,Hq,Hk,back", [([40], 4, 1, 2), ([1024], 8, 2, 3), ([300] * 60, 8, 8, 2)])
+def test_launches_are_counted(lengths, Hq, Hk, back):
+    """The list and the attention; the sums of dK and dV where their key blocks are cut in parts."""
+    from rank_bottleneck_block_gb300 import lowrank as L
+
+    shape = _shape(lengths, Hq, Hk, 64)
+    run = _make(shape, I.make_packed_case(shape, lengths, seed=15))
+    for call, want in ((run.forward, 2), (run.backward, back)):
+        before = L.lr_launch_count()
+        call()
+        assert L.lr_launch_count() - before == want
+    _ok()
+
+
+def test_two_graphs_with_one_workspace():
+    """Captured calls whose workspaces are the same memory, replayed one after another in any order."""
+    from rank_bottleneck_block_gb300.runner import GraphStep
+
+    runs = []
+    for i, lengths in enumerate(([300, 211, 0, 514], [1, 64, 900, 60])):
+        shape = _shape(lengths, 4, 2, 128)
+        case = I.make_packed_case(shape, lengths, seed=40 + i)
+        runs.append((shape, case, _make(shape, case)))
+    first, second = runs[0][2], runs[1][2]
+    second.ws, second.ws_b = first.ws, first.ws_b
+    graphs = [GraphStep(run.step) for _, _, run in runs]
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1, 0)):
+        for _, _, run in runs:
+            for n in ROWS + ("lse",):
+                getattr(run, n).fill_(7.0)
+        for i in order:
+            graphs[i]()
+        for shape, case, run in runs:
+            _check(shape, case, run)
+
+
+@pytest.mark.parametrize("Hq,Hk,dh", [(2, 1, 64), (12, 4, 128)])
+def test_thousands_of_sequences(Hq, Hk, dh):
+    """More sequences than the list's kernel has threads, most of them empty or of one token."""
+    rng = np.random.default_rng(3)
+    lengths = rng.choice([0, 0, 0, 1, 1, 2, 5], size=5000).tolist()
+    lengths[4321] = 333
+    shape = _shape(lengths, Hq, Hk, dh, 4)
+    case = I.make_packed_case(shape, lengths, seed=16, first=1)
+    run = _make(shape, case)
+    run.step()
+    _check(shape, case, run)
+
+
 def test_two_calls_on_two_streams():
     cases = []
     for i, lengths in enumerate(([300, 211], [64] * 7)):
