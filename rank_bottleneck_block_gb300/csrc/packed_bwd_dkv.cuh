@@ -55,6 +55,17 @@ struct Tiles {
   }
 };
 
+// A place in a ring of loads, and the parity of its turn there.
+struct Ring {
+  uint32_t stage = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++stage == n) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
 // P of 64 rows (L: -lse log2 e of them) of one key from its scores, in place, and packed.  MASK: rows before `from` or from
 // `rows` on do not see the key.
 template <bool MASK>
@@ -243,6 +254,8 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
       const uint32_t id_s = idesc_n<false>(kRows);  // K Q^T, V dO^T: all K-major
       const uint32_t id_g = idesc_n<true>(dh16);    // P^T dO, dS^T Q: A from TMEM, B MN-major
       const uint32_t ts = uniform(tmem) + w * kRows, tg = ts + 2 * kRows;
+      const int steps = (a.tq * a.G + 15) / 16;  // of 16 rows of a tile
+      const bool full = steps == 8 && ksteps == 8;
       uint8_t* sS = w ? sdO : sQ;  // B of the scores
       uint8_t* sG = w ? sQ : sdO;  // B of the gradient
       const Desc ad = sdesc(smem_addr(w ? sV : sK), 16, 1024), sd = sdesc(smem_addr(sS), 16, 1024),
@@ -254,13 +267,21 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
       uint64_t* score_full = w ? dp_full : s_full;
       uint64_t* mine_full = w ? ds_full : p_full;
       bool ok = true;
-      uint32_t g = 0, items = 0, turns = 0;
+      uint32_t items = 0, mine = 0, turns = 0;
+      Ring s, g;  // the tile of the next score, and of the next gradient
       auto wait = [&](uint64_t* bar, uint32_t phase) {
         return warp_wait(bar, phase & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
       };
       auto take_turn = [&] {
         ++turns;
         return wait(&turn[w], w ? turns + 1 : turns);
+      };
+      // Behind a score: the turn passes first, for a commit takes its issuer some 100 cycles.
+      auto score_issued = [&](bool last) {
+        mbar_arrive(&turn[1 - w]);
+        commit1(score_full);
+        if (w) commit1(&o_empty[s.stage]);
+        if (last) commit1(kv_free);
       };
       for (int it = 0; ok; ++it) {
         Item x;
@@ -272,46 +293,63 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
         const Tiles tiles(x, a.tq, a.taken.parts);
         if (tiles.n == 0) continue;
         const int left = min(a.tq, x.len - (tiles.first + tiles.n - 1) * a.tq) * a.G;  // rows of the last tile
-        auto issue_score = [&](int i) {  // of the item's tile i; the turn passes
-          if (elect()) {
-            mma_ss(ts, ad, sd.at((g + i) % ns * kTile), id_s, ksteps);
-            mbar_arrive(&turn[1 - w]);
-            commit1(score_full);
-            if (w) commit1(&o_empty[(g + i) % ns]);
-            if (i + 1 == tiles.n) commit1(kv_free);
-          }
-        };
-        ok = wait(kv_full, items) && wait(&bs_full[g % ns], g / ns) && take_turn();
+        ok = wait(kv_full, items) && wait(&bs_full[s.stage], s.phase) && take_turn();
         if (!ok) break;
         tc_fence_after();
-        issue_score(0);
-        for (int i = 0; i < tiles.n && ok; ++i) {
-          const uint32_t b = g + i, st = b % ng;
-          const bool last = i + 1 == tiles.n;
-          const int rows = last ? left : a.tq * a.G, steps = (rows + 15) / 16;
-          ok = wait(&bg_full[st], b / ng);
-          if (ok && last && left < 16 * steps && left < a.tq * a.G) {
-            // rows past the sequence's end that the product's last step reads
-            zero_rows(sG + st * kTile, left, 16 * steps, halves);
-            fence_async_smem();
-            __syncwarp();
-          }
-          ok = ok && (last || wait(&bs_full[(b + 1) % ns], (b + 1) / ns)) && (i > 0 || wait(acc_free, items + 1)) &&
-               wait(mine_full, b) && take_turn();
+        if (elect()) {
+          mma_ss(ts, ad, sd.at(s.stage * kTile), id_s, ksteps);
+          score_issued(tiles.n == 1);
+        }
+        s.next(ns);
+        ok = wait(acc_free, items + 1);
+        // The operand of a gradient is there: the other issuer took a score from it in a turn before.
+        for (int i = 0; ok && i + 1 < tiles.n; ++i) {
+          const Desc gb = gd.at(g.stage * kTile), sb = sd.at(s.stage * kTile);
+          const uint32_t acc = i > 0 ? 1u : 0u;
+          ok = wait(&bs_full[s.stage], s.phase) && wait(mine_full, mine) && take_turn();
           if (!ok) break;
           tc_fence_after();
-          if (elect()) {
-            mma_ts(tg, ts, gd.at(st * kTile), id_g, i > 0 ? 1u : 0u, min(4, steps));
-            if (steps > 4) mma_ts(tg, ts + 64, gd.at(st * kTile + 4 * 2048), id_g, 1u, steps - 4);
-            if (last) {
-              mbar_arrive(&turn[1 - w]);
-              commit1(acc_full);
-            }
+          if (full && elect()) {
+            mma_ts_n<4>(tg, ts, gb, id_g, acc);
+            mma_ts_n<4>(tg, ts + 64, gb.at(4 * 2048), id_g, 1u);
+            mma_ss_n<8>(ts, ad, sb, id_s);
+            score_issued(i + 2 == tiles.n);
+            commit1(&bg_empty[g.stage]);
           }
-          if (!last) issue_score(i + 1);
-          if (elect()) commit1(&bg_empty[st]);  // behind the turn: a commit takes its issuer some 100 cycles
+          if (!full && elect()) {
+            mma_ts(tg, ts, gb, id_g, acc, min(4, steps));
+            if (steps > 4) mma_ts(tg, ts + 64, gb.at(4 * 2048), id_g, 1u, steps - 4);
+            mma_ss(ts, ad, sb, id_s, ksteps);
+            score_issued(i + 2 == tiles.n);
+            commit1(&bg_empty[g.stage]);
+          }
+          s.next(ns);
+          g.next(ng);
+          ++mine;
         }
-        g += tiles.n;
+        if (!ok) break;
+        // The last tile, which may be a part of one.
+        const Desc gb = gd.at(g.stage * kTile);
+        const int lsteps = (left + 15) / 16;
+        if (left < 16 * lsteps && left < a.tq * a.G) {  // rows past the sequence's end that the product's last step reads
+          ok = wait(&bg_full[g.stage], g.phase);
+          if (!ok) break;
+          zero_rows(sG + g.stage * kTile, left, 16 * lsteps, halves);
+          fence_async_smem();
+          __syncwarp();
+        }
+        ok = wait(mine_full, mine) && take_turn();
+        if (!ok) break;
+        tc_fence_after();
+        if (elect()) {
+          mma_ts(tg, ts, gb, id_g, tiles.n > 1 ? 1u : 0u, min(4, lsteps));
+          if (lsteps > 4) mma_ts(tg, ts + 64, gb.at(4 * 2048), id_g, 1u, lsteps - 4);
+          mbar_arrive(&turn[1 - w]);
+          commit1(acc_full);
+          commit1(&bg_empty[g.stage]);
+        }
+        g.next(ng);
+        ++mine;
         ++items;
       }
       if (elect()) {

@@ -277,20 +277,20 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
         if (x.head < 0) break;
         const int n = x.nblocks(t, a.tq), nmax = max(x.nblocks(0, a.tq), x.nblocks(1, a.tq));
         const int last = x.keys(t, a.tq) - (n - 1) * kRows;  // keys of the tile's last block that some row sees
-        auto issue_s = [&](int j, uint32_t blk) {  // S of block j, which is the blk-th of all; the turn passes
-          if (elect()) {
-            mma_ss(ts, qd, kd.at(2 * kTile * (blk & 1)), id_s, ksteps);
-            mbar_arrive(&turn[1 - t]);
-            commit1(&s_full[t]);
-            commit1(&kv_empty[2 * (blk & 1)]);
-            if (j + 1 == n) commit1(&q_free[t]);
-          }
+        auto issue_s = [&](int j, uint32_t blk) {  // S of block j, which is the blk-th of all
+          const Desc k = kd.at(2 * kTile * (blk & 1));
+          if (ksteps == 8) mma_ss_n<8>(ts, qd, k, id_s);
+          else mma_ss(ts, qd, k, id_s, ksteps);
+          mbar_arrive(&turn[1 - t]);  // the turn passes before the commits, which take the issuer some 100 cycles each
+          commit1(&s_full[t]);
+          commit1(&kv_empty[2 * (blk & 1)]);
+          if (j + 1 == n) commit1(&q_free[t]);
         };
         ok = (n == 0 || (wait(&q_full[t], items) && wait(&kv_full[2 * (b & 1)], b >> 1))) && take_turn();
         if (!ok) break;
         tc_fence_after();
-        if (n > 0) issue_s(0, b);
-        else pass_turn();
+        if (n == 0) pass_turn();
+        else if (elect()) issue_s(0, b);
         for (int j = 0; j < nmax && ok; ++j, ++b) {
           uint64_t* v_full = &kv_full[2 * (b & 1) + 1];
           uint64_t* v_empty = &kv_empty[2 * (b & 1) + 1];
@@ -303,8 +303,25 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
             pass_turn();
             continue;
           }
-          ok = wait(v_full, b >> 1) && (j + 1 == n || wait(&kv_full[2 * ((b + 1) & 1)], (b + 1) >> 1));
-          const int steps = j + 1 < n ? 8 : (last + 15) / 16, left = x.len - j * kRows;
+          const Desc v = vd.at(2 * kTile * (b & 1));
+          if (j + 1 < n) {
+            ok = wait(v_full, b >> 1) && wait(&kv_full[2 * ((b + 1) & 1)], (b + 1) >> 1) &&
+                 (j > 0 || wait(&o_free[t], items + 1)) && wait(&p_full[2 * t], p_of++) && take_turn();
+            if (!ok) break;
+            tc_fence_after();
+            if (elect()) mma_ts_n<4>(to, ts, v, id_o, j > 0 ? 1u : 0u);
+            ok = wait(&p_full[2 * t + 1], p_second++);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect()) {
+              mma_ts_n<4>(to, ts + 32, v.at(4 * 2048), id_o, 1u);
+              issue_s(j + 1, b + 1);
+              commit1(v_empty);
+            }
+            continue;
+          }
+          ok = wait(v_full, b >> 1);
+          const int steps = (last + 15) / 16, left = x.len - j * kRows;
           if (ok && left < 16 * steps) {  // rows past the sequence's end that the product's last step reads
             zero_rows(sKV + (2 * (b & 1) + 1) * kTile, left, 16 * steps, halves);  // (both issuers: the same zeroes)
             fence_async_smem();
@@ -313,7 +330,6 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
           ok = ok && (j > 0 || wait(&o_free[t], items + 1)) && wait(&p_full[2 * t], p_of++) && take_turn();
           if (!ok) break;
           tc_fence_after();
-          const Desc v = vd.at(2 * kTile * (b & 1));
           if (elect()) mma_ts(to, ts, v, id_o, j > 0 ? 1u : 0u, min(4, steps));
           if (steps > 4) {
             ok = wait(&p_full[2 * t + 1], p_second++);
@@ -321,13 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) packed_fwd_kernel(const __grid_co
             tc_fence_after();
             if (elect()) mma_ts(to, ts + 32, v.at(4 * 2048), id_o, 1u, steps - 4);
           }
-          if (j + 1 < n) {
-            issue_s(j + 1, b + 1);
-          } else if (elect()) {
+          if (elect()) {
             mbar_arrive(&turn[1 - t]);
             commit1(&o_last[t]);
+            commit1(v_empty);
           }
-          if (elect()) commit1(v_empty);  // behind the turn: a commit takes its issuer some 100 cycles
         }
         if (n > 0) ++items;
       }
