@@ -187,7 +187,9 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
           if (!wait(&k_full[st], b / kStagesK)) return false;
           tc_fence_after();
           if (elect()) {
-            mma_ss(tm + (b & 1) * kRows, qd, kd.at(st * kTile), id_s, ksteps);
+            const Desc kb = kd.at(st * kTile);
+            if (ksteps == 8) mma_ss_n<8>(tm + (b & 1) * kRows, qd, kb, id_s);
+            else mma_ss(tm + (b & 1) * kRows, qd, kb, id_s, ksteps);
             commit1(&s_full[b & 1]);
             if (j + 1 == n) commit1(qd_free);
           }
@@ -207,8 +209,14 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
           tc_fence_after();
           if (elect()) {
             const uint32_t ds = tm + (b & 1) * kRows;
-            mma_ts(tm + 3 * kRows, ds, gd.at(st * kTile), id_g, j > 0 ? 1u : 0u, min(4, steps));
-            if (steps > 4) mma_ts(tm + 3 * kRows, ds + 64, gd.at(st * kTile + 4 * 2048), id_g, 1u, steps - 4);
+            const Desc gb = gd.at(st * kTile);
+            if (steps == 8) {
+              mma_ts_n<4>(tm + 3 * kRows, ds, gb, id_g, j > 0 ? 1u : 0u);
+              mma_ts_n<4>(tm + 3 * kRows, ds + 64, gb.at(4 * 2048), id_g, 1u);
+            } else {
+              mma_ts(tm + 3 * kRows, ds, gb, id_g, j > 0 ? 1u : 0u, min(4, steps));
+              if (steps > 4) mma_ts(tm + 3 * kRows, ds + 64, gb.at(4 * 2048), id_g, 1u, steps - 4);
+            }
             commit1(&k_empty[st]);
             if (j + 1 == n) commit1(dq_last);
           }
@@ -246,7 +254,9 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
           if (!ok) break;
           tc_fence_after();
           if (elect()) {
-            mma_ss(tm + 2 * kRows, od, vd.at(st * kTile), id_s, ksteps);
+            const Desc vb = vd.at(st * kTile);
+            if (ksteps == 8) mma_ss_n<8>(tm + 2 * kRows, od, vb, id_s);
+            else mma_ss(tm + 2 * kRows, od, vb, id_s, ksteps);
             commit1(dp_full);
             commit1(&v_empty[st]);
             if (j + 1 == n) commit1(qd_free);

@@ -262,7 +262,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // A value that every lane holds, known to the compiler as one of the whole warp: what follows from it is computed once
 // and is at hand for the matrix instructions, which take their operands from such registers.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // Waits, for a limited time, for a copy or MMA in flight before the block ends (error paths).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
