@@ -267,14 +267,16 @@ def test_many_calls_give_the_same_bits():
     assert all(torch.equal(getattr(run, n), t) for n, t in keep.items())
 
 
-@pytest.mark.parametrize("lengths,Hq,Hk,back", [([40], 4, 1, 2), ([1024], 8, 2, 3), ([300] * 60, 8, 8, 2)])
-def test_launches_are_counted(lengths, Hq, Hk, back):
-    """The list and the attention; the sums of dK and dV where their key blocks are cut in parts."""
+@pytest.mark.parametrize("lengths,Hq,Hk,front,back", [([40], 4, 1, 1, 2), ([1024], 8, 2, 1, 3), ([300] * 60, 8, 8, 2, 2),
+                                                      ([1] * 40 + [0] * 300, 2, 1, 2, 2)])
+def test_launches_are_counted(lengths, Hq, Hk, front, back):
+    """The list (of a forward: where not every item has an SM) and the attention; the sums of dK and dV where their key
+    blocks are cut in parts."""
     from rank_bottleneck_block_gb300 import lowrank as L
 
     shape = _shape(lengths, Hq, Hk, 64)
     run = _make(shape, I.make_packed_case(shape, lengths, seed=15))
-    for call, want in ((run.forward, 2), (run.backward, back)):
+    for call, want in ((run.forward, front), (run.backward, back)):
         before = L.lr_launch_count()
         call()
         assert L.lr_launch_count() - before == want
@@ -333,10 +335,24 @@ def test_two_calls_on_two_streams():
 @pytest.mark.parametrize("offs", [[0, 50, 40, 100], [-1, 10, 20, 30], [0, 10, 20, 101], [0, 200, 20, 100],
                                   [0, -2 ** 31, 20, 100], [0, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1], [90, 80, 70, 60]])
 def test_offsets_out_of_order_write_nothing(offs):
+    _refuses_offsets(I.PackedShape(T=100, nseq=3, Hq=4, Hk=2, dh=64), [20, 30, 50], offs)
+
+
+@pytest.mark.parametrize("nseq,bad", [(n, i) for n in (60, 256, 257, 300) for i in (0, 1, 31, 32, 33, 255, 256, 257, 299)
+                                      if i < n])
+def test_one_offset_out_of_order_among_many(nseq, bad):
+    """Whether a list is made or every block finds its own item."""
+    lengths = [0] * nseq
+    lengths[nseq // 2] = 40
+    offs = np.concatenate([[0], np.cumsum(lengths)])
+    offs[bad] = offs[bad + 1] + 1
+    _refuses_offsets(I.PackedShape(T=50, nseq=nseq, Hq=2, Hk=1, dh=64), lengths, offs.tolist())
+
+
+def _refuses_offsets(shape, lengths, offs):
     from rank_bottleneck_block_gb300 import lowrank as L
 
-    shape = I.PackedShape(T=100, nseq=3, Hq=4, Hk=2, dh=64)
-    case = I.make_packed_case(shape, [20, 30, 50], seed=1)
+    case = I.make_packed_case(shape, lengths, seed=1)
     run = _make(shape, case)
     good = run.offs
     run.offs = torch.tensor(offs, dtype=torch.int32, device="cuda")
