@@ -12,12 +12,15 @@
 // threads first: the K-th of these bounds what can be among the K largest, and only what reaches it is compared with each
 // other (K times a group's share at most, whatever the values).
 //
-// Measured: 4096 rows of 131072 bf16 logits forward 175 us (6.1 TB/s, 91 % of a copy's rate), backward 304 us (7.1 TB/s;
-// with the exponential of fp32 566 us, bound by instructions).  One row of 131072 with the 20 largest: 12 us; the join is
+// Measured: 4096 rows of 131072 bf16 logits forward 171 us (6.3 TB/s, 93 % of a copy's rate; 182 with arithmetic on single
+// numbers, 174 with five blocks an SM, which spill), backward 304 us (7.1 TB/s; with the exponential of fp32 566 us, bound
+// by instructions).  One row of 131072 with the 20 largest: 12 us; the join is
 // a chain of short steps behind one another.
 #include "logprob_kernels.cuh"
 
 #include <algorithm>
+
+#include "f32x2.cuh"
 
 namespace lr {
 namespace {
@@ -148,7 +151,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 template <typename ST, bool TOP>
-__global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 ? 5 : 6) logprob_fwd_kernel(LogprobFwd a, LogprobPlan plan) {
+__global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 ? 4 : 6) logprob_fwd_kernel(LogprobFwd a, LogprobPlan plan) {
   __shared__ Part warps[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.x / plan.splits), split = static_cast<int>(blockIdx.x - 1u * t * plan.splits);
@@ -192,17 +195,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(ST) == 2 ? 5 : 6) logprob_fwd
     }
     if (!(gm <= p.m)) p = join(p, Part{gm, 0.f, 0.f}, c);
     if (p.m > neg_inf()) {
+      const uint64_t nm = f2_pack(-p.m, -p.m), cc = f2_pack(c, c);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        float s[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+        uint64_t s2 = 0, w2 = 0;
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) {
-          const float d = fmaxf(c * (v[u][e] - p.m), kFloor), x = ex2(d);
-          s[e & 1] += x;
-          w[e & 1] = fmaf(x, d, w[e & 1]);
+        for (int e = 0; e < kGroup; e += 2) {
+          float d[2], s[2];
+          f2_unpack(f2_mul(f2_add(f2_pack(v[u][e], v[u][e + 1]), nm), cc), d[0], d[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            d[i] = fmaxf(d[i], kFloor);
+            s[i] = ex2(d[i]);
+          }
+          const uint64_t x = f2_pack(s[0], s[1]);
+          s2 = f2_add(s2, x);
+          w2 = f2_fma(x, f2_pack(d[0], d[1]), w2);
         }
-        p.s += s[0] + s[1];
-        p.w += w[0] + w[1];
+        float x[2], y[2];
+        f2_unpack(s2, x[0], x[1]);
+        f2_unpack(w2, y[0], y[1]);
+        p.s += x[0] + x[1];
+        p.w += y[0] + y[1];
       }
     }
   }
@@ -452,8 +466,8 @@ LogprobPlan logprob_plan(int T, int V, int es, int sms) {
   LogprobPlan p;
   const int most = V + 16 / es - 1;  // places of a row, counted from a 16-byte boundary
   p.nseg = (most + kLogprobSeg - 1) / kLogprobSeg;
-  // One block to a row where rows fill the GPU one and a half times (five blocks an SM); else a row over several, each with
-  // one load of half its threads at least.  515 rows of 50021 in fp32: 34.9 us when cut for 15 blocks an SM, 33.6 for 8, 36.5
+  // One block to a row where there are eight an SM (four of bf16 or six of fp32 run at a time); else a row over several, each
+  // with one load of half its threads at least.  515 rows of 50021 in fp32: 34.9 us when cut for 15 blocks an SM, 33.6 for 8, 36.5
   // for 6; 1500 rows in bf16: 43.9, 39.2, 39.1.
   const int fit = (most + 4095) / 4096;
   const int want = (8 * sms + T - 1) / T;

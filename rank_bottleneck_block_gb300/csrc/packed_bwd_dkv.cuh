@@ -55,17 +55,6 @@ struct Tiles {
   }
 };
 
-// A place in a ring of loads, and the parity of its turn there.
-struct Ring {
-  uint32_t stage = 0, phase = 0;
-  __device__ __forceinline__ void next(uint32_t n) {
-    if (++stage == n) {
-      stage = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 // P of 64 rows (L: -lse log2 e of them) of one key from its scores, in place, and packed.  MASK: rows before `from` or from
 // `rows` on do not see the key.
 template <bool MASK>

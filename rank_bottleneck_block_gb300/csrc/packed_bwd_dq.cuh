@@ -171,6 +171,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
                  gd = sdesc(smem_addr(sK), kHalf, 1024);
       bool ok = true;
       uint32_t g = 0, items = 0;
+      Ring s, k;  // K of the next S, and of the next dQ
       auto wait = [&](uint64_t* bar, uint32_t phase) {
         return warp_wait(bar, phase & 1, abort_flag, a.err, DEV_ERR_TIMEOUT_MMA);
       };
@@ -183,21 +184,22 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
         if (x.head < 0) break;
         const int n = x.nblocks(0, a.tq), last = x.keys(0, a.tq) - (n - 1) * kRows;
         auto issue_s = [&](int j) {  // S of the item's block j
-          const uint32_t b = g + j, st = b % kStagesK;
-          if (!wait(&k_full[st], b / kStagesK)) return false;
+          const uint32_t b = g + j;
+          if (!wait(&k_full[s.stage], s.phase)) return false;
           tc_fence_after();
           if (elect()) {
-            const Desc kb = kd.at(st * kTile);
+            const Desc kb = kd.at(s.stage * kTile);
             if (ksteps == 8) mma_ss_n<8>(tm + (b & 1) * kRows, qd, kb, id_s);
             else mma_ss(tm + (b & 1) * kRows, qd, kb, id_s, ksteps);
             commit1(&s_full[b & 1]);
             if (j + 1 == n) commit1(qd_free);
           }
+          s.next(kStagesK);
           return true;
         };
         ok = wait(qd_full, items) && issue_s(0) && (n == 1 || issue_s(1));
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t b = g + j, st = b % kStagesK;
+          const uint32_t b = g + j, st = k.stage;
           const int steps = j + 1 < n ? 8 : (last + 15) / 16, left = x.len - j * kRows;
           ok = (j > 0 || wait(dq_free, items + 1)) && wait(&ds_full[b & 1], b >> 1);
           if (!ok) break;
@@ -220,6 +222,7 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DqArgs& a, unsig
             commit1(&k_empty[st]);
             if (j + 1 == n) commit1(dq_last);
           }
+          k.next(kStagesK);
           if (j + 2 < n) ok = issue_s(j + 2);
         }
         g += n;
