@@ -297,7 +297,8 @@ __device__ __forceinline__ void body(const BwdMaps& maps, const DkvArgs& a, unsi
           const uint32_t acc = i > 0 ? 1u : 0u;
           // What comes last is awaited last: P behind the turn, the turn behind dS (4 x 4096 tokens, 32 over 8 heads: 1182 ->
           // 1168 us).
-          ok = wait(&bs_full[s.stage], s.phase) && (w ? wait(mine_full, mine) && take_turn() : take_turn() && wait(mine_full, mine));
+          ok = wait(&bs_full[s.stage], s.phase) &&
+               (w ? wait(mine_full, mine) && take_turn() : take_turn() && wait(mine_full, mine));
           if (!ok) break;
           tc_fence_after();
           if (full && elect()) {

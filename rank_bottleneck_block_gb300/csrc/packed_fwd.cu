@@ -26,7 +26,7 @@
 // What bounds it is the issuing: a wait takes its warp some 200 cycles even when there is nothing to wait for, and a
 // commit 100.  16384 tokens, 32 over 8 heads: one issuer 2354 us, one for each tile 1929, by strict turns 1530 (both at
 // will, so that their instructions interleave: 1803), a step without branches between its instructions and the turn
-// awaited before P 1380 (1.59 PFLOP/s).  Without its exponentials the kernel gained 8 %, without the maxima 4 %.
+// awaited before P 1346 (1.63 PFLOP/s).  Without its exponentials the kernel gained 8 %, without the maxima 4 %.
 #include <algorithm>
 #include <type_traits>
 
