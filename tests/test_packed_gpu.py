@@ -267,6 +267,27 @@ def test_many_calls_give_the_same_bits():
     assert all(torch.equal(getattr(run, n), t) for n, t in keep.items())
 
 
+def test_other_offsets_in_a_graph_that_makes_a_list():
+    """More items than SMs: the captured calls cut the sequences that they find."""
+    from rank_bottleneck_block_gb300.runner import GraphStep
+
+    lengths = [300] * 10
+    shape = _shape(lengths, 8, 8, 64)
+    case = I.make_packed_case(shape, lengths, seed=17)
+    run = _make(shape, case)
+    graph = GraphStep(run.step)
+    graph()
+    _check(shape, case, run)
+    for other in ([3000] + [0] * 9, [0, 1, 700, 0, 0, 1500, 31, 2, 128, 129], [0] * 10):
+        new = I.make_packed_case(shape, other, seed=18, first=3 if sum(other) < 2990 else 0)
+        for n in ("q", "k", "v", "dout", "offs"):
+            getattr(run, n).copy_(new[n])
+        for n in ROWS + ("lse",):
+            getattr(run, n).fill_(7.0)
+        graph()
+        _check(shape, new, run)
+
+
 @pytest.mark.parametrize("lengths,Hq,Hk,front,back", [([40], 4, 1, 1, 2), ([1024], 8, 2, 1, 3), ([300] * 60, 8, 8, 2, 2),
                                                       ([1] * 40 + [0] * 300, 2, 1, 2, 2)])
 def test_launches_are_counted(lengths, Hq, Hk, front, back):
