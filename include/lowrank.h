@@ -354,11 +354,17 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
  * first, equal logits by their index, a NaN before any number; top = 0: both unused and may
  * be NULL.  logp, entropy, lse: fp32 [T].
  * A logit of -inf has p = 0.  A row of nothing else has lse = -inf, entropy 0, and no
- * gradient.  A row that holds a NaN or +inf has NaN for all three.
+ * gradient.  A row that holds a NaN or +inf has NaN for all three, with or without a target.
+ * lse alone is infinite where scale times the largest logit leaves fp32's range.
  * Backward of sum(dlogp * logp + dentropy * entropy):
  *     dlogits_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + entropy)).
  * dlogp: fp32 [T]; dentropy: fp32 [T] or NULL (entropy is then unused and may be NULL);
  * lse, entropy: the forward's.  dlogits may be logits (the same pointer and row distance).
+ * log p_j is taken as z_j - lse while the rounding of lse moves p by 2^-14 of itself at most
+ * (bf16: |lse| up to 1024) or 2^-18 (fp32: up to 64).  Where |lse| is larger or not finite the
+ * row is read once more for its maximum and sum, and log p_j comes from differences to the
+ * maximum, as logp and entropy do in the forward: no offset that a row's logits share changes
+ * their gradient.
  * Rows without a gradient (no target or dlogp 0, and dentropy 0) are set to 0 unread.
  * scale finite and positive; V <= 2^19, T <= 2^24; every pointer 16-byte aligned (rows need not be).
  * Sums are fp32; the gradient is rounded once.

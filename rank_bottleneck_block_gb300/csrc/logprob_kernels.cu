@@ -369,61 +369,38 @@ __global__ void __launch_bounds__(kThreads) logprob_join_kernel(LogprobFwd a, Lo
   });
 }
 
-// 2^x of the gradient: bf16 takes the hardware approximation (its 2^-22 is far below the rounding of the result), fp32
-// the library's exponential of the difference, whose rounding a factor of log2 e would double.
-template <typename ST>
-struct Prob;
-template <>
-struct Prob<bf16> {
-  static __device__ __forceinline__ void get(float x, float scale, float lse, float& lp, float& p) {
-    lp = fmaxf(fmaf(x, scale, -lse), kFloor);
-    p = ex2(lp * kLog2e);
-  }
-};
-template <>
-struct Prob<float> {
-  static __device__ __forceinline__ void get(float x, float scale, float lse, float& lp, float& p) {
-    lp = fmaxf(fmaf(x, scale, -lse), kFloor);
-    p = expf(lp);
-  }
+// The gradient of a row, d_j = scale (p_j (-de (lp_j + H) - dl) + [j = target] dl) = p_j (e lp_j + f) + [j = target] hit.
+struct Grad {
+  int k;
+  float e, f, hit;
 };
 
-template <typename ST, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads, 4) logprob_bwd_kernel(LogprobBwd a, int chunks, int chunk) {
-  const int t = static_cast<int>(blockIdx.x / chunks), part = static_cast<int>(blockIdx.x - 1u * t * chunks);
-  const ST* row = static_cast<const ST*>(a.logits) + t * a.ld;
-  ST* out = static_cast<ST*>(a.out) + t * a.ldo;
-  pdl_wait();
-  const int k = a.target[t];
-  const float lse = a.lse[t], given = a.dlogp[t];
-  const float de = ENTROPY ? a.dentropy[t] : 0.f, h = ENTROPY ? a.entropy[t] : 0.f;
-  const float dl = k >= 0 && k < a.V ? given : 0.f;
-  // d_j = scale (p_j (-de (lp_j + H) - dl) + [j = target] dl) = p_j (e lp_j + f) + [j = target] hit
-  const float e = -de * a.scale, hit = dl * a.scale;
-  const float f = fmaf(e, h, -hit) + (lse - lse);  // NaN where lse is
+// e^x of the gradient: bf16 takes the hardware approximation of 2^x (its 2^-22 is far below the rounding of the result),
+// fp32 the library's exponential, whose rounding a factor of log2 e would double.
+template <typename ST>
+__device__ __forceinline__ float exp_of(float x) {
+  if constexpr (sizeof(ST) == 2) return ex2(x * kLog2e);
+  else return expf(x);
+}
+
+// Up to here the rounding of lse (2^-24 of it, which p takes over as it is) is taken: 2^-14 of p for bf16, a 64th of
+// the result's own rounding, and 2^-18 for fp32, what log p = 64 costs anyway.  Beyond, far_row takes longer: 4096 rows of
+// 131072 in bf16 310 us on this side and 486 on the other (three passes over the logits are 475), 2048 in fp32 312 and 513,
+// a single row of bf16 7 and 31.
+template <typename ST>
+constexpr float kFarLse = sizeof(ST) == 2 ? 1024.f : 64.f;
+
+// Places begin .. end - 1 of a row (counted from the 16-byte boundary before it) and of its gradient: `gradient` makes a
+// group of logits from place `at` on into its gradient, or all are 0 without being read.
+template <typename ST, typename F>
+__device__ __forceinline__ void write_gradient(const ST* row, ST* out, int V, int begin, int end, bool zero, F gradient) {
   const int shift = lead(row), oshift = lead(out);
-  const long long begin = 1LL * part * chunk;
-  const int end = static_cast<int>(min(begin + chunk, 1LL * a.V + shift));
   constexpr int kU = kUnroll<ST>, kStride = kThreads * kGroup;
-  const bool zero = (dl == 0.f && de == 0.f) || lse == neg_inf();  // no gradient, or no distribution
   const bool whole = oshift == shift;  // both rows can be taken in aligned groups
-  auto gradient = [&](float* v, int at) {
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-      float lp, p;
-      Prob<ST>::get(v[i], a.scale, lse, lp, p);
-      v[i] = p * (ENTROPY ? fmaf(e, lp, f) : f);
-    }
-    if (static_cast<unsigned>(k - at) < kGroup && hit != 0.f) {
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i)
-        if (at + i == k) v[i] += hit;
-    }
-  };
-  for (int i = static_cast<int>(begin); i < end; i += kU * kStride) {
+  for (int i = begin; i < end; i += kU * kStride) {
     const int at = i + threadIdx.x * kGroup - shift;
     float v[kU][kGroup];
-    if (whole && i >= shift && i + kU * kStride <= end && i + kU * kStride <= a.V + shift) {
+    if (whole && i >= shift && i + kU * kStride <= end && i + kU * kStride <= V + shift) {
       if (zero) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
@@ -445,19 +422,111 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_bwd_kernel(LogprobBwd a, 
 #pragma unroll
           for (int n = 0; n < kGroup; ++n) v[u][n] = 0.f;
         } else {
-          load_group(row, j, a.V, v[u]);
+          load_group(row, j, V, v[u]);
           gradient(v[u], j);
         }
-        if (whole && j >= 0 && j + kGroup <= a.V) {
+        if (whole && j >= 0 && j + kGroup <= V) {
           store8(out + j, v[u]);
         } else {
 #pragma unroll
           for (int n = 0; n < kGroup; ++n)
-            if (j + n >= 0 && j + n < a.V) out[j + n] = from_float<ST>(v[u][n]);
+            if (j + n >= 0 && j + n < V) out[j + n] = from_float<ST>(v[u][n]);
         }
       }
     }
   }
+}
+
+__device__ __forceinline__ void add_hit(float* v, int at, const Grad& g) {
+  if (static_cast<unsigned>(g.k - at) < kGroup && g.hit != 0.f) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (at + i == g.k) v[i] += g.hit;
+  }
+}
+
+// A whole row whose lse does not tell its probabilities: rounded, it has lost log s (logits that share a large offset,
+// or masks of the type's lowest value alone), or it is not finite.  One block takes the row's m and s again and then log p
+// from differences to m, as the forward does; it reads the row twice, and before it writes any of it (the gradient may
+// take the logits' place).
+template <typename ST, bool ENTROPY>
+__device__ __noinline__ void far_row(const ST* row, ST* out, int V, float scale, Grad g) {
+  __shared__ Part warps[kWarps];
+  const float c = scale * kLog2e;
+  const int shift = lead(row);
+  constexpr int kU = kUnroll<ST>, kStride = kThreads * kGroup;
+  Part p{neg_inf(), 0.f, 0.f};
+  for (int i = 0; i < V + shift; i += kU * kStride) {
+    const int at = i + threadIdx.x * kGroup - shift;
+    float v[kU][kGroup], m = neg_inf();
+    if (i >= shift && i + kU * kStride <= V + shift) {
+      load_groups(row + at, kStride, v);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) load_group(row, at + u * kStride, V, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int n = 0; n < kGroup; ++n) m = max_nan(m, v[u][n]);
+    if (!(m <= p.m)) p = join(p, Part{m, 0.f, 0.f}, c);
+    if (p.m > neg_inf()) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float s = 0.f;
+#pragma unroll
+        for (int n = 0; n < kGroup; ++n) s += ex2(fmaxf(c * (v[u][n] - p.m), kFloor));
+        p.s += s;
+      }
+    }
+  }
+  p = warp_join(p, c);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = p;
+  __syncthreads();
+  p = warps[0];
+#pragma unroll 1
+  for (int i = 1; i < kWarps; ++i) p = join(p, warps[i], c);
+  const float log_s = kLn2 * log2f(p.s), bad = p.m <= kMax ? 0.f : __int_as_float(0x7fc00000);  // a NaN or +inf in the row
+  write_gradient(row, out, V, 0, V + shift, p.m == neg_inf(), [&](float* v, int at) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const float lp = fmaxf(fmaf(scale, v[i] - p.m, -log_s), kFloor);
+      v[i] = fmaf(exp_of<ST>(lp), ENTROPY ? fmaf(g.e, lp, g.f) : g.f, bad);
+    }
+    add_hit(v, at, g);
+  });
+}
+
+template <typename ST, bool ENTROPY>
+__global__ void __launch_bounds__(kThreads, 4) logprob_bwd_kernel(LogprobBwd a, int chunks, int chunk) {
+  const int t = static_cast<int>(blockIdx.x / chunks), part = static_cast<int>(blockIdx.x - 1u * t * chunks);
+  const ST* row = static_cast<const ST*>(a.logits) + t * a.ld;
+  ST* out = static_cast<ST*>(a.out) + t * a.ldo;
+  pdl_wait();
+  const int k = a.target[t];
+  const float lse = a.lse[t], given = a.dlogp[t];
+  const float de = ENTROPY ? a.dentropy[t] : 0.f, h = ENTROPY ? a.entropy[t] : 0.f;
+  const float dl = k >= 0 && k < a.V ? given : 0.f;
+  Grad g;
+  g.k = k;
+  g.e = -de * a.scale;
+  g.hit = dl * a.scale;
+  g.f = fmaf(g.e, h, -g.hit);
+  const bool zero = dl == 0.f && de == 0.f;  // no gradient
+  if (!zero && !(fabsf(lse) <= kFarLse<ST>)) {
+    if (part == 0) far_row<ST, ENTROPY>(row, out, a.V, a.scale, g);
+    return;
+  }
+  const long long begin = 1LL * part * chunk;
+  const int end = static_cast<int>(min(begin + chunk, 1LL * a.V + lead(row)));
+  write_gradient(row, out, a.V, static_cast<int>(begin), end, zero, [&](float* v, int at) {
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const float lp = fmaxf(fmaf(v[i], a.scale, -lse), kFloor);
+      v[i] = exp_of<ST>(lp) * (ENTROPY ? fmaf(g.e, lp, g.f) : g.f);
+    }
+    add_hit(v, at, g);
+  });
 }
 
 }  // namespace
