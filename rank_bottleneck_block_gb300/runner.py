@@ -632,8 +632,9 @@ class PackedAttention(_Assigned):
     case: q [T, Hq*dh], k, v [T, Hk*dh] (rows may be further apart: columns of a packed matrix), offs int32 [nseq + 1]
     (sequence i is rows offs[i] to offs[i + 1] - 1) and, for backward(), dout [T, Hq*dh].  forward() writes o and lse
     [T, Hq] fp32 (the log-sum-exp of each row's scores); backward() reads them and writes dq, dk, dv.  Rows of no
-    sequence are not written (the outputs' memory is not initialised).  Offsets are read on the device: where they are
-    not in order nothing is written, and lr_check_device_error says so.
+    sequence are not written: they hold zeros from the start, and what an earlier call wrote there where its offsets had
+    them (zero those of dq, dk and dv before anything that sums over all rows, as a projection's weight gradient does).
+    Offsets are read on the device: where they are not in order nothing is written, and lr_check_device_error says so.
 
     The tensors are attributes, and may be replaced by others of their size and type on the same device, 16-byte
     aligned: new offsets, or the o and lse of another forward.  The calls' arguments are converted once for each
@@ -665,11 +666,11 @@ class PackedAttention(_Assigned):
         for n in ("offs", "q", "k", "v", "dout"):
             t = case.get(n)
             setattr(self, n, None if t is None else self._fit(n, t).to(device))
-        self.o = torch.empty(q, dtype=td, device=device)
-        self.lse = torch.empty(s.T, s.Hq, dtype=torch.float32, device=device)
+        self.o = torch.zeros(q, dtype=td, device=device)
+        self.lse = torch.zeros(s.T, s.Hq, dtype=torch.float32, device=device)
         back = self.dout is not None
-        self.dq = torch.empty(q, dtype=td, device=device) if back else None
-        self.dk, self.dv = (torch.empty(k, dtype=td, device=device) if back else None for _ in range(2))
+        self.dq = torch.zeros(q, dtype=td, device=device) if back else None
+        self.dk, self.dv = (torch.zeros(k, dtype=td, device=device) if back else None for _ in range(2))
         self.ws_b = _buf(L.lr_packed_attn_bwd_workspace_bytes(self.sh), device) if back else None
 
     def _common(self):
