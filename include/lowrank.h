@@ -316,7 +316,8 @@ lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const 
  * any result, whatever they hold.  A value that is not finite reaches results of its own
  * sequence only, there also those of rows before it.
  * bf16 only (LR_F32: LR_ERR_UNSUPPORTED).  Hq a multiple of Hk, G <= 128, dh a multiple of 8
- * up to 128, H*dh <= 2^24, T*Hq <= 2^30, nseq <= 2^24; scale finite and positive.
+ * up to 128, H*dh <= 2^24, T*Hq <= 2^30, nseq <= 2^24; scale positive, at most 2.35e38;
+ * scale log2(e) q_t.k_j has to stay within fp32's range.
  * Products are of bf16 operands summed in fp32; P and dS are rounded to bf16 for theirs, the
  * softmax statistics, O, dQ, dK and dV are fp32 until they are rounded once.
  * Offsets live on the device and are read there: if they are not in order or leave the
@@ -366,7 +367,7 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
  * maximum, as logp and entropy do in the forward: no offset that a row's logits share changes
  * their gradient.
  * Rows without a gradient (no target or dlogp 0, and dentropy 0) are set to 0 unread.
- * scale finite and positive; V <= 2^19, T <= 2^24; every pointer 16-byte aligned (rows need not be).
+ * scale positive, at most 2.35e38; V <= 2^19, T <= 2^24; every pointer 16-byte aligned (rows need not be).
  * Sums are fp32; the gradient is rounded once.
  */
 size_t lr_logprob_workspace_bytes(lr_dtype dt, int T, int V, int top);

@@ -2623,8 +2623,9 @@ static lr_status check_packed(lr_dtype dt, const lr_packed_shape* sh) {
   return LR_OK;
 }
 
+// The kernels work in powers of two: scale log2(e) has to be finite, too.
 static lr_status check_scale(float scale) {
-  if (!(scale > 0.f) || scale > 3.4e38f) return fail(LR_ERR_SHAPE, "scale must be finite and positive");
+  if (!(scale > 0.f) || scale > 2.35e38f) return fail(LR_ERR_SHAPE, "scale = %g must be positive, 2.35e38 at most", scale);
   return LR_OK;
 }
 
