@@ -672,6 +672,8 @@ class PackedAttention(_Assigned):
         self.dq = torch.zeros(q, dtype=td, device=device) if back else None
         self.dk, self.dv = (torch.zeros(k, dtype=td, device=device) if back else None for _ in range(2))
         self.ws_b = _buf(L.lr_packed_attn_bwd_workspace_bytes(self.sh), device) if back else None
+        if self._device.type == "cuda" and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self._device).synchronize()  # a call on any stream finds the zeros written
 
     def _common(self):
         return (self.dt, L.ctypes.pointer(self.sh), self.scale, self.offs, *self._rows("q", "k", "v", "o"), self.lse)

@@ -105,3 +105,24 @@ def test_padded_batch_through_an_output_layer_and_back():
         assert np.abs(got - want["dg"]).max() <= 1e-4 * np.abs(want["dg"]).max()
     total = np.sqrt(sum((x ** 2).sum() for x in before))
     assert abs(float(norm) - total) <= 1e-5 * total
+
+
+def test_a_first_call_on_another_stream():
+    """The outputs' first zeros are written by then, however much work the constructor's stream had before it."""
+    from rank_bottleneck_block_gb300.runner import PackedAttention
+
+    lengths = [200, 77]
+    shape = I.PackedShape(T=300, nseq=2, Hq=4, Hk=2, dh=64)
+    case = I.make_packed_case(shape, lengths, seed=1, first=3, device="cuda")
+    want = PackedAttention(shape, case)
+    want.step()
+    m = torch.ones(8192, 8192, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        m @ m
+    run = PackedAttention(shape, case)
+    run.step(side)
+    _ok()
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        assert torch.equal(getattr(run, n), getattr(want, n)), n
