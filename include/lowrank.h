@@ -319,7 +319,8 @@ lr_status lr_qk_bwd(lr_dtype dt, int T, const lr_qk_shape* sh, float eps, const 
  * up to 128, H*dh <= 2^24, T*Hq <= 2^30, nseq <= 2^24; scale positive, at most 2.35e38;
  * scale log2(e) q_t.k_j has to stay within fp32's range.
  * Products are of bf16 operands summed in fp32; P and dS are rounded to bf16 for theirs, the
- * softmax statistics, O, dQ, dK and dV are fp32 until they are rounded once.
+ * softmax statistics, O, dQ, dK and dV are fp32 until they are rounded once.  The backward's P
+ * takes over the roundings of lse, up to |lse| 2^-22 of itself (2^-9 where scores reach 8192).
  * Offsets live on the device and are read there: if they are not in order or leave the
  * rows, the call writes no result and lr_check_device_error reports LR_ERR_SHAPE.
  * The workspace holds the list of work items, D and, in the backward of few and long

@@ -48,10 +48,10 @@ __global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs a, const in
   store8(a.dv.p + t * a.dv.ld + 1LL * h * a.dh + c, v);
 }
 
-// Parts of an item of dK and dV: not more items than 152 SMs, no part of less than four row tiles of a sequence twice as
-// long as the average, and eight at most: a part costs some 5 us besides its tiles.  Whole backward: one sequence of 1024
-// tokens, 32 over 8 heads, 53.5 us uncut and 47.7 in parts; of 2048, 8 over 1, 168 and 43; eight of 128, 32 over 8, 24
-// uncut and 36 in four.
+// Parts of an item of dK and dV: not more items than 152 SMs (a GB300's; the size query, which asks too, needs no device), no
+// part of less than four row tiles of a sequence twice as long as the average, and eight at most: a part costs some 5 us
+// besides its tiles.  Whole backward: one sequence of 1024 tokens, 32 over 8 heads, 53.5 us uncut and 47.7 in parts; of
+// 2048, 8 over 1, 168 and 43; eight of 128, 32 over 8, 24 uncut and 36 in four.
 int dkv_parts(int T, int nseq, int Hq, int Hk) {
   const long long items = plan_capacity(T, nseq, kRows) * Hk;
   const long long tiles = 2LL * T / nseq / (kRows / (Hq / Hk));

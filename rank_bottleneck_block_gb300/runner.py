@@ -714,7 +714,8 @@ class TokenLogProbs(_Assigned):
     entropy and writes dlogits.
 
     The tensors are attributes, and may be replaced as those of PackedAttention; dlogits may be logits itself (a
-    backward in place).
+    backward in place).  On the GPU each begins at a 16-byte boundary, also when it is given to the constructor:
+    targets that are tokens from the second on are cloned (tokens[1:].clone()); rows of logits may begin anywhere.
     """
 
     _FORWARD = ("logits", "target", "logp", "entropy", "lse", "top_ids", "top_logp", "ws")
