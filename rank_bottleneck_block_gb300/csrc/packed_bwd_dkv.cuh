@@ -13,9 +13,10 @@
 // (one sequence of 1024 tokens, 32 over 8 heads: 64 items, of which the first had 32 tiles).
 //
 // The heads of a group add up in the same accumulators, in a fixed order.  TMEM is full (S^T, dP^T, dV and dK, 128
-// columns each; up to 64 channels dV and dK leave half of theirs unused), so S^T and dP^T have one buffer; what keeps the tensor cores at work is that they belong to two chains:
-// one issuer takes dV of tile i and then S^T of tile i + 1, the other dK of tile i and then dP^T of tile i + 1, by
-// turns, and the element-wise warps compute P while the second has its turn and dS while the first has.
+// columns each; up to 64 channels dV and dK leave half of theirs unused), so S^T and dP^T have one buffer; what keeps the
+// tensor cores at work is that they belong to two chains: one issuer takes dV of tile i and then S^T of tile i + 1, the
+// other dK of tile i and then dP^T of tile i + 1, by turns, and the element-wise warps compute P while the second has its
+// turn and dS while the first has.
 //
 // Rows past the end of the sequence get P = dS = 0 by selection, and rows of dO and Q there are zeroed in shared memory
 // before their products.  Rows of a tile that no token has (128 is no multiple of G) stay zero from the start.

@@ -118,3 +118,31 @@ def test_a_batch_with_some_rows_far_from_zero(dtype):
     torch.cuda.synchronize()
     rows = [0, 1, 2, 3, 299, 300, 301, 650, 1299]
     _check_gradient(shape, case, run.dlogits[rows], rows)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("extra", [(3, 0), (0, 5), (1, 1), (8, 16), (1001, 2)])
+def test_far_rows_that_lie_apart_and_in_a_graph(extra, dtype):
+    """Rows of logits and of the gradient on any alignment, the two different; nothing beside them changes."""
+    from rank_bottleneck_block_gb300.runner import GraphStep, TokenLogProbs
+
+    T, V = 7, 20003
+    shape = I.LogProbShape(T=T, V=V, dtype=dtype)
+    case = I.make_logprob_case(shape, seed=3, device="cuda")
+    case["logits"][::2] += 5e3
+    case["logits"][3] = LOW[dtype]
+    td = case["logits"].dtype
+    m = torch.full((T, V + extra[0]), LOW[dtype] * -1, dtype=td, device="cuda")  # larger than any logit, if it were read
+    m[:, :V] = case["logits"]
+    d = torch.full((T, V + extra[1]), 7.0, dtype=td, device="cuda")
+    run = TokenLogProbs(shape, case)
+    run.logits, run.dlogits = m[:, :V], d[:, :V]
+    run.step()
+    torch.cuda.synchronize()
+    _check_gradient(shape, case, run.dlogits)
+    keep = d.clone()
+    graph = GraphStep(run.step)
+    d[:, :V] = 0
+    graph()
+    torch.cuda.synchronize()
+    assert torch.equal(d, keep) and (d[:, V:] == 7).all() and (m[:, V:] == LOW[dtype] * -1).all()
