@@ -362,11 +362,11 @@ lr_status lr_packed_attn_bwd(lr_dtype dt, const lr_packed_shape* sh, float scale
  *     dlogits_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + entropy)).
  * dlogp: fp32 [T]; dentropy: fp32 [T] or NULL (entropy is then unused and may be NULL);
  * lse, entropy: the forward's.  dlogits may be logits (the same pointer and row distance).
- * log p_j is taken as z_j - lse while the rounding of lse moves p by 2^-14 of itself at most
- * (bf16: |lse| up to 1024) or 2^-18 (fp32: up to 64).  Where |lse| is larger or not finite the
- * row is read once more for its maximum and sum, and log p_j comes from differences to the
- * maximum, as logp and entropy do in the forward: no offset that a row's logits share changes
- * their gradient.
+ * log p_j is taken as z_j - lse while the rounding of lse moves it (and so p, relative to
+ * itself) by 2^-14 at most (bf16: |lse| up to 1024) or 2^-18 (fp32: up to 64).  Where |lse| is
+ * larger or not finite the row is read once more for its maximum and sum, and log p_j comes from
+ * differences to the maximum, as logp and entropy do in the forward: an offset that a row's
+ * logits share costs their gradient no more than that.
  * Rows without a gradient (no target or dlogp 0, and dentropy 0) are set to 0 unread.
  * scale positive, at most 2.35e38; V <= 2^19, T <= 2^24; every pointer 16-byte aligned (rows need not be).
  * Sums are fp32; the gradient is rounded once.
